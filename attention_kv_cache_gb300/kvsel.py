@@ -23,6 +23,11 @@ SCORE_SOFTMAX, SCORE_LOGITS = 0, 1
 LAYERS_EACH, LAYERS_L1_MEAN, LAYERS_MAX = 0, 1, 2
 HEADS_EACH, HEADS_SUM = 0, 1
 MAX_BATCH, MAX_WINDOW, MAX_ROWS, MAX_PAGE, WS_ALIGN = 128, 64, 256, 256, 256
+DTYPE_BF16, DTYPE_F16, DTYPE_E4M3 = 0, 1, 2
+ORDER_HEAD, ORDER_ROW = 0, 1            # order inside a page: heads outside rows, rows outside heads
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDED, ROPE_RAMP = 0, 1, 2, 3
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+PAGED_MAX_BATCH = 4096
 
 
 class KvselError(RuntimeError):
@@ -61,6 +66,30 @@ class ClaaShape(ctypes.Structure):
                 ("n_sel", ctypes.c_int32), ("ws_bytes", ctypes.c_size_t)]
 
 
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("original_len", ctypes.c_int64)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("factor", ctypes.c_float),
+                ("norm_eps", ctypes.c_float), ("weight_bias", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64)]
+
+
+class PagedAttendDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32)]
+
+
 class TraceEntry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int64), ("ms", ctypes.c_double)]
 
@@ -88,6 +117,15 @@ def _load():
         "kvsel_claa_select": (I32, [D, P(ClaaParams), VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
         "kvsel_attend_workspace_size": (I32, [D, I32, I32, I32, P(SZ)]),
         "kvsel_attend": (I32, [D, VP, I32, VP, VP, VP, VP, I32, I32, I32, VP, VP, SZ, VP]),
+        "kvsel_page_assign_workspace_size": (I32, [I32, P(SZ)]),
+        "kvsel_page_assign": (I32, [I32, I64, I32, I32, VP, VP, VP, VP, I64, VP, VP, VP, VP, VP, I64, VP, VP, VP, VP,
+                                    SZ, VP]),
+        "kvsel_rope_freqs": (I32, [I32, P(RopeScaling), P(ctypes.c_double), P(ctypes.c_float)]),
+        "kvsel_rope_append": (I32, [P(CacheDesc), P(RopeDesc), I64, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP,
+                                    VP, VP]),
+        "kvsel_paged_attend_workspace_size": (I32, [P(CacheDesc), P(PagedAttendDesc), P(SZ)]),
+        "kvsel_paged_attend": (I32, [P(CacheDesc), P(PagedAttendDesc), VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ,
+                                     VP]),
         "kvsel_read_device_error": (I32, [VP, VP]),
         "kvsel_noalloc_read_device_error": (I32, [VP]),
         "kvsel_selftest_bounded_wait": (I32, [VP, ctypes.c_uint32, I32, VP]),
@@ -108,7 +146,10 @@ _lib = _load()
 EXPORTED = ("kvsel_workspace_size", "kvsel_score", "kvsel_score_noalloc", "kvsel_prefill_attention",
             "kvsel_score_from_lse", "kvsel_combine_layers",
             "kvsel_aggregate", "kvsel_select", "kvsel_topk", "kvsel_compact", "kvsel_compact_layers",
-            "kvsel_pagetable", "kvsel_claa_shape", "kvsel_claa_select", "kvsel_attend_workspace_size", "kvsel_attend", "kvsel_read_device_error", "kvsel_noalloc_read_device_error", "kvsel_selftest_bounded_wait", "kvsel_status_string",
+            "kvsel_pagetable", "kvsel_claa_shape", "kvsel_claa_select", "kvsel_attend_workspace_size", "kvsel_attend",
+            "kvsel_page_assign_workspace_size", "kvsel_page_assign", "kvsel_rope_freqs", "kvsel_rope_append",
+            "kvsel_paged_attend_workspace_size", "kvsel_paged_attend", "kvsel_read_device_error",
+            "kvsel_noalloc_read_device_error", "kvsel_selftest_bounded_wait", "kvsel_status_string",
             "kvsel_version", "kvsel_trace_enable", "kvsel_trace_read", "kvsel_launch_count")
 
 
@@ -271,6 +312,85 @@ def kvsel_attend(desc, q, n_q: int, k, v, kv_indptr, kv_indices, n_per_row: int,
     nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
     _check(_lib.kvsel_attend(ctypes.byref(desc), _ptr(q), n_q, _ptr(k), _ptr(v), _ptr(kv_indptr), _ptr(kv_indices),
                              n_per_row, block, max_blocks, _ptr(o), _ptr(ws), nb, _stream(stream)), "kvsel_attend")
+
+
+def make_cache_desc(*, h_q: int, h_kv: int, head_dim: int, page_size: int, n_pages: int, dtype: int = DTYPE_BF16,
+                    cache_dtype: Optional[int] = None, order: int = ORDER_HEAD,
+                    strides: Optional[Sequence[int]] = None) -> CacheDesc:
+    """A pool of pages: contiguous [n_pages][h_kv][P][d] (``ORDER_HEAD``) or [n_pages][P][h_kv][d] (``ORDER_ROW``),
+    or any ``strides`` (page, head, row) in elements."""
+    if strides is None:
+        page = h_kv * page_size * head_dim
+        strides = (page, page_size * head_dim, head_dim) if order == ORDER_HEAD else (page, head_dim, h_kv * head_dim)
+    return CacheDesc(h_q, h_kv, head_dim, page_size, n_pages, dtype, dtype if cache_dtype is None else cache_dtype,
+                     *strides)
+
+
+def make_rope_desc(*, rot_dim: int, layout: int = ROPE_HALF, factor: float = 1.0, norm_eps: float = 1e-6,
+                   weight_bias: float = 0.0, q=None, k=None, v=None) -> RopeDesc:
+    """Rotation and norm of a step's rows; ``q``, ``k`` and ``v`` are tensors [tokens, heads, d] of the strides the
+    calls will have (their last dimension contiguous)."""
+    strides = []
+    for t in (q, k, v):
+        if t is not None and t.stride(2) != 1:
+            raise ValueError("the elements of a head row must be contiguous")
+        strides += (0, 0) if t is None else (t.stride(0), t.stride(1))
+    return RopeDesc(rot_dim, layout, factor, norm_eps, weight_bias, *strides)
+
+
+def make_paged_attend_desc(*, batch: int, max_blocks: int, q_stride: int = 0, scale: float = 0.0, softcap: float = 0.0,
+                           window: int = 0) -> PagedAttendDesc:
+    return PagedAttendDesc(batch, max_blocks, q_stride, scale, softcap, window)
+
+
+def kvsel_page_assign_workspace_size(batch: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kvsel_page_assign_workspace_size(batch, ctypes.byref(n)), "kvsel_page_assign_workspace_size")
+    return n.value
+
+
+def kvsel_page_assign(page_size: int, n_pages: int, lens, n_new, free_pages, free_head, block_tables, lens_out,
+                      free_head_out, indptr, slots, positions, seq_ids, ws, ws_bytes=None, pos_offset=None, stream=None):
+    """batch, max_blocks, the queue's size and max_tokens are those of lens, block_tables, free_pages and slots."""
+    nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.kvsel_page_assign(page_size, n_pages, lens.numel(), block_tables.shape[1], _ptr(lens), _ptr(n_new),
+                                  _ptr(pos_offset), _ptr(free_pages), free_pages.numel(), _ptr(free_head),
+                                  _ptr(block_tables), _ptr(lens_out), _ptr(free_head_out), _ptr(indptr), slots.numel(),
+                                  _ptr(slots), _ptr(positions), _ptr(seq_ids), _ptr(ws), nb, _stream(stream)),
+           "kvsel_page_assign")
+
+
+def kvsel_rope_freqs(rot_dim: int, scaling: RopeScaling):
+    """(inv_freq, factor): radians per position of each pair (a list of rot_dim / 2 floats) and the factor on cos
+    and sin."""
+    f, scale = (ctypes.c_double * max(1, rot_dim // 2))(), ctypes.c_float(0)
+    _check(_lib.kvsel_rope_freqs(rot_dim, ctypes.byref(scaling), f, ctypes.byref(scale)), "kvsel_rope_freqs")
+    return list(f), scale.value
+
+
+def kvsel_rope_append(cache: CacheDesc, rope: RopeDesc, q, k, v, positions, slots, q_weight, k_weight, inv_freq, q_out,
+                      k_cache, v_cache, k_scale=None, v_scale=None, ws=None, stream=None):
+    """The number of tokens is the first dimension of q (or of k without q)."""
+    n = (k if q is None else q).shape[0]
+    _check(_lib.kvsel_rope_append(ctypes.byref(cache), ctypes.byref(rope), n, _ptr(q), _ptr(k), _ptr(v),
+                                  _ptr(positions), _ptr(slots), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                                  _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(ws),
+                                  _stream(stream)), "kvsel_rope_append")
+
+
+def kvsel_paged_attend_workspace_size(cache: CacheDesc, desc: PagedAttendDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kvsel_paged_attend_workspace_size(ctypes.byref(cache), ctypes.byref(desc), ctypes.byref(n)),
+           "kvsel_paged_attend_workspace_size")
+    return n.value
+
+
+def kvsel_paged_attend(cache: CacheDesc, desc: PagedAttendDesc, q, k_cache, v_cache, block_tables, lens, slopes, k_scale,
+                       v_scale, o, lse, ws, ws_bytes=None, stream=None):
+    nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.kvsel_paged_attend(ctypes.byref(cache), ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(block_tables), _ptr(lens), _ptr(slopes), _ptr(k_scale), _ptr(v_scale),
+                                   _ptr(o), _ptr(lse), _ptr(ws), nb, _stream(stream)), "kvsel_paged_attend")
 
 
 def kvsel_read_device_error(ws, stream=None) -> int:

@@ -418,6 +418,198 @@ KVSEL_API kvsel_status kvsel_pagetable(const kvsel_desc* desc, const uint8_t* ma
                              void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Decoding on over a paged cache.
+ *
+ * The calls above score, select and compact a prompt's cache, which is packed and of fixed size.  The
+ * calls below carry the decode that follows: a pool of pages holds the rows of many requests, each
+ * request lists its pages in a block table, and a step of one or more new rows per request runs
+ *   kvsel_page_assign   pages, slots and positions of the step's new rows (once for all layers),
+ *   kvsel_rope_append   norm, rotation and the write of the new K / V rows (per layer),
+ *   kvsel_paged_attend  attention of one new query row per head over the request's rows (per layer).
+ * Lengths, tables and slots live in device memory and nothing synchronises, so a step can be captured.
+ * DELTA, 'Key designs' 3 (caches in pages of P tokens); CompactAttention, 'Future directions' (page
+ * metadata built on the kernel side, without a CPU-GPU synchronisation).
+ *
+ * Row t of a request is row t % P of page block_table[t / P]; its slot is page * P + t % P.
+ */
+enum { KVSEL_DTYPE_BF16 = 0, KVSEL_DTYPE_F16 = 1, KVSEL_DTYPE_E4M3 = 2 };
+
+#define KVSEL_PAGED_MAX_BATCH 4096
+
+/* A pool of pages of one layer's K (and one of its V): the row of KV head g at slot s starts at element
+ * (s / P) * page_stride + g * head_stride + (s % P) * row_stride and is contiguous.  Both orders of a page
+ * (heads outside rows, rows outside heads) are strides, and so is a packed [h_kv][rows][d] cache. */
+typedef struct {
+  int32_t h_q;            /* query heads, multiple of h_kv */
+  int32_t h_kv;           /* KV heads >= 1 */
+  int32_t head_dim;       /* d: a multiple of 16, 16 .. 256 (kvsel_paged_attend: 64 or 128) */
+  int32_t page_size;      /* P: rows per page, 1 .. KVSEL_MAX_PAGE */
+  int64_t n_pages;        /* pages of the pool: 1 .. 2^31 - 1 */
+  int32_t dtype;          /* q, k, v, weights and outputs: KVSEL_DTYPE_BF16 or KVSEL_DTYPE_F16 */
+  int32_t cache_dtype;    /* the pool: dtype, or KVSEL_DTYPE_E4M3 (a value times its head's scale) */
+  int64_t page_stride;    /* in elements of the pool; each a multiple of 16 bytes and >= 0 */
+  int64_t head_stride;
+  int64_t row_stride;
+} kvsel_cache_desc;
+
+/*
+ * kvsel_page_assign — pages, slots, positions and block tables of a step's new rows, from lengths.
+ *
+ * Request b holds lens[b] rows (in its first ceil(lens[b] / P) table entries) and gets n_new[b] more.
+ * The pages it lacks are taken from the queue free_pages[free_head ..) in request order and written to
+ * its table behind the ones it has; every other table entry is left as it was.  The step's tokens are
+ * numbered request by request: token indptr[b] + i is row t = lens[b] + i of request b, with
+ *   slots      = table[t / P] * P + t % P
+ *   positions  = t + pos_offset[b]      (a compacted cache holds fewer rows than its text has positions)
+ *   seq_ids    = b
+ * Tokens from indptr[batch] to max_tokens (the padding of a captured step) get slot -1, position 0 and
+ * request -1.  The updated lengths and queue head may be written over the old ones, so that the replays
+ * of a captured step go on from one another.
+ *
+ *   lens, n_new    [device] int64 [batch]
+ *   pos_offset     [device] int64 [batch], or NULL (0)
+ *   free_pages     [device] int32 [n_free] page ids, each in [0, n_pages)
+ *   free_head      [device] int64 [1]: entries of free_pages taken so far
+ *   block_tables   [device] int32 [batch][max_blocks], in and out
+ *   lens_out       [device] int64 [batch] out: lens + n_new; may be lens
+ *   free_head_out  [device] int64 [1] out; may be free_head
+ *   indptr         [device] int64 [batch + 1] out
+ *   slots          [device] int64 [max_tokens] out
+ *   positions      [device] int64 [max_tokens] out (nullable)
+ *   seq_ids        [device] int32 [max_tokens] out (nullable)
+ *   ws             [device] workspace of kvsel_page_assign_workspace_size() bytes
+ *
+ * A step that cannot be carried out (a negative length or count, a request longer than max_blocks * P
+ * rows, more than max_tokens tokens, a queue with too few pages or a head outside it) records
+ * KVSEL_ERR_INVALID_ARG (detail: the request, or batch for the sums) and assigns nothing: slots -1,
+ * positions 0, requests -1, indptr 0, lengths and head unchanged, tables as they were.  A page id outside
+ * [0, n_pages) records KVSEL_ERR_DEVICE and its rows get slot -1.
+ */
+KVSEL_API kvsel_status kvsel_page_assign_workspace_size(int32_t batch, size_t* bytes);
+KVSEL_API kvsel_status kvsel_page_assign(int32_t page_size, int64_t n_pages, int32_t batch, int32_t max_blocks,
+                                         const int64_t* lens, const int64_t* n_new, const int64_t* pos_offset,
+                                         const int32_t* free_pages, int64_t n_free, const int64_t* free_head,
+                                         int32_t* block_tables, int64_t* lens_out, int64_t* free_head_out,
+                                         int64_t* indptr, int64_t max_tokens, int64_t* slots, int64_t* positions,
+                                         int32_t* seq_ids, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * kvsel_rope_freqs — angles per position of rotary pairs, with the long-context scalings.  Host only.
+ *
+ * theta_i = base^(-2 i / rot_dim), i < rot_dim / 2, then
+ *   PLAIN   theta
+ *   LINEAR  theta / factor
+ *   BANDED  by the pair's wavelength w = 2 pi / theta against the original context L0: theta where
+ *           w < L0 / high, theta / factor where w > L0 / low, between them
+ *           (1 - s) theta / factor + s theta with s = (L0 / w - low) / (high - low)
+ *   RAMP    by the pair's index: r theta / factor + (1 - r) theta with r rising linearly from 0 to 1
+ *           between the (whole) indexes whose pairs turn `high` and `low` times over L0; cos and sin are
+ *           scaled by 0.1 ln(factor) + 1
+ *
+ *   inv_freq  [host] double [rot_dim / 2] out: radians per position (kvsel_rope_append reads it from
+ *             device memory)
+ *   scale     [host] float out: the factor on cos and sin (kvsel_rope_desc.factor)
+ */
+enum { KVSEL_ROPE_PLAIN = 0, KVSEL_ROPE_LINEAR = 1, KVSEL_ROPE_BANDED = 2, KVSEL_ROPE_RAMP = 3 };
+typedef struct {
+  int32_t type;           /* KVSEL_ROPE_PLAIN .. KVSEL_ROPE_RAMP */
+  double base;            /* > 1 */
+  double factor;          /* >= 1 (not read by PLAIN) */
+  double low, high;       /* BANDED, RAMP: 0 < low < high */
+  int64_t original_len;   /* BANDED, RAMP: L0 >= 1 */
+} kvsel_rope_scaling;
+KVSEL_API kvsel_status kvsel_rope_freqs(int32_t rot_dim, const kvsel_rope_scaling* scaling, double* inv_freq,
+                                        float* scale);
+
+/*
+ * kvsel_rope_append — norm and rotation of the new queries and keys, and the new K / V rows into the pool.
+ *
+ * For every token i with slots[i] >= 0 and every head of q and k:
+ *   y = x / sqrt(mean(x^2) + norm_eps) * (weight + weight_bias)     (with a weight; else y = x)
+ *   the pairs of the first rot_dim elements of y turn by positions[i] * inv_freq[pair]:
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin); HALF pairs element j with j + rot_dim / 2,
+ *   INTERLEAVED 2 j with 2 j + 1; the other elements pass.
+ * q goes to q_out, k and v (v as it is) to the rows of `slots` in the pools; in an e4m3 pool value x is held
+ * as x / scale of its head, rounded to nearest and clamped to +-448.  Tokens with slot -1 are padding:
+ * nothing of theirs is written.  All arithmetic is fp32 with one rounding at the end; angles are formed
+ * to 2^-32 of a turn at any position below 2^31.
+ *
+ *   q          [device] dtype, element (i, h, c) at i * q_stride + h * q_head_stride + c; NULL with q_out:
+ *              keys and values only (rows of a compacted cache: rot_dim 0, no weights)
+ *   k, v       [device] dtype, likewise; NULL together with the pools: queries only
+ *   positions  [device] int64 [n_tokens]; inv_freq [device] double [rot_dim / 2]; both NULL with rot_dim 0
+ *   slots      [device] int64 [n_tokens]; may be NULL when k and v are (no token is padding)
+ *   q_weight, k_weight  [device] dtype [d], or NULL: no norm
+ *   q_out      [device] dtype [n_tokens][h_q][d]; may be q when q is laid out the same
+ *   k_cache, v_cache  [device] pools; the slots of a call are distinct (a slot named twice holds one of the
+ *              rows, or parts of both)
+ *   k_scale, v_scale  [device] fp32 [h_kv], both given exactly when the pool is e4m3
+ *   ws         [device] workspace or NULL (the error word): a slot outside [-1, n_pages * P) is not written
+ *              and, with ws, KVSEL_ERR_DEVICE is recorded (detail: the token)
+ */
+enum { KVSEL_ROPE_HALF = 0, KVSEL_ROPE_INTERLEAVED = 1 };
+typedef struct {
+  int32_t rot_dim;        /* 0 (no rotation) .. d, a multiple of 16 */
+  int32_t layout;         /* KVSEL_ROPE_HALF or KVSEL_ROPE_INTERLEAVED */
+  float factor;           /* on cos and sin */
+  float norm_eps;         /* >= 0 */
+  float weight_bias;      /* added to the norm weights (0, or 1 for weights stored as w - 1) */
+  int64_t q_stride, q_head_stride;   /* elements, each a multiple of 8 (16 bytes) */
+  int64_t k_stride, k_head_stride;
+  int64_t v_stride, v_head_stride;
+} kvsel_rope_desc;
+KVSEL_API kvsel_status kvsel_rope_append(const kvsel_cache_desc* cache, const kvsel_rope_desc* rope, int64_t n_tokens,
+                                         const void* q, const void* k, const void* v, const int64_t* positions,
+                                         const int64_t* slots, const void* q_weight, const void* k_weight,
+                                         const double* inv_freq, void* q_out, void* k_cache, void* v_cache,
+                                         const float* k_scale, const float* v_scale, void* ws, cudaStream_t stream);
+
+/*
+ * kvsel_paged_attend — attention of one new query row per head over a request's rows in the pool.
+ *
+ * Request b with n = lens[b] rows (its newest row, the query's own, among them) sees rows
+ * t in [max(0, n - window), n), or all n without a window:
+ *   z_t = scale <q, k_t>;  with softcap c: z_t = c tanh(z_t / c);  with slopes: z_t += slope_h (t - (n - 1))
+ *   o = sum_t softmax(z)_t v_t,  lse = log sum_t exp(z_t)
+ * Query head h reads KV head h / (h_q / h_kv).  A request with no row gives o = 0 and lse = -inf.  Rows
+ * that a request does not see take no part whatever the pool holds there (infinities and NaN too).
+ *
+ *   q             [device] dtype, element (b, h, c) at b * q_stride + h * d + c
+ *   k_cache, v_cache  [device] pools
+ *   block_tables  [device] int32 [batch][max_blocks]; entries behind a request's last page are not read
+ *   lens          [device] int64 [batch]
+ *   slopes        [device] fp32 [h_q], or NULL
+ *   k_scale, v_scale  [device] fp32 [h_kv], both given exactly when the pool is e4m3
+ *   o             [device] dtype [batch][h_q][d] out
+ *   lse           [device] fp32 [batch][h_q] out, or NULL
+ *   ws            [device] workspace of kvsel_paged_attend_workspace_size() bytes (the splits' partials);
+ *                 the size depends on the current device: query it where the call runs
+ *
+ * A length outside [0, max_blocks * P] records KVSEL_ERR_INVALID_ARG (detail: the request), which then
+ * counts as empty; a page id outside [0, n_pages) records KVSEL_ERR_DEVICE (detail: the request) and its
+ * rows are left out.
+ *
+ * Arithmetic: products of the 16-bit values (e4m3 values as fp16, exactly) accumulated in fp32 on the
+ * tensor cores, softmax statistics in fp32, P taken as a high and a low 16-bit part.  With an e4m3 pool
+ * the query row is held in fp16 scaled by a power of two of its own (2^-24 of the row's largest value).
+ */
+typedef struct {
+  int32_t batch;          /* requests: 1 .. KVSEL_PAGED_MAX_BATCH */
+  int32_t max_blocks;     /* columns of the block tables >= 1, (max_blocks + 1) * P < 2^31 */
+  int64_t q_stride;       /* elements between requests' queries, a multiple of 8; 0: h_q * d */
+  float scale;            /* on the scores; 0: 1 / sqrt(d) */
+  float softcap;          /* c > 0, or 0: none */
+  int32_t window;         /* rows seen, >= 1, or 0: all */
+} kvsel_paged_attend_desc;
+KVSEL_API kvsel_status kvsel_paged_attend_workspace_size(const kvsel_cache_desc* cache,
+                                                         const kvsel_paged_attend_desc* desc, size_t* bytes);
+KVSEL_API kvsel_status kvsel_paged_attend(const kvsel_cache_desc* cache, const kvsel_paged_attend_desc* desc,
+                                          const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, const int64_t* lens, const float* slopes,
+                                          const float* k_scale, const float* v_scale, void* o, float* lse, void* ws,
+                                          size_t ws_bytes, cudaStream_t stream);
+
+/*
  * kvsel_score_noalloc — kvsel_score for callers that cannot allocate device memory.
  *
  * The pages have no counterpart to this call; it exists for callers with no
