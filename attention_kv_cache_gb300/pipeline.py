@@ -3,7 +3,8 @@
 score -> [aggregate over layers / heads] -> top-k -> compact, and the block-union
 page table when the workload has a block mask; the CLAA schedule (per-layer
 selections plus a prune index from the token-wise max over a layer buffer) for
-workloads that carry one.  Every step runs in libkvsel's kernels; this module
+workloads that carry one; the decode that goes on from the kept rows over a pool
+of pages (PagedDecoder).  Every step runs in libkvsel's kernels; this module
 only allocates device memory and orders the calls on one stream.
 """
 
@@ -199,3 +200,97 @@ class ClaaPipeline:
         """q [1, n_layers, h_q, W, d]; k, v the prompt's caches (flat, layout of the library)."""
         K.kvsel_claa_select(self.desc, self.params, q, k, v, self.scores, self.layer_scores, self.prune_scores,
                             self.idx, self.prune_idx, self.k_out, self.v_out, self.ws, self.ws_bytes, stream)
+
+
+_KIND = {torch.bfloat16: K.DTYPE_BF16, torch.float16: K.DTYPE_F16, torch.float8_e4m3fn: K.DTYPE_E4M3}
+
+
+class PagedDecoder:
+    """Decoding on from compacted caches: a pool of pages per layer, block tables, and one step's calls.
+
+    ``admit`` puts the kept rows of a batch's compacted caches into pages.  Each step then calls ``begin``
+    once (pages, slots and positions of one new row per request) and ``layer`` for every layer (norm,
+    rotation and write of the new rows, attention over the request's rows).  A step's calls update the
+    lengths in place and synchronise nothing, so a step can be captured and replayed.
+
+    ``rope`` is a kvsel.RopeScaling over ``rot_dim`` elements (None: rows arrive rotated); ``norms`` is
+    (q_weight, k_weight) per layer, or None; ``scales`` is (k_scale, v_scale) [n_layers, h_kv] of an
+    8-bit pool (``cache_dtype`` torch.float8_e4m3fn).
+    """
+
+    def __init__(self, *, n_layers: int, h_q: int, h_kv: int, head_dim: int, batch: int, max_rows: int,
+                 n_pages: int, page_size: int = 16, dtype=torch.bfloat16, cache_dtype=None, rope=None,
+                 rot_dim: Optional[int] = None, rope_layout: int = K.ROPE_HALF, norms=None, norm_eps: float = 1e-6,
+                 scales=None, softcap: float = 0.0, window: int = 0, slopes=None, device="cuda"):
+        cache_dtype = dtype if cache_dtype is None else cache_dtype
+        P = page_size
+        self.n_layers, self.batch, self.n_pages, self.P = n_layers, batch, n_pages, P
+        self.h_q, self.h_kv, self.d, self.device = h_q, h_kv, head_dim, device
+        self.norms, self.scales, self.slopes, self.norm_eps, self.rope_layout = norms, scales, slopes, norm_eps, rope_layout
+        self.cache = K.make_cache_desc(h_q=h_q, h_kv=h_kv, head_dim=head_dim, page_size=P, n_pages=n_pages,
+                                       dtype=_KIND[dtype], cache_dtype=_KIND[cache_dtype])
+        self.rot_dim, self.factor, self.inv_freq = 0, 1.0, None
+        if rope is not None:
+            self.rot_dim = head_dim if rot_dim is None else rot_dim
+            freqs, self.factor = K.kvsel_rope_freqs(self.rot_dim, rope)
+            self.inv_freq = torch.tensor(freqs, dtype=torch.float64, device=device)
+        max_blocks = -(-max_rows // P)
+        self.attend = K.make_paged_attend_desc(batch=batch, max_blocks=max_blocks, softcap=softcap, window=window)
+        i64 = dict(dtype=torch.int64, device=device)
+        shape = (n_layers, n_pages, h_kv, P, head_dim)
+        self.k_cache, self.v_cache = torch.empty(shape, dtype=cache_dtype, device=device), torch.empty(
+            shape, dtype=cache_dtype, device=device)
+        self.tables = torch.zeros((batch, max_blocks), dtype=torch.int32, device=device)
+        self.free_pages = torch.arange(n_pages, dtype=torch.int32, device=device)
+        self.free_head, self.lens = torch.zeros(1, **i64), torch.zeros(batch, **i64)
+        self.pos_offset, self.n_new = torch.zeros(batch, **i64), torch.ones(batch, **i64)
+        self.indptr = torch.empty(batch + 1, **i64)
+        self.slots, self.positions = torch.empty(batch, **i64), torch.empty(batch, **i64)
+        self.q_out = torch.empty((batch, h_q, head_dim), dtype=dtype, device=device)
+        self.o = torch.empty_like(self.q_out)
+        n = max(K.kvsel_page_assign_workspace_size(batch), K.kvsel_paged_attend_workspace_size(self.cache, self.attend))
+        ws = torch.zeros(n + K.WS_ALIGN, dtype=torch.uint8, device=device)
+        off = (-ws.data_ptr()) % K.WS_ALIGN
+        self.ws = ws[off:off + n]
+
+    def _assign(self, n_new, slots, positions, stream):
+        K.kvsel_page_assign(self.P, self.n_pages, self.lens, n_new, self.free_pages, self.free_head, self.tables,
+                            self.lens, self.free_head, self.indptr, slots, positions, None, self.ws,
+                            pos_offset=self.pos_offset, stream=stream)
+
+    def _scale(self, layer):
+        return (None, None) if self.scales is None else (self.scales[0][layer], self.scales[1][layer])
+
+    def admit(self, k_out, v_out, text_lens, rows: Optional[int] = None, stream=None):
+        """The first ``rows`` rows (all by default) of compacted caches [batch, n_layers, h_kv, rows, d] into pages;
+        ``text_lens`` [batch] positions each request's text has, so that its next row gets the next position."""
+        rows = k_out.shape[3] if rows is None else rows
+        n = self.batch * rows
+        self.pos_offset.copy_(torch.as_tensor(text_lens, dtype=torch.int64) - rows)
+        slots = torch.empty(n, dtype=torch.int64, device=self.device)
+        self._assign(torch.full_like(self.lens, rows), slots, None, stream)
+        for layer in range(self.n_layers):
+            ks, vs = self._scale(layer)
+            for b in range(self.batch):
+                k, v = (x[b, layer, :, :rows].transpose(0, 1) for x in (k_out, v_out))     # [rows, h_kv, d]
+                desc = K.make_rope_desc(rot_dim=0, k=k, v=v)
+                K.kvsel_rope_append(self.cache, desc, None, k, v, None, slots[b * rows:(b + 1) * rows], None, None, None,
+                                    None, self.k_cache[layer], self.v_cache[layer], ks, vs, self.ws, stream=stream)
+
+    def begin(self, stream=None):
+        """Pages, slots and positions of one new row per request."""
+        self._assign(self.n_new, self.slots, self.positions, stream)
+
+    def layer(self, layer: int, q, k, v, stream=None):
+        """q [batch, h_q, d], k and v [batch, h_kv, d] (any row strides) of the step's rows; returns o [batch, h_q, d],
+        which the next call overwrites."""
+        ks, vs = self._scale(layer)
+        desc = K.make_rope_desc(rot_dim=self.rot_dim, layout=self.rope_layout, factor=self.factor,
+                                norm_eps=self.norm_eps, q=q, k=k, v=v)
+        qw, kw = (None, None) if self.norms is None else self.norms[layer]
+        K.kvsel_rope_append(self.cache, desc, q, k, v, self.positions if self.rot_dim else None, self.slots, qw, kw,
+                            self.inv_freq, self.q_out, self.k_cache[layer], self.v_cache[layer], ks, vs, self.ws,
+                            stream=stream)
+        K.kvsel_paged_attend(self.cache, self.attend, self.q_out, self.k_cache[layer], self.v_cache[layer], self.tables,
+                             self.lens, self.slopes, ks, vs, self.o, None, self.ws, stream=stream)
+        return self.o
