@@ -7,6 +7,10 @@ namespace kvsel {
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// CTAs of a kernel resident at once on the current device (0: it cannot be queried), asked once per device,
+// kernel and shared-memory size (paged_api.cu).
+int64_t resident_ctas(const void* kern, int threads, size_t smem);
+
 // ---- page_assign.cu ----------------------------------------------------------------------
 struct AssignArgs {
   int32_t P, batch, max_blocks;
@@ -30,6 +34,8 @@ kvsel_status launch_page_assign(const AssignArgs& a, cudaStream_t s);
 // ---- rope_append.cu ----------------------------------------------------------------------
 struct RopeArgs {
   int32_t h_q, h_kv, d, P, rot, e4m3;
+  int32_t unit_rows;    // head rows of a unit (set by the launcher)
+  int64_t share, extra; // units of every warp, and warps with one more (set by the launcher)
   int64_t n, n_slots, page_stride, head_stride, row_stride;
   int64_t q_stride, q_head, k_stride, k_head, v_stride, v_head;
   float factor, eps, bias;

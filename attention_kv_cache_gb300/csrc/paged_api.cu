@@ -1,6 +1,8 @@
 // C ABI of the calls over a paged cache: argument checks and the kernels' arguments.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <vector>
 
 #include "paged.cuh"
 
@@ -65,6 +67,33 @@ kvsel_status check_attend(const kvsel_cache_desc* cache, const kvsel_paged_atten
 }
 
 }  // namespace
+
+int64_t resident_ctas(const void* kern, int threads, size_t smem) {
+  struct Entry {
+    int dev, threads;
+    const void* kern;
+    size_t smem;
+    int64_t n;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> known;
+  int dev = 0, sms = 0, per_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  for (const Entry& e : known)
+    if (e.dev == dev && e.kern == kern && e.threads == threads && e.smem == smem) return e.n;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || set_smem(kern, smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  known.push_back({dev, threads, kern, smem, (int64_t)sms * per_sm});
+  return known.back().n;
+}
+
 }  // namespace kvsel
 
 using namespace kvsel;

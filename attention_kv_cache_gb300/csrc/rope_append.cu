@@ -7,20 +7,38 @@
 // position, modulo 2^64, is the fraction of a turn exactly up to position * 2^-65, so a far position loses
 // nothing that a 32-bit product of position and frequency would lose; the top 32 bits go to sincospif.
 //
-// One pass over the data: a head row is d / 16 lanes of 16 elements, chosen so that both elements of a
-// pair lie in one lane (elements 8 j .. 8 j + 7 and rot / 2 + 8 j .. of a half layout, 16 j .. 16 j + 15 of
-// an interleaved one), so a row is read once, summed by shuffles, turned in registers and written once.
-// A warp takes the head rows of one token, 32 / (lanes of a row) at a time, and forms its lanes' 8 angles
-// once for all of them; with few tokens the rows of a token are dealt over several warps.
+// One pass over the data, by single warps: a unit is up to kStageBytes of a token's query, key or value rows.  Every
+// warp has an equal share of all units; its units come by bulk copies into a ring of kStages stages (one copy where the rows are contiguous), are
+// normed and turned where they lie, and go out by bulk copies from there; 16-bit value rows go through untouched.
+// A row is d / 16 lanes of 16 elements, chosen so that both elements of a pair lie in one lane (elements 8 j .. and
+// rot / 2 + 8 j .. of a half layout, 16 j .. of an interleaved one), and the lanes of a row sum its squares by shuffles.
+//
+// Bound: the bytes of the rows, if enough of them are in flight (which is why the stages are shared memory and not
+// registers) and the arithmetic stays below the issue rate:
+//   - weight, cosine and sine are one 2x2 matrix per pair, formed once per token (two pairs per lane) and read by
+//     every row: (a, b) -> r (A a - B b, C b + D a) with A = w_a cos, B = w_b sin, C = w_b cos, D = w_a sin and r
+//     the row's norm;
+//   - two pairs share an instruction (packed fp32);
+//   - frequencies in turns are formed once per CTA (64-bit floating point is slow on this GPU).
+//
+// Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 39 us (202 MB, 5.2 TB/s; the copies
+// without the arithmetic 35 us); 32768 tokens of 64 + 8 + 8 heads into e4m3, 222 us (1276 MB, 5.8 TB/s; copies alone
+// 205 us); one token 4.7 us.  With rows in registers instead (steps of 4 rows, 16 warps per SM): 52 and 288 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace kvsel {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kWarps = 5;             // per CTA
+constexpr int kRopeThreads = 32 * kWarps;
+constexpr int kStages = 3;            // per warp: one loading, one turned, one leaving
+constexpr int kStageBytes = 4096;
 
 template <typename T>
 struct Pair;
@@ -43,14 +61,52 @@ struct Pair<__half> {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 u, float* f) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// two fp32 values in one register pair
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 get(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// A lane's 16 elements as four packed pairs of first elements and four of second ones.
+template <typename T, bool HALF>
+__device__ __forceinline__ void unpack16(const uint4* r, F2* a, F2* b) {
+  const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = Pair<T>::get(w[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
+  for (int m = 0; m < 4; ++m) {
+    const float2 x = Pair<T>::get(w[HALF ? m : 2 * m]), y = Pair<T>::get(w[HALF ? m + 4 : 2 * m + 1]);
+    a[m] = HALF ? f2(x.x, x.y) : f2(x.x, y.x);
+    b[m] = HALF ? f2(y.x, y.y) : f2(x.y, y.y);
+  }
+}
+// the packed pairs back in the order of the elements
+template <bool HALF>
+__device__ __forceinline__ void order16(const F2* a, const F2* b, float* x) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const float2 u = get(a[m]), v = get(b[m]);
+    x[HALF ? 2 * m : 4 * m] = u.x;
+    x[HALF ? 2 * m + 1 : 4 * m + 2] = u.y;
+    x[HALF ? 8 + 2 * m : 4 * m + 1] = v.x;
+    x[HALF ? 9 + 2 * m : 4 * m + 3] = v.y;
   }
 }
 template <typename T>
@@ -66,142 +122,316 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float* f) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// One lane's 16 elements of a head row, normed and turned.
-template <typename T, bool HALF>
-__device__ __forceinline__ void turn(float* x, bool norm, const float* w, bool rotate, const float* cs, const float* sn,
-                                     float inv_d, float eps, int group) {
-  if (norm) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-    for (int o = group >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(fmaf(ss, inv_d, eps));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
-  }
-  if (rotate) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ia = HALF ? i : 2 * i, ib = HALF ? i + 8 : 2 * i + 1;
-      const float a = x[ia], b = x[ib];
-      x[ia] = fmaf(a, cs[i], -(b * sn[i]));
-      x[ib] = fmaf(b, cs[i], a * sn[i]);
-    }
-  }
+// Shared memory, in this order: the warps' stages, the warps' matrices of a token's pairs ([2 kinds][8][chunks] float4:
+// entry 2 m of chunk j holds (A, -B) of its pairs 2 m and 2 m + 1, entry 2 m + 1 holds (C, D)), weights [2][d], turns
+// [rot / 2], the stages' barriers.
+__host__ __device__ inline size_t rope_smem(int d, int rot) {
+  return (size_t)kWarps * (kStages * kStageBytes + 2 * 8 * (d / 16) * 16) + (size_t)2 * d * 4 + (size_t)rot / 2 * 8 +
+         (size_t)kWarps * kStages * 8;
 }
 
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constant__ RopeArgs a, int parts) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  const int64_t i = w / parts;
-  const int part = (int)(w - i * parts);
-  if (i >= a.n) return;
-  const int64_t slot = a.slots != nullptr ? a.slots[i] : 0;
-  if (slot == -1) return;                                       // padding: nothing is written
-  bool cached = a.k != nullptr;
-  if (cached && (slot < 0 || slot >= a.n_slots)) {
-    if (lane == 0 && part == 0) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)i);
-    cached = false;
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+// GROUP: lanes of a head row (the power of two >= d / 16), or 0: found at run time.
+template <typename T, bool HALF, int GROUP>
+__global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int chunks = a.d / 16, pairs = a.rot / 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* stages = smem + (size_t)warp * kStages * kStageBytes;
+  uint8_t* after = smem + (size_t)kWarps * kStages * kStageBytes;
+  float4* mats = reinterpret_cast<float4*>(after) + warp * 2 * 8 * chunks;
+  float* wts = reinterpret_cast<float*>(after + (size_t)kWarps * 2 * 8 * chunks * 16);
+  int64_t* turns = reinterpret_cast<int64_t*>(wts + 2 * a.d);
+  const uint32_t bar0 = sm100::smem_addr(turns + pairs) + warp * kStages * 8;
+  const uint32_t st0 = sm100::smem_addr(stages);
+  int group = GROUP;
+  if (GROUP == 0)
+    for (group = 1; group < chunks;) group <<= 1;
+  const int rows = 32 / group, sub = lane / group, j = lane % group;   // this lane: chunk j of row `sub` of `rows`
+  const bool live = j < chunks, rotate = j < a.rot / 16;
+  const int o0 = HALF && rotate ? 8 * j : 16 * j, o1 = HALF && rotate ? pairs + 8 * j : 16 * j + 8;
+
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) sm100::mbar_init(bar0 + 8 * i, 1);
+    sm100::fence_barrier_init();
   }
-  // this lane's elements: chunk j of a head row, rows `sub` of every `rows` rows taken at a time
-  const int chunks = a.d / 16;
-  int group = 1;
-  while (group < chunks) group <<= 1;
-  const int rows = 32 / group, sub = lane / group, j = lane % group;
-  const bool live = j < chunks;
-  const bool rotate = j < a.rot / 16;
-  const int o0 = HALF && rotate ? 8 * j : 16 * j, o1 = HALF && rotate ? a.rot / 2 + 8 * j : 16 * j + 8;
-  const int iq = a.q != nullptr ? (a.h_q + rows - 1) / rows : 0, ik = cached ? (a.h_kv + rows - 1) / rows : 0;
-  const int total = iq + 2 * ik;
-  const int u0 = (int)((int64_t)total * part / parts), u1 = (int)((int64_t)total * (part + 1) / parts);
-  float cs[8], sn[8];
-  if (rotate && u0 < iq + ik) {
-    const int64_t pos = a.positions[i];
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      // turns per position as a signed multiple of 2^-64 (whole turns drop out), times the position
-      double f = a.inv_freq[8 * j + p] * 0.15915494309189533577;
-      f -= rint(f);
-      const int64_t turns = __double2ll_rn(f * 18446744073709551616.0) * pos;
-      sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &sn[p], &cs[p]);
-      cs[p] *= a.factor;
-      sn[p] *= a.factor;
-    }
-  }
+  __syncwarp();
   const float inv_d = 1.f / (float)a.d;
-  const int64_t page = slot / a.P;
-  const int64_t at = page * a.page_stride + (slot - page * a.P) * a.row_stride;
-  for (int u = u0; u < u1; ++u) {
-    const int kind = u < iq ? 0 : u < iq + ik ? 1 : 2;          // a query, key or value row
-    const int h = (u - (kind == 0 ? 0 : kind == 1 ? iq : iq + ik)) * rows + sub;
-    const bool on = live && h < (kind == 0 ? a.h_q : a.h_kv);
-    const T* src = kind == 0   ? static_cast<const T*>(a.q) + i * a.q_stride + h * a.q_head
-                   : kind == 1 ? static_cast<const T*>(a.k) + i * a.k_stride + h * a.k_head
-                               : static_cast<const T*>(a.v) + i * a.v_stride + h * a.v_head;
-    float x[16];
-    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-    if (on) {
-      r0 = *reinterpret_cast<const uint4*>(src + o0);
-      r1 = *reinterpret_cast<const uint4*>(src + o1);
-    }
-    unpack8<T>(r0, x);
-    unpack8<T>(r1, x + 8);
-    if (kind < 2) {
-      const T* wt = static_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
-      float wf[16];
-      if (wt != nullptr && live) {
-        unpack8<T>(*reinterpret_cast<const uint4*>(wt + o0), wf);
-        unpack8<T>(*reinterpret_cast<const uint4*>(wt + o1), wf + 8);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) wf[e] += a.bias;
-      }
-      turn<T, HALF>(x, wt != nullptr, wf, rotate, cs, sn, inv_d, a.eps, group);
-    }
-    if (!on) continue;
-    if (kind == 0) {
-      T* dst = static_cast<T*>(a.q_out) + (i * a.h_q + h) * a.d;
-      *reinterpret_cast<uint4*>(dst + o0) = pack8<T>(x);
-      *reinterpret_cast<uint4*>(dst + o1) = pack8<T>(x + 8);
+  const int row_bytes = a.d * 2;
+  const int iq = a.q != nullptr ? (a.h_q + a.unit_rows - 1) / a.unit_rows : 0;
+  const int ik = a.k != nullptr ? (a.h_kv + a.unit_rows - 1) / a.unit_rows : 0;
+  const int total = iq + 2 * ik;
+  // kind (query, key, value rows), first row and rows of unit u
+  auto unit = [&](int u, int& kind, int& h0, int& n) {
+    kind = u < iq ? 0 : u < iq + ik ? 1 : 2;
+    h0 = (u - (kind == 0 ? 0 : kind == 1 ? iq : iq + ik)) * a.unit_rows;
+    n = min(a.unit_rows, (kind == 0 ? a.h_q : a.h_kv) - h0);
+  };
+  // this warp's share of all tokens' units, laid end to end: from unit u of token i, `left` of them
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t first = a.share * w + min(w, a.extra);
+  int64_t left = a.share + (w < a.extra ? 1 : 0);
+  int i = (first >> 31) == 0 ? (int)first / total : (int)(first / total);   // (a 32-bit division where it will do)
+  int u = (int)(first - (int64_t)i * total);
+
+  // ---- the units' loads, kStages - 1 ahead
+  int64_t lleft = left;
+  int li = i, lu = u, lst = 0;                                // next unit to load, its stage
+  auto load = [&]() {
+    if (lleft == 0) return;
+    --lleft;
+    int kind, h0, n;
+    unit(lu, kind, h0, n);
+    const int64_t ts = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+    const int64_t hs = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
+    const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + li * ts + h0 * hs;
+    const uint32_t dst = st0 + lst * kStageBytes, bar = bar0 + 8 * lst;
+    if (lane == 0) sm100::mbar_expect_tx(bar, n * row_bytes);
+    if (hs == a.d) {
+      if (lane == 0) bulk_load(dst, src, n * row_bytes, bar);
     } else {
-      const int64_t to = at + h * a.head_stride;
-      void* pool = kind == 1 ? a.k_cache : a.v_cache;
-      if (a.e4m3) {
-        const float s = 1.f / (kind == 1 ? a.k_scale : a.v_scale)[h];
+      __syncwarp();
+      for (int h = lane; h < n; h += 32) bulk_load(dst + h * row_bytes, src + h * hs, row_bytes, bar);
+    }
+    lst = lst == kStages - 1 ? 0 : lst + 1;
+    if (++lu == total) {
+      lu = 0;
+      ++li;
+    }
+  };
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= s;
-        uint8_t* dst = static_cast<uint8_t*>(pool) + to;
-        *reinterpret_cast<uint2*>(dst + o0) = pack8_e4m3(x);
-        *reinterpret_cast<uint2*>(dst + o1) = pack8_e4m3(x + 8);
-      } else {
-        T* dst = static_cast<T*>(pool) + to;
-        *reinterpret_cast<uint4*>(dst + o0) = kind == 1 ? pack8<T>(x) : r0;
-        *reinterpret_cast<uint4*>(dst + o1) = kind == 1 ? pack8<T>(x + 8) : r1;
+  for (int e = 0; e < kStages - 1; ++e) load();
+
+  // ---- what all tokens share, while those land
+  for (int x = threadIdx.x; x < 2 * a.d; x += kRopeThreads) {
+    const T* w = static_cast<const T*>(x < a.d ? a.q_weight : a.k_weight);
+    wts[x] = w != nullptr ? (float)w[x < a.d ? x : x - a.d] + a.bias : 1.f;
+  }
+  // turns per position as signed multiples of 2^-64 (whole turns drop out)
+  for (int x = threadIdx.x; x < pairs; x += kRopeThreads) {
+    double f = a.inv_freq[x] * 0.15915494309189533577;
+    f -= rint(f);
+    turns[x] = __double2ll_rn(f * 18446744073709551616.0);
+  }
+  __syncthreads();
+  // the matrices of the elements that pass: their weights alone
+  for (int x = lane; x < 2 * 8 * (chunks - a.rot / 16); x += 32) {
+    const int kind = x / (8 * (chunks - a.rot / 16)), y = x % (8 * (chunks - a.rot / 16));
+    const int c = a.rot / 16 + y / 8, p = y % 8;
+    float* ab = reinterpret_cast<float*>(mats + (kind * 8 + p / 2 * 2) * chunks + c) + (p & 1);
+    float* cd = reinterpret_cast<float*>(mats + (kind * 8 + p / 2 * 2 + 1) * chunks + c) + (p & 1);
+    ab[0] = wts[kind * a.d + 16 * c + (HALF ? p : 2 * p)];
+    cd[0] = wts[kind * a.d + 16 * c + (HALF ? 8 + p : 2 * p + 1)];
+    ab[2] = cd[2] = 0.f;
+  }
+
+
+  int st = 0, phase = 0;
+  while (left > 0) {
+    const int64_t slot = a.slots != nullptr ? a.slots[i] : 0, pos = pairs > 0 ? a.positions[i] : 0;
+    const bool cached = slot >= 0 && slot < a.n_slots;
+    if (a.k != nullptr && !cached && slot != -1 && lane == 0 && u == 0) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)i);
+    int64_t at = 0;                                             // of the slot in the pool
+    if (cached) {
+      const int64_t page = (slot >> 31) == 0 ? (int)slot / a.P : slot / a.P;
+      at = page * a.page_stride + (slot - page * a.P) * a.row_stride;
+    }
+    if (pairs > 0 && u < iq + ik && slot != -1) {
+      __syncwarp();                                             // the last token's matrices are read
+      for (int c = lane; c < pairs / 2; c += 32) {              // pairs 2 c and 2 c + 1
+        float sn[2], cs[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sincospif((float)(int32_t)((turns[2 * c + e] * pos) >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);
+          sn[e] *= a.factor;
+          cs[e] *= a.factor;
+        }
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          const float* wk = wts + kind * a.d;
+          float2 wa, wb;
+          if (HALF) {
+            wa = *reinterpret_cast<const float2*>(wk + 2 * c);
+            wb = *reinterpret_cast<const float2*>(wk + pairs + 2 * c);
+          } else {
+            const float4 v = *reinterpret_cast<const float4*>(wk + 4 * c);
+            wa = make_float2(v.x, v.z);
+            wb = make_float2(v.y, v.w);
+          }
+          float4* to = mats + (kind * 8 + c % 4 * 2) * chunks + c / 4;
+          to[0] = make_float4(wa.x * cs[0], wa.y * cs[1], -(wb.x * sn[0]), -(wb.y * sn[1]));
+          to[chunks] = make_float4(wb.x * cs[0], wb.y * cs[1], wa.x * sn[0], wa.y * sn[1]);
+        }
+      }
+      __syncwarp();
+    }
+    for (; u < total && left > 0; ++u, --left) {
+      int kind, h0, n;
+      unit(u, kind, h0, n);
+      // the unit two ahead goes into the stage stored last: its bytes have left before it is written again
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+      load();
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(bar0 + 8 * st, phase))) {
+        // the copies in flight land (or their own wait runs out) before the warp leaves
+        if (lane == 0) set_device_error(a.err, KVSEL_ERR_TIMEOUT, 6u);
+        for (int e = 1; e < kStages; ++e) {
+          const int x = (st + e) % kStages;
+          if (x != lst) sm100::mbar_wait(bar0 + 8 * x, phase ^ (x < st ? 1 : 0));
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        return;
+      }
+      const bool e8 = kind > 0 && a.e4m3;
+      uint8_t* stage = stages + st * kStageBytes;
+      const bool skip = slot == -1 || (kind > 0 && !cached);
+      if (!skip && (kind < 2 || e8)) {
+        const bool norm = kind < 2 && (kind == 0 ? a.q_weight : a.k_weight) != nullptr;
+        const float4* mt = mats + kind * 8 * chunks + j;
+        // two rows of every lane at once: their sums and shuffles overlap, and they share the matrices' reads
+        for (int hb = sub; hb - sub < n; hb += 2 * rows) {
+          bool on[2];
+          float scale[2] = {1.f, 1.f};
+          F2 x[2][4], y[2][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int h = hb + t * rows;
+            on[t] = live && h < n;
+            uint4 r[2];
+            r[0] = r[1] = make_uint4(0, 0, 0, 0);
+            if (on[t]) {
+              r[0] = *reinterpret_cast<const uint4*>(stage + h * row_bytes + 2 * o0);
+              r[1] = *reinterpret_cast<const uint4*>(stage + h * row_bytes + 2 * o1);
+              if (e8) scale[t] = 1.f / (kind == 1 ? a.k_scale : a.v_scale)[h0 + h];
+            }
+            unpack16<T, HALF>(r, x[t], y[t]);
+          }
+          if (norm) {
+            float ss[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              F2 s2 = mul(x[t][0], x[t][0]), t2 = mul(y[t][0], y[t][0]);
+#pragma unroll
+              for (int m = 1; m < 4; ++m) {
+                s2 = fma(x[t][m], x[t][m], s2);
+                t2 = fma(y[t][m], y[t][m], t2);
+              }
+              const float2 sf = get(s2), tf = get(t2);
+              ss[t] = (sf.x + sf.y) + (tf.x + tf.y);
+            }
+            if (GROUP > 0) {
+#pragma unroll
+              for (int o = GROUP / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
+            } else {
+              for (int o = group >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) scale[t] *= rsqrtf(fmaf(ss[t], inv_d, a.eps));
+          }
+          if (kind < 2 && live) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float4 ab = mt[2 * m * chunks], cd = mt[(2 * m + 1) * chunks];
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const F2 p = x[t][m], q = y[t][m];
+                x[t][m] = mul(p, f2(ab.x, ab.y));
+                y[t][m] = mul(q, f2(cd.x, cd.y));
+                if (rotate) {
+                  x[t][m] = fma(q, f2(ab.z, ab.w), x[t][m]);
+                  y[t][m] = fma(p, f2(cd.z, cd.w), y[t][m]);
+                }
+              }
+            }
+          }
+          if (e8) __syncwarp();                                 // a row's bytes lie over its lanes' values
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const F2 s2 = f2(scale[t], scale[t]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              x[t][m] = mul(x[t][m], s2);
+              y[t][m] = mul(y[t][m], s2);
+            }
+            float f[16];
+            order16<HALF>(x[t], y[t], f);
+            if (!on[t]) continue;
+            uint8_t* row = stage + (hb + t * rows) * row_bytes;
+            if (e8) {
+              *reinterpret_cast<uint2*>(row + o0) = pack8_e4m3(f);
+              *reinterpret_cast<uint2*>(row + o1) = pack8_e4m3(f + 8);
+            } else {
+              *reinterpret_cast<uint4*>(row + 2 * o0) = pack8<T>(f);
+              *reinterpret_cast<uint4*>(row + 2 * o1) = pack8<T>(f + 8);
+            }
+          }
+        }
+      }
+      sm100::fence_proxy_async_smem();
+      __syncwarp();
+      if (!skip) {
+        const uint32_t src = st0 + st * kStageBytes;
+        if (kind == 0) {
+          if (lane == 0) bulk_store(static_cast<T*>(a.q_out) + ((int64_t)i * a.h_q + h0) * a.d, src, n * row_bytes);
+        } else {
+          const int eb = e8 ? 1 : 2;
+          uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + (at + h0 * a.head_stride) * eb;
+          if (a.head_stride == a.d && !e8) {
+            if (lane == 0) bulk_store(dst, src, n * row_bytes);
+          } else {
+            for (int h = lane; h < n; h += 32) bulk_store(dst + h * a.head_stride * eb, src + h * row_bytes, a.d * eb);
+          }
+        }
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
       }
     }
+    u = 0;
+    ++i;
   }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // written before the kernel ends
 }
 
 }  // namespace
 
-kvsel_status launch_rope_append(const RopeArgs& a, int32_t dtype, int32_t layout, cudaStream_t s) {
+kvsel_status launch_rope_append(const RopeArgs& in, int32_t dtype, int32_t layout, cudaStream_t s) {
+  using Kernel = void (*)(const RopeArgs);
+  RopeArgs a = in;
   int group = 1;
   while (group < a.d / 16) group <<= 1;
-  const int rows = 32 / group;
-  const int total = (a.q != nullptr ? (a.h_q + rows - 1) / rows : 0) + (a.k != nullptr ? 2 * ((a.h_kv + rows - 1) / rows) : 0);
-  int64_t parts = ceil_div(152 * 16, a.n);
-  if (parts > total) parts = total;
-  const int64_t grid = ceil_div(a.n * parts, kRopeThreads / 32);
-  if (grid >= (int64_t(1) << 31)) return KVSEL_ERR_UNSUPPORTED;
-  TraceScope ts("rope_append", s);
+  const int rows = 32 / group, fit = kStageBytes / (2 * a.d);
+  a.unit_rows = fit >= rows ? fit / rows * rows : fit;
   const bool half = layout == KVSEL_ROPE_HALF;
-  if (dtype == KVSEL_DTYPE_BF16) {
-    if (half) rope_append<__nv_bfloat16, true><<<(unsigned)grid, kRopeThreads, 0, s>>>(a, (int)parts);
-    else rope_append<__nv_bfloat16, false><<<(unsigned)grid, kRopeThreads, 0, s>>>(a, (int)parts);
-  } else {
-    if (half) rope_append<__half, true><<<(unsigned)grid, kRopeThreads, 0, s>>>(a, (int)parts);
-    else rope_append<__half, false><<<(unsigned)grid, kRopeThreads, 0, s>>>(a, (int)parts);
-  }
+  auto pick = [&](auto t) -> Kernel {
+    using T = decltype(t);
+    if (group == 8) return half ? rope_append<T, true, 8> : rope_append<T, false, 8>;
+    if (group == 4) return half ? rope_append<T, true, 4> : rope_append<T, false, 4>;
+    return half ? rope_append<T, true, 0> : rope_append<T, false, 0>;
+  };
+  const Kernel kern = dtype == KVSEL_DTYPE_BF16 ? pick(__nv_bfloat16()) : pick(__half());
+  const size_t smem = rope_smem(a.d, a.rot);
+  const int64_t resident = resident_ctas((const void*)kern, kRopeThreads, smem);
+  if (resident <= 0) return KVSEL_ERR_CUDA;
+  const int64_t units = (a.q != nullptr ? ceil_div(a.h_q, a.unit_rows) : 0) + (a.k != nullptr ? 2 * ceil_div(a.h_kv, a.unit_rows) : 0);
+  const int64_t grid = std::min(resident, ceil_div(a.n * units, kWarps));
+  a.share = a.n * units / (grid * kWarps);
+  a.extra = a.n * units % (grid * kWarps);
+  TraceScope ts("rope_append", s);
+  kern<<<(unsigned)grid, kRopeThreads, smem, s>>>(a);
   return launch_status();
 }
 
