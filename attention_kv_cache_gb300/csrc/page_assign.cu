@@ -76,6 +76,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_assign_plan(const __grid_co
   int32_t* pg = tok + a.batch + 1;
   int32_t* old = pg + a.batch + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
+  wait_for_earlier_kernels();
+  if (!fill) let_later_kernels_start();                        // (the fill: it waits for this grid's end)
   const int64_t head = *a.free_head;
   const int64_t cap = (int64_t)a.max_blocks * a.P;             // < 2^31
   if (tid == 0) bad = 0x7fffffff;
@@ -170,6 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_assign_plan(const __grid_co
 // The tokens and table entries of a planned step.
 __global__ void __launch_bounds__(kFillThreads) page_assign_fill(const __grid_constant__ AssignArgs a) {
   extern __shared__ int32_t tok[];
+  wait_for_earlier_kernels();
   Plan p;
   p.n_tok = a.plan[0];
   p.n_pg = a.plan[1];
@@ -197,14 +200,12 @@ kvsel_status launch_page_assign(const AssignArgs& a, cudaStream_t s) {
   if (set_smem((const void*)page_assign_plan, smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   {
     TraceScope ts("page_assign", s);
-    page_assign_plan<<<1, threads, smem, s>>>(a, one ? 1 : 0);
-    const kvsel_status st = launch_status();
+    const kvsel_status st = launch_after(page_assign_plan, dim3(1), threads, smem, s, a, one ? 1 : 0);
     if (st != KVSEL_OK || one) return st;
   }
   TraceScope ts("page_assign_fill", s);
   const int64_t grid = ceil_div(a.max_tokens, (int64_t)kFillThreads * kTokensPerThread);
-  page_assign_fill<<<(unsigned)grid, kFillThreads, sizeof(int32_t) * (a.batch + 1), s>>>(a);
-  return launch_status();
+  return launch_after(page_assign_fill, dim3((unsigned)grid), kFillThreads, sizeof(int32_t) * (a.batch + 1), s, a);
 }
 
 }  // namespace kvsel

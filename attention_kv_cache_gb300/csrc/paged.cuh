@@ -7,6 +7,29 @@ namespace kvsel {
 
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A launch whose CTAs may start while the stream's last kernel drains; the kernel calls wait_for_earlier_kernels()
+// before it touches memory that others write or read.
+template <typename... Params, typename... Args>
+kvsel_status launch_after(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  const bool ok = cudaLaunchKernelEx(&c, kern, static_cast<Params>(args)...) == cudaSuccess;
+  count_launch();
+  return ok && cudaGetLastError() == cudaSuccess ? KVSEL_OK : KVSEL_ERR_CUDA;
+}
+// Everything the stream's earlier kernels wrote is there, and what they read may be overwritten.
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The stream's next kernel may be launched (it still waits for this grid's end before it touches memory).
+__device__ __forceinline__ void let_later_kernels_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // CTAs of a kernel resident at once on the current device (0: it cannot be queried), asked once per device,
 // kernel and shared-memory size (paged_api.cu).
 int64_t resident_ctas(const void* kern, int threads, size_t smem);

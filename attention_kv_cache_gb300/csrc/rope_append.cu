@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
     sm100::fence_barrier_init();
   }
   __syncwarp();
+  wait_for_earlier_kernels();
   const float inv_d = 1.f / (float)a.d;
   const int row_bytes = a.d * 2;
   const int iq = a.q != nullptr ? (a.h_q + a.unit_rows - 1) / a.unit_rows : 0;
@@ -431,8 +432,7 @@ kvsel_status launch_rope_append(const RopeArgs& in, int32_t dtype, int32_t layou
   a.share = a.n * units / (grid * kWarps);
   a.extra = a.n * units % (grid * kWarps);
   TraceScope ts("rope_append", s);
-  kern<<<(unsigned)grid, kRopeThreads, smem, s>>>(a);
-  return launch_status();
+  return launch_after(kern, dim3((unsigned)grid), kRopeThreads, smem, s, a);
 }
 
 }  // namespace kvsel

@@ -438,7 +438,8 @@ enum { KVSEL_DTYPE_BF16 = 0, KVSEL_DTYPE_F16 = 1, KVSEL_DTYPE_E4M3 = 2 };
 
 /* A pool of pages of one layer's K (and one of its V): the row of KV head g at slot s starts at element
  * (s / P) * page_stride + g * head_stride + (s % P) * row_stride and is contiguous.  Both orders of a page
- * (heads outside rows, rows outside heads) are strides, and so is a packed [h_kv][rows][d] cache. */
+ * (heads outside rows, rows outside heads) are strides, and so is a packed [h_kv][rows][d] cache.
+ * Every row of every page is memory that a call may read, whatever it holds. */
 typedef struct {
   int32_t h_q;            /* query heads, multiple of h_kv */
   int32_t h_kv;           /* KV heads >= 1 */
