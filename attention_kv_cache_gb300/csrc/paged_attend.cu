@@ -1,89 +1,77 @@
 // Attention over a paged pool: the merge of the requests' pieces, and the launches (the kernels are in paged_attend.cuh).
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "paged_attend.cuh"
 
 namespace kvsel {
 namespace {
 
-// o of a request that several lanes hold: sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over its pieces in lane
-// order.  blockIdx.y is the request, or (more requests than lanes) the lane in which one begins that goes on; blockIdx.x
-// takes `heads` query heads of it.  Every piece's rows are 128-byte lines read once.  A request of few pieces gives a
-// warp to each head; of many, all warps to one head after another, each warp a share of the pieces.
+// o of a request that several lanes hold: sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over its pieces i.
+// blockIdx.y is the request (or the lane) whose span says which pieces; blockIdx.x takes `heads` query heads of it.
+// A request of few pieces gives a warp to each head; of many, all warps to one head after another, each warp every
+// kJoinWarps-th piece.  A warp loads kJoinLoads pieces at once, offsets and rows together, and keeps its own running
+// offset: latency is what this costs, so nothing waits for anything but the span.
 //
 // Launched while the attention runs (its CTAs fit beside it) and waiting for its end, so that no launch lies between.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
+constexpr int kJoinLoads = 10;
 constexpr int kFewPieces = 16;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join(const __grid_constant__ PagedArgs a, int nt8, int by_lane, int heads) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join(const __grid_constant__ PagedArgs a, int nt8, int heads) {
   constexpr int V = D / 32;                         // values of a row per lane
-  __shared__ float red[kJoinWarps][D];
-  __shared__ float redl[kJoinWarps];
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  __shared__ Vec red[kJoinWarps][32];
+  __shared__ float2 redml[kJoinWarps];
   wait_for_earlier_kernels();
-  const int T = a.cum[a.batch], N = a.cum[a.batch + 1];
-  int b = blockIdx.y;
-  if (by_lane) {
-    const int li = blockIdx.y;
-    if (li >= N) return;
-    const int end = lane_begin(li + 1, T, N);
-    if (end <= lane_begin(li, T, N) || end >= T) return;
-    b = find_request(a.cum, a.batch, end - 1);      // the request of the lane's last step
-    if (a.cum[b] < lane_begin(li, T, N)) return;    // it began in an earlier lane
-  }
-  const int c0 = a.cum[b], c1 = a.cum[b + 1];
-  if (c0 == c1) return;
-  const int i0 = lane_of(c0, T, N), i1 = lane_of(c1 - 1, T, N);
-  if (i0 == i1) return;
+  const int2 span = a.span[blockIdx.y];
+  const int b = a.by_lane ? span.x : blockIdx.y, i0 = a.by_lane ? blockIdx.y : span.x, i1 = span.y;
+  if (i0 >= i1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int padded = a.h_kv * a.tiles * nt8;
-  const bool few = i1 - i0 < kFewPieces;
+  const bool few = heads > 1 && i1 - i0 < kFewPieces;
   for (int hh = few ? warp : 0; hh < heads; hh += few ? kJoinWarps : 1) {
     const int h = blockIdx.x * heads + hh;
     if (h >= a.h_q) return;                         // (the whole CTA where its warps share a head)
     const int g = h / a.G;
     const int at = g * a.tiles * nt8 + (h - g * a.G);                    // the head among the padded heads
-    auto row_of = [&](int i) -> int64_t { return (int64_t)(2 * i + (i == i0 ? 1 : 0)) * padded + at; };
-    float M = -INFINITY;
-    for (int i = i0 + lane; i <= i1; i += 32) M = fmaxf(M, a.part_ml[row_of(i)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float num[V], den = 0.f;
+    float M = -INFINITY, den = 0.f, num[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) num[e] = 0.f;
-#pragma unroll 4
-    for (int i = i0 + (few ? 0 : warp); i <= i1; i += few ? 1 : kJoinWarps) {
-      const int64_t r = row_of(i);
-      const float2 ml = a.part_ml[r];
-      const float w = ml.x == M ? 1.f : exp2f(ml.x - M);   // (both -inf: scores that are all NaN, or no score)
-      float v[V];
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(a.part + r * D + 4 * lane);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(a.part + r * D + 2 * lane);
-        v[0] = x.x, v[1] = x.y;
-      }
+    // (offset, sum, row) taken into the warp's own; a piece whose scores were all NaN, or none, has offset -inf
+    auto take = [&](float2 ml, const float* v) {
+      const float top = fmaxf(M, ml.x);
+      const float wo = M == top ? 1.f : exp2f(M - top), wn = ml.x == top ? 1.f : exp2f(ml.x - top);
+      M = top;
+      den = den * wo + ml.y * wn;
 #pragma unroll
-      for (int e = 0; e < V; ++e) num[e] = fmaf(w, v[e], num[e]);
-      den = fmaf(w, ml.y, den);
+      for (int e = 0; e < V; ++e) num[e] = num[e] * wo + v[e] * wn;
+    };
+    const int step = few ? 1 : kJoinWarps;
+    for (int i = i0 + (few ? 0 : warp); i <= i1; i += kJoinLoads * step) {
+      float2 ml[kJoinLoads];
+      Vec v[kJoinLoads];
+#pragma unroll
+      for (int k = 0; k < kJoinLoads; ++k)
+        if (i + k * step <= i1) {
+          const int64_t r = (int64_t)(2 * (i + k * step) + (i + k * step == i0 ? 1 : 0)) * padded + at;
+          ml[k] = a.part_ml[r];
+          v[k] = reinterpret_cast<const Vec*>(a.part + r * D)[lane];
+        }
+#pragma unroll
+      for (int k = 0; k < kJoinLoads; ++k)
+        if (i + k * step <= i1) take(ml[k], reinterpret_cast<const float*>(&v[k]));
     }
     if (!few) {
       __syncthreads();                              // the last head's sums are read
 #pragma unroll
-      for (int e = 0; e < V; ++e) red[warp][V * lane + e] = num[e];
-      if (lane == 0) redl[warp] = den;
+      for (int e = 0; e < V; ++e) reinterpret_cast<float*>(&red[warp][lane])[e] = num[e];
+      if (lane == 0) redml[warp] = make_float2(M, den);
       __syncthreads();
       if (warp != 0) continue;
-      den = 0.f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) num[e] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kJoinWarps; ++i) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) num[e] += red[i][V * lane + e];
-        den += redl[i];
-      }
+      for (int i = 1; i < kJoinWarps; ++i) take(redml[i], reinterpret_cast<const float*>(&red[i][lane]));
     }
     const float s = den == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / den;
     const int64_t oh = (int64_t)b * a.h_q + h;
@@ -130,8 +118,8 @@ int sm_count() {
 }
 
 struct Geometry {
-  int nt, tiles, lanes, grid;
-  size_t cum_off, ml_off, part_off, total;
+  int nt, tiles, lanes, grid, by_lane;
+  size_t span_off, ml_off, part_off, total;
 };
 // One CTA per SM, fewer when the bound on the steps needs fewer warps.
 bool geometry(const PagedShape& p, Geometry* out) {
@@ -150,8 +138,9 @@ bool geometry(const PagedShape& p, Geometry* out) {
   o.grid = (int)std::min<int64_t>(sms, ceil_div(lanes * units, v.warps));
   const int64_t heads = units * 8 * o.nt;
   auto up = [](size_t x) { return (x + KVSEL_WS_ALIGN - 1) / KVSEL_WS_ALIGN * KVSEL_WS_ALIGN; };
-  o.cum_off = sizeof(DeviceError);
-  o.ml_off = up(o.cum_off + sizeof(int32_t) * ((size_t)p.batch + 2));
+  o.by_lane = p.batch > lanes;
+  o.span_off = sizeof(DeviceError);
+  o.ml_off = up(o.span_off + sizeof(int2) * (size_t)(o.by_lane ? lanes : p.batch));
   o.part_off = up(o.ml_off + sizeof(float2) * 2 * (size_t)(lanes * heads));
   o.total = up(o.part_off + sizeof(float) * 2 * (size_t)(lanes * heads) * p.d);
   return true;
@@ -183,7 +172,7 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.v_scale = v_scale;
   a.o = o;
   a.lse = lse;
-  a.cum = reinterpret_cast<int32_t*>(base + geo.cum_off);
+  a.span = reinterpret_cast<int2*>(base + geo.span_off);
   a.part_ml = reinterpret_cast<float2*>(base + geo.ml_off);
   a.part = reinterpret_cast<float*>(base + geo.part_off);
   a.err = reinterpret_cast<DeviceError*>(ws);
@@ -204,6 +193,7 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.out_f16 = p.dtype == KVSEL_DTYPE_F16;
   a.tiles = geo.tiles;
   a.lanes = geo.lanes;
+  a.by_lane = geo.by_lane;
   const size_t smem = var.smem + sizeof(int32_t) * (size_t)p.batch;
   if (set_smem((const void*)var.kern, smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   {
@@ -212,11 +202,10 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
     if (st != KVSEL_OK) return st;
   }
   TraceScope ts("paged_join", s);
-  const int by_lane = p.batch > geo.lanes;
-  const int rows = by_lane ? geo.lanes : p.batch;
+  const int rows = geo.by_lane ? geo.lanes : p.batch;
   const int heads = (int64_t)rows * p.h_q > 4 * 152 ? kJoinWarps : 1;    // a CTA per head while those are few
   const dim3 grid((unsigned)ceil_div(p.h_q, heads), (unsigned)rows);
-  return launch_after(p.d == 64 ? paged_join<64> : paged_join<128>, grid, 32 * kJoinWarps, 0, s, a, 8 * geo.nt, by_lane, heads);
+  return launch_after(p.d == 64 ? paged_join<64> : paged_join<128>, grid, 32 * kJoinWarps, 0, s, a, 8 * geo.nt, heads);
 }
 
 }  // namespace kvsel

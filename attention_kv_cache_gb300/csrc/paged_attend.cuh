@@ -41,13 +41,16 @@ struct PagedArgs {
   float* lse;
   float* part;          // [2 * lanes][h_kv * tiles * 8 * NT][d]: partial O
   float2* part_ml;      // [2 * lanes][h_kv * tiles * 8 * NT]: its offset (base 2) and sum
-  int32_t* cum;         // [batch + 1] first step of each request, then the lanes in use
+  // What paged_join merges: of every request its first and last lane, or (more requests than lanes, by_lane) of every
+  // lane the request that begins in it and goes on, and that request's last lane.  First >= last: nothing.
+  int2* span;
   DeviceError* err;
   int64_t page_stride, head_stride, row_stride, q_stride;
   float scale, softcap;
   int32_t h_q, h_kv, G, P, batch, max_blocks, n_pages, window, out_f16;
   int32_t tiles;        // tiles of query heads per KV head
   int32_t lanes;        // lanes the grid can hold
+  int32_t by_lane;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -225,10 +228,9 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
   let_later_kernels_start();                        // (paged_join: it waits for this grid's end)
   const int T = step_sums<32 * W>(a, cum);
   const int N = max(1, min(a.lanes, T / kMinSteps));
-  if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b <= a.batch; b += 32 * W) a.cum[b] = cum[b];
-    if (threadIdx.x == 0) a.cum[a.batch + 1] = N;
-  }
+  if (a.by_lane && blockIdx.x == 0)                 // lanes without a step
+    for (int i = threadIdx.x; i < a.lanes; i += 32 * W)
+      if (i >= N || lane_begin(i, T, N) == lane_begin(i + 1, T, N)) a.span[i] = make_int2(0, -1);
   // requests without a row: o = 0, lse = -inf
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
     if (cum[b] != cum[b + 1]) continue;
@@ -236,6 +238,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
     for (int x = threadIdx.x; x < a.h_q * (D / 2); x += 32 * W) ob[x] = 0u;
     if (a.lse != nullptr)
       for (int x = threadIdx.x; x < a.h_q; x += 32 * W) a.lse[(int64_t)b * a.h_q + x] = -INFINITY;
+    if (!a.by_lane && threadIdx.x == 0) a.span[b] = make_int2(0, -1);
   }
   const int units = a.h_kv * a.tiles;
   const int heads_pad = units * 8 * NT;
@@ -316,6 +319,10 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       const int f = first_row(n, a.window);
       const int row_end = min(x1, cum[b + 1]);
       const bool starts = x == cum[b], ends = row_end == cum[b + 1];
+      if (unit == 0 && lane == 0) {                 // (one warp of the lane speaks for all)
+        if (!a.by_lane && starts) a.span[b] = make_int2(li, ends ? li : lane_of(cum[b + 1] - 1, T, N));
+        if (a.by_lane && row_end == x1) a.span[li] = make_int2(b, starts && !ends ? lane_of(cum[b + 1] - 1, T, N) : -1);
+      }
       // B fragments of the query rows (head 8 nt + gq of the tile): elements 2 tq, +1 and 8 + 2 tq, +1 of
       // every 16, or 4 tq .. 4 tq + 3 where the K fragments come from bytes
       uint32_t qb[NT][KS][2];
