@@ -174,10 +174,26 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current_stream = None      # () -> handle of torch's current stream on the current device
+
+
+def _find_current_stream():
+    """torch.cuda.current_stream() builds a Stream object (2.8 us of a call); where torch has them, its own getters of
+    the handle take 0.2 us."""
+    global _current_stream
+    import torch
+    handle = torch.cuda.current_stream().cuda_stream          # (initialises CUDA on the first call)
+    device, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if device is not None and raw is not None and raw(device()) == handle:
+        _current_stream = lambda: raw(device())
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return handle
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream() if _current_stream is not None else _find_current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -372,7 +388,7 @@ def kvsel_rope_append(cache: CacheDesc, rope: RopeDesc, q, k, v, positions, slot
                       k_cache, v_cache, k_scale=None, v_scale=None, ws=None, stream=None):
     """The number of tokens is the first dimension of q (or of k without q)."""
     n = (k if q is None else q).shape[0]
-    _check(_lib.kvsel_rope_append(ctypes.byref(cache), ctypes.byref(rope), n, _ptr(q), _ptr(k), _ptr(v),
+    _check(_lib.kvsel_rope_append(cache, rope, n, _ptr(q), _ptr(k), _ptr(v),
                                   _ptr(positions), _ptr(slots), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
                                   _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(ws),
                                   _stream(stream)), "kvsel_rope_append")
@@ -388,7 +404,7 @@ def kvsel_paged_attend_workspace_size(cache: CacheDesc, desc: PagedAttendDesc) -
 def kvsel_paged_attend(cache: CacheDesc, desc: PagedAttendDesc, q, k_cache, v_cache, block_tables, lens, slopes, k_scale,
                        v_scale, o, lse, ws, ws_bytes=None, stream=None):
     nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
-    _check(_lib.kvsel_paged_attend(ctypes.byref(cache), ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+    _check(_lib.kvsel_paged_attend(cache, desc, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                    _ptr(block_tables), _ptr(lens), _ptr(slopes), _ptr(k_scale), _ptr(v_scale),
                                    _ptr(o), _ptr(lse), _ptr(ws), nb, _stream(stream)), "kvsel_paged_attend")
 
