@@ -186,6 +186,9 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.h_kv = p.h_kv;
   a.G = p.h_q / p.h_kv;
   a.P = p.P;
+  a.p_shift = 0;
+  while ((1 << a.p_shift) < p.P) ++a.p_shift;
+  a.p_mul = (uint32_t)((((uint64_t)1 << 32) * ((1u << a.p_shift) - (uint32_t)p.P)) / (uint32_t)p.P + 1);
   a.batch = p.batch;
   a.max_blocks = p.max_blocks;
   a.n_pages = p.n_pages;

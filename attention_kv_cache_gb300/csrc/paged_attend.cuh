@@ -28,7 +28,7 @@
 namespace kvsel {
 
 constexpr int kKeys = 32;             // rows per step: one per lane
-constexpr int kMinSteps = 2;          // a lane is not given fewer steps than this
+constexpr int kMinSteps = 1;          // a lane is not given fewer steps than this
 constexpr float kLog2e = 1.4426950408889634f;
 enum Kind { kBf16 = 0, kF16 = 1, kE4m3 = 2 };
 
@@ -48,6 +48,7 @@ struct PagedArgs {
   int64_t page_stride, head_stride, row_stride, q_stride;
   float scale, softcap;
   int32_t h_q, h_kv, G, P, batch, max_blocks, n_pages, window, out_f16;
+  uint32_t p_mul, p_shift;   // division of a row below 2^31 by P: (mulhi(p_mul, t) + t) >> p_shift
   int32_t tiles;        // tiles of query heads per KV head
   int32_t lanes;        // lanes the grid can hold
   int32_t by_lane;
@@ -254,11 +255,13 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
     int pb = find_request(cum, a.batch, x0);        // request of the next step to look up
     int pn = (int)a.lens[pb];
     int px = x0;
-    // This lane's row of step px: its page (-1: not seen, or not in the pool) and its row there; looked up a step before
-    // its copy.
-    int32_t id = -1, within = 0;
-    auto look = [&]() {
-      id = -1;
+    // This lane's row of a step: its page's entry in the table (read ahead: nothing waits for it here) and its row there.
+    struct Row {
+      int32_t id, within, b;
+      bool seen;
+    };
+    auto look = [&]() -> Row {
+      Row r{0, 0, 0, false};
       if (px < x1) {
         while (px >= cum[pb + 1]) {
           ++pb;
@@ -266,23 +269,24 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
         }
         const int f = first_row(pn, a.window);
         const int t = (f / kKeys + (px - cum[pb])) * kKeys + lane;
-        if (t >= f && t < pn) {
-          const int blk = t / a.P;
-          within = t - blk * a.P;
-          id = __ldg(a.tables + (int64_t)pb * a.max_blocks + blk);
-          if (id < 0 || id >= a.n_pages) {
-            set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)pb);
-            id = -1;
-          }
+        r.b = pb;
+        r.seen = t >= f && t < pn;
+        if (r.seen) {
+          const int blk = (int)((__umulhi(a.p_mul, (uint32_t)t) + (uint32_t)t) >> a.p_shift);   // t / P
+          r.within = t - blk * a.P;
+          r.id = __ldg(a.tables + (int64_t)pb * a.max_blocks + blk);
         }
         ++px;
       }
+      return r;
     };
-    // Copies the looked-up step into stage `buf`, 16-byte chunks by all lanes, whole rows at a time, and returns the rows
-    // it has; rows without a source are zeros.
-    auto issue = [&](int buf) -> uint32_t {
-      const int64_t off = (id < 0 ? 0 : (int64_t)id * a.page_stride + (int64_t)within * a.row_stride) * elem_bytes<KIND>();
-      const uint32_t seen = __ballot_sync(0xffffffffu, id >= 0);
+    // Copies a step into stage `buf`, 16-byte chunks by all lanes, whole rows at a time, and returns the rows it has;
+    // rows without a source are zeros.
+    auto issue = [&](const Row& r, int buf) -> uint32_t {
+      const bool ok = r.seen && r.id >= 0 && r.id < a.n_pages;
+      if (r.seen && !ok) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)r.b);
+      const int64_t off = (ok ? (int64_t)r.id * a.page_stride + (int64_t)r.within * a.row_stride : 0) * elem_bytes<KIND>();
+      const uint32_t seen = __ballot_sync(0xffffffffu, ok);
       constexpr int KPI = 32 / CPR;                 // rows per copy instruction
       const uint32_t ks = st0 + buf * stage_bytes<D, KIND>();
       const int c = lane % CPR;
@@ -290,24 +294,27 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       for (int i = 0; i < kKeys / KPI; ++i) {
         const int x = i * KPI + lane / CPR;
         const int64_t ox = __shfl_sync(0xffffffffu, off, x) + c * 16;
-        const bool ok = (seen >> x) & 1u;
+        const bool has = (seen >> x) & 1u;
         const uint32_t dst = ks + chunk_at<RB>(x, c);
-        cp_async16(dst, kbase + ox, ok);
-        cp_async16(dst + KV, vbase + ox, ok);
+        cp_async16(dst, kbase + ox, has);
+        cp_async16(dst + KV, vbase + ox, has);
       }
       return seen;
     };
     uint32_t seen[NS];                              // rows of the stages, by age: seen[0] is the step computed
 #pragma unroll
     for (int i = 0; i < NS; ++i) seen[i] = 0;
-    look();
+    Row next;                                       // of the step to copy next
+    {
+      Row ahead[NS];
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) {
-      if (x0 + i < x1) {
-        seen[i] = issue(i);
-        look();
+      for (int i = 0; i < NS; ++i) ahead[i] = look();
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i) {
+        if (x0 + i < x1) seen[i] = issue(ahead[i], i);
+        asm volatile("cp.async.commit_group;" ::: "memory");
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      next = ahead[NS - 1];
     }
 
     // ---- the row pieces of this lane --------------------------------------------------------------
@@ -397,8 +404,8 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
         // the step NS - 1 ahead into the stage read last
         uint32_t ahead = 0;
         if (x + NS - 1 < x1) {
-          ahead = issue(buf == 0 ? NS - 1 : buf - 1);
-          look();
+          ahead = issue(next, buf == 0 ? NS - 1 : buf - 1);
+          next = look();
         }
         seen[NS - 1] = ahead;
         const uint32_t ks = st0 + buf * stage_bytes<D, KIND>(), vs = ks + KV;
