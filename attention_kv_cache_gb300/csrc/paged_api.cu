@@ -2,7 +2,6 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
-#include <vector>
 
 #include "paged.cuh"
 
@@ -75,23 +74,28 @@ int64_t resident_ctas(const void* kern, int threads, size_t smem) {
     size_t smem;
     int64_t n;
   };
+  constexpr int kMost = 128;                // further combinations are asked every time
   static std::mutex mu;
-  static std::vector<Entry> known;
+  static Entry known[kMost];
+  static int n_known = 0;
   int dev = 0, sms = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     (void)cudaGetLastError();
     return 0;
   }
   std::lock_guard<std::mutex> lock(mu);
-  for (const Entry& e : known)
+  for (int i = 0; i < n_known; ++i) {
+    const Entry& e = known[i];
     if (e.dev == dev && e.kern == kern && e.threads == threads && e.smem == smem) return e.n;
+  }
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || set_smem(kern, smem) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess) {
     (void)cudaGetLastError();
     return 0;
   }
-  known.push_back({dev, threads, kern, smem, (int64_t)sms * per_sm});
-  return known.back().n;
+  const int64_t n = (int64_t)sms * per_sm;
+  if (n_known < kMost) known[n_known++] = {dev, threads, kern, smem, n};
+  return n;
 }
 
 }  // namespace kvsel

@@ -197,7 +197,7 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.tiles = geo.tiles;
   a.lanes = geo.lanes;
   a.by_lane = geo.by_lane;
-  const size_t smem = var.smem + sizeof(int32_t) * (size_t)p.batch;
+  const size_t smem = var.smem + sizeof(int2) * (size_t)p.batch;
   if (set_smem((const void*)var.kern, smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   {
     TraceScope ts("paged_attend", s);

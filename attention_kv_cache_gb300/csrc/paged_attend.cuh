@@ -132,7 +132,7 @@ template <int D, int KIND>
 __host__ __device__ constexpr int n_stages() { return 196608 / (n_warps<D, KIND>() * stage_bytes<D, KIND>()); }
 template <int D, int KIND>
 __host__ __device__ constexpr int smem_bytes(int batch) {
-  return 1024 + n_warps<D, KIND>() * n_stages<D, KIND>() * stage_bytes<D, KIND>() + 4 * (batch + 1);
+  return 1024 + n_warps<D, KIND>() * n_stages<D, KIND>() * stage_bytes<D, KIND>() + 8 * (batch + 1);
 }
 
 // Byte offset of 16-byte chunk c of row x: halves of 128-byte rows one after another, chunks of eight rows
@@ -152,13 +152,14 @@ __device__ __forceinline__ uint32_t chunk_from(uint32_t at, int mt, int c) {
 // First visible row of a request of n rows.
 __device__ __forceinline__ int first_row(int n, int window) { return window > 0 && n > window ? n - window : 0; }
 // First step of lane i of N over T steps.
-__device__ __forceinline__ int lane_begin(int i, int T, int N) { return (int)((int64_t)i * T / N); }
+__device__ __forceinline__ int quotient(uint64_t x, int y) { return (x >> 32) == 0 ? (int)((uint32_t)x / (uint32_t)y) : (int)(x / y); }
+__device__ __forceinline__ int lane_begin(int i, int T, int N) { return quotient((uint64_t)i * T, N); }
 // The lane that holds step x.
-__device__ __forceinline__ int lane_of(int x, int T, int N) { return (int)(((int64_t)(x + 1) * N + T - 1) / T) - 1; }
+__device__ __forceinline__ int lane_of(int x, int T, int N) { return quotient((uint64_t)(x + 1) * N + T - 1, T) - 1; }
 
-// cum[b] = steps of the requests before b, in shared memory; returns all steps.  Every CTA forms it.
+// cum[b] = (steps of the requests before b, rows of b), in shared memory; returns all steps.  Every CTA forms it.
 template <int THREADS>
-__device__ int step_sums(const PagedArgs& a, int32_t* cum) {
+__device__ int step_sums(const PagedArgs& a, int2* cum) {
   __shared__ int32_t warp_sum[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.batch + THREADS - 1) / THREADS;
@@ -173,7 +174,7 @@ __device__ int step_sums(const PagedArgs& a, int32_t* cum) {
     }
     const int n = (int)L;
     const int steps = (n + kKeys - 1) / kKeys - first_row(n, a.window) / kKeys;
-    cum[b] = steps;
+    cum[b] = make_int2(steps, n);
     sum += steps;
   }
   int inc = sum;
@@ -191,20 +192,20 @@ __device__ int step_sums(const PagedArgs& a, int32_t* cum) {
   }
   int at = base + inc - sum;
   for (int b = b0; b < b1; ++b) {
-    const int s = cum[b];
-    cum[b] = at;
+    const int s = cum[b].x;
+    cum[b].x = at;
     at += s;
   }
-  if (tid == 0) cum[a.batch] = total;
+  if (tid == 0) cum[a.batch] = make_int2(total, 0);
   __syncthreads();
   return total;
 }
 
-__device__ __forceinline__ int find_request(const int32_t* cum, int batch, int x) {
+__device__ __forceinline__ int find_request(const int2* cum, int batch, int x) {
   int lo = 0, hi = batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= x) lo = mid; else hi = mid;
+    if (cum[mid].x <= x) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
   constexpr int KS = D / 16;                        // 16-wide slices of the head dim
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  int32_t* cum = reinterpret_cast<int32_t*>(sbase + W * NS * stage_bytes<D, KIND>());
+  int2* cum = reinterpret_cast<int2*>(sbase + W * NS * stage_bytes<D, KIND>());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
   const uint32_t st0 = sm100::smem_addr(sbase) + warp * NS * stage_bytes<D, KIND>();
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       if (i >= N || lane_begin(i, T, N) == lane_begin(i + 1, T, N)) a.span[i] = make_int2(0, -1);
   // requests without a row: o = 0, lse = -inf
   for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-    if (cum[b] != cum[b + 1]) continue;
+    if (cum[b].x != cum[b + 1].x) continue;
     uint32_t* ob = reinterpret_cast<uint32_t*>(a.o) + (int64_t)b * a.h_q * (D / 2);
     for (int x = threadIdx.x; x < a.h_q * (D / 2); x += 32 * W) ob[x] = 0u;
     if (a.lse != nullptr)
@@ -251,9 +252,45 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
     const uint8_t* kbase = static_cast<const uint8_t*>(a.k) + (int64_t)g * a.head_stride * elem_bytes<KIND>();
     const uint8_t* vbase = static_cast<const uint8_t*>(a.v) + (int64_t)g * a.head_stride * elem_bytes<KIND>();
 
+    // ---- what all requests share: scales and slopes of the unit's heads (2 tq, 2 tq + 1 of each tile); in base 2, but for
+    // capped scores, which get it with the cap
+    const float ksc = a.scale * (a.k_scale != nullptr ? a.k_scale[g] : 1.f) * (a.softcap != 0.f ? 1.f : kLog2e);
+    const float vsc = a.v_scale != nullptr ? a.v_scale[g] : 1.f;
+    const float cap2 = a.softcap * kLog2e, icap = a.softcap != 0.f ? 1.f / a.softcap : 0.f;
+    const bool plain = a.softcap == 0.f && a.slopes == nullptr;
+    float sl[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hl = (tile * NT + nt) * 8 + 2 * tq + e;
+        sl[nt][e] = a.slopes != nullptr && hl < a.G ? a.slopes[g * a.G + hl] * kLog2e : 0.f;
+      }
+    // Query rows of a request (heads 8 nt + gq of the tile) as they are: elements 2 tq, +1 and 8 + 2 tq, +1 of every 16,
+    // or 4 tq .. 4 tq + 3 where the K fragments come from bytes.  With one tile per warp they are fetched a request
+    // ahead (two tiles leave no registers for that).
+    uint32_t qn[NT][KS][2];
+    auto load_q = [&](int request, uint32_t (*to)[KS][2]) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hl = (tile * NT + nt) * 8 + gq;
+        const bool live = hl < a.G;
+        const uint32_t* qrow = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
+                                                                 (int64_t)request * a.q_stride +
+                                                                 (int64_t)(live ? g * a.G + hl : 0) * D);
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          const int e0 = KIND == kE4m3 ? 2 * tq : tq, e1 = KIND == kE4m3 ? 2 * tq + 1 : 4 + tq;
+          to[nt][c][0] = live ? __ldg(qrow + 8 * c + e0) : 0u;
+          to[nt][c][1] = live ? __ldg(qrow + 8 * c + e1) : 0u;
+        }
+      }
+    };
+    int b = find_request(cum, a.batch, x0);         // request of the next piece
+    if (NT == 1) load_q(b, qn);
+
     // ---- the steps' rows, ahead of the arithmetic -----------------------------------------------
-    int pb = find_request(cum, a.batch, x0);        // request of the next step to look up
-    int pn = (int)a.lens[pb];
+    int pb = b;                                     // request of the next step to look up
     int px = x0;
     // This lane's row of a step: its page's entry in the table (read ahead: nothing waits for it here) and its row there.
     struct Row {
@@ -263,12 +300,10 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
     auto look = [&]() -> Row {
       Row r{0, 0, 0, false};
       if (px < x1) {
-        while (px >= cum[pb + 1]) {
-          ++pb;
-          pn = (int)a.lens[pb];
-        }
-        const int f = first_row(pn, a.window);
-        const int t = (f / kKeys + (px - cum[pb])) * kKeys + lane;
+        while (px >= cum[pb + 1].x) ++pb;
+        const int2 at = cum[pb];
+        const int pn = at.y, f = first_row(pn, a.window);
+        const int t = (f / kKeys + (px - at.x)) * kKeys + lane;
         r.b = pb;
         r.seen = t >= f && t < pn;
         if (r.seen) {
@@ -319,37 +354,27 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
 
     // ---- the row pieces of this lane --------------------------------------------------------------
     int buf = 0, x = x0;
-    int b = find_request(cum, a.batch, x0);
     while (x < x1) {
-      while (x >= cum[b + 1]) ++b;
-      const int n = (int)a.lens[b];
+      const int first = cum[b].x, last = cum[b + 1].x;         // the request's steps
+      const int n = cum[b].y;
       const int f = first_row(n, a.window);
-      const int row_end = min(x1, cum[b + 1]);
-      const bool starts = x == cum[b], ends = row_end == cum[b + 1];
+      const int row_end = min(x1, last);
+      const bool starts = x == first, ends = row_end == last;
       if (unit == 0 && lane == 0) {                 // (one warp of the lane speaks for all)
-        if (!a.by_lane && starts) a.span[b] = make_int2(li, ends ? li : lane_of(cum[b + 1] - 1, T, N));
-        if (a.by_lane && row_end == x1) a.span[li] = make_int2(b, starts && !ends ? lane_of(cum[b + 1] - 1, T, N) : -1);
+        if (!a.by_lane && starts) a.span[b] = make_int2(li, ends ? li : lane_of(last - 1, T, N));
+        if (a.by_lane && row_end == x1) a.span[li] = make_int2(b, starts && !ends ? lane_of(last - 1, T, N) : -1);
       }
-      // B fragments of the query rows (head 8 nt + gq of the tile): elements 2 tq, +1 and 8 + 2 tq, +1 of
-      // every 16, or 4 tq .. 4 tq + 3 where the K fragments come from bytes
+      // the query rows as B fragments, fp16 where the pool is e4m3
       uint32_t qb[NT][KS][2];
-      float qs[NT];                                 // what the row of head 8 nt + gq was divided by
+      float sc[NT][2];                              // score factors of heads 2 tq, 2 tq + 1 of each tile
+      if (NT > 1) load_q(b, qn);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int hl = (tile * NT + nt) * 8 + gq;
-        const bool live = hl < a.G;
-        const uint32_t* qrow = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
-                                                                 (int64_t)b * a.q_stride +
-                                                                 (int64_t)(live ? g * a.G + hl : 0) * D);
-        qs[nt] = 1.f;
 #pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          const int e0 = KIND == kE4m3 ? 2 * tq : tq, e1 = KIND == kE4m3 ? 2 * tq + 1 : 4 + tq;
-          qb[nt][c][0] = live ? __ldg(qrow + 8 * c + e0) : 0u;
-          qb[nt][c][1] = live ? __ldg(qrow + 8 * c + e1) : 0u;
-        }
+        for (int c = 0; c < KS; ++c) qb[nt][c][0] = qn[nt][c][0], qb[nt][c][1] = qn[nt][c][1];
+        sc[nt][0] = sc[nt][1] = ksc;
         if constexpr (KIND == kE4m3) {
-          // bf16 queries to fp16: the row divided by the power of two at its largest value
+          // bf16 queries: the row divided by the power of two at its largest value
           if (!a.out_f16) {
             float mx = 0.f;
 #pragma unroll
@@ -361,8 +386,9 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             // powers 2^-100 .. 2^100 keep both the factor and its inverse normal
             const int ex = min(100, max(-100, (int)((__float_as_uint(mx) >> 23) & 0xff) - 127));
-            qs[nt] = __uint_as_float((uint32_t)(ex + 127) << 23);
-            const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+            const float by = __uint_as_float((uint32_t)(ex + 127) << 23), inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sc[nt][e] *= __shfl_sync(0xffffffffu, by, (2 * tq + e) * 4);
 #pragma unroll
             for (int c = 0; c < KS; ++c)
 #pragma unroll
@@ -374,20 +400,11 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
           }
         }
       }
-      // per accumulator column (heads 2 tq, 2 tq + 1 of each tile): score factor and bias slope
-      // (base 2, but for capped scores, which get it with the cap)
-      const float ksc = a.scale * (a.k_scale != nullptr ? a.k_scale[g] : 1.f) * (a.softcap != 0.f ? 1.f : kLog2e);
-      const float cap2 = a.softcap * kLog2e, icap = a.softcap != 0.f ? 1.f / a.softcap : 0.f;
-      float sc[NT][2], sl[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int hl = (tile * NT + nt) * 8 + 2 * tq + e;
-          sc[nt][e] = ksc * (KIND == kE4m3 ? __shfl_sync(0xffffffffu, qs[nt], (2 * tq + e) * 4) : 1.f);
-          sl[nt][e] = a.slopes != nullptr && hl < a.G ? a.slopes[g * a.G + hl] * kLog2e : 0.f;
-        }
-      const bool plain = a.softcap == 0.f && a.slopes == nullptr;
+      const int now = b;
+      if (ends) {                                   // on to the next request with a row; its queries are fetched by then
+        do ++b; while (b < a.batch && cum[b + 1].x == last);
+        if (NT == 1 && row_end < x1) load_q(b, qn);
+      }
       bool fresh = true;                            // one of this lane's heads has no offset yet
       float o[KS][NT][4], l[NT][2], m[NT][2], mo[NT][2];   // mo: the offset taken off, 0 while there is none
 #pragma unroll
@@ -446,7 +463,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
             }
         }
         if (!plain) {                               // capped and biased scores, in base 2
-          const int t0 = (f / kKeys + (x - cum[b])) * kKeys + gq - (n - 1);
+          const int t0 = (f / kKeys + (x - first)) * kKeys + gq - (n - 1);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -582,30 +599,40 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       // d of accumulator element e of slice c: rows gq and gq + 8 of the slice, or 2 gq and 2 gq + 1 from bytes
       const int d0 = KIND == kE4m3 ? 2 * gq : gq, d1 = KIND == kE4m3 ? 2 * gq + 1 : gq + 8;
       if (starts && ends) {
-        const float vsc = a.v_scale != nullptr ? a.v_scale[g] : 1.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float inv[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            inv[e] = l[nt][e] == 0.f ? 0.f : vsc / l[nt][e];
             const int hl = (tile * NT + nt) * 8 + 2 * tq + e;
-            if (hl >= a.G) continue;
-            const int64_t oh = (int64_t)b * a.h_q + g * a.G + hl;
-            const float inv = l[nt][e] == 0.f ? 0.f : vsc / l[nt][e];
-#pragma unroll
-            for (int c = 0; c < KS; ++c) {
-              const float y0 = o[c][nt][e] * inv, y1 = o[c][nt][e + 2] * inv;
-              if (a.out_f16) {
-                __half* orow = static_cast<__half*>(a.o) + oh * D + 16 * c;
-                orow[d0] = __float2half_rn(y0);
-                orow[d1] = __float2half_rn(y1);
-              } else {
-                __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + oh * D + 16 * c;
-                orow[d0] = __float2bfloat16_rn(y0);
-                orow[d1] = __float2bfloat16_rn(y1);
-              }
-            }
-            if (a.lse != nullptr && gq == 0) a.lse[oh] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
+            if (a.lse != nullptr && gq == 0 && hl < a.G)
+              a.lse[(int64_t)now * a.h_q + g * a.G + hl] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
           }
+          // transposed back, a lane holds consecutive d of one head: 2 tq, +1 of both halves of a slice, or 4 tq .. + 3
+          const int hl = (tile * NT + nt) * 8 + gq;
+          uint32_t* orow = static_cast<uint32_t*>(a.o) + ((int64_t)now * a.h_q + g * a.G + hl) * (D / 2);
+          auto pack = [&](float u, float v) -> uint32_t {
+            if (a.out_f16) {
+              const __half2 y = __floats2half2_rn(u, v);
+              return *reinterpret_cast<const uint32_t*>(&y);
+            }
+            const __nv_bfloat162 y = __floats2bfloat162_rn(u, v);
+            return *reinterpret_cast<const uint32_t*>(&y);
+          };
+#pragma unroll
+          for (int c = 0; c < KS; ++c) {
+            const uint32_t y0 = transpose8x8(pack(o[c][nt][0] * inv[0], o[c][nt][1] * inv[1]));
+            const uint32_t y1 = transpose8x8(pack(o[c][nt][2] * inv[0], o[c][nt][3] * inv[1]));
+            if (hl >= a.G) continue;
+            if constexpr (KIND == kE4m3) {
+              *reinterpret_cast<uint2*>(orow + 8 * c + 2 * tq) = make_uint2(__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632));
+            } else {
+              orow[8 * c + tq] = y0;
+              orow[8 * c + 4 + tq] = y1;
+            }
+          }
+        }
       } else {
         const int64_t row = (int64_t)(2 * li + (starts ? 1 : 0)) * heads_pad + unit * 8 * NT;
 #pragma unroll
