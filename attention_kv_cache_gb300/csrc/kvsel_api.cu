@@ -352,7 +352,7 @@ using namespace kvsel;
 // ============================================================================= C ABI
 extern "C" {
 
-const char* kvsel_version(void) { return "kvsel 0.2 (sm_103a)"; }
+const char* kvsel_version(void) { return "kvsel 0.3 (sm_103a)"; }
 
 const char* kvsel_status_string(kvsel_status s) {
   switch (s) {
