@@ -57,7 +57,7 @@ kvsel_status launch_page_assign(const AssignArgs& a, cudaStream_t s);
 // ---- rope_append.cu ----------------------------------------------------------------------
 struct RopeArgs {
   int32_t h_q, h_kv, d, P, rot, e4m3;
-  int32_t unit_rows;    // head rows of a unit (set by the launcher)
+  int32_t unit_rows, stage_bytes, stages;   // head rows of a unit, a warp's ring (set by the launcher)
   int64_t share, extra; // units of every warp, and warps with one more (set by the launcher)
   int64_t n, n_slots, page_stride, head_stride, row_stride;
   int64_t q_stride, q_head, k_stride, k_head, v_stride, v_head;

@@ -5,10 +5,10 @@
 //
 // The angle is formed in turns as a 64-bit fraction: inv_freq / (2 pi) as a multiple of 2^-64 times the
 // position, modulo 2^64, is the fraction of a turn exactly up to position * 2^-65, so a far position loses
-// nothing that a 32-bit product of position and frequency would lose; the top 32 bits go to sincospif.
+// nothing that a 32-bit product of position and frequency would lose.
 //
-// One pass over the data, by single warps: a unit is up to kStageBytes of a token's query, key or value rows.  Every
-// warp has an equal share of all units; its units come by bulk copies into a ring of kStages stages (one copy where the rows are contiguous), are
+// One pass over the data, by single warps: a unit is up to kUnitBytes of a token's query, key or value rows.  Every
+// warp has an equal share of all units; its units come by bulk copies into a ring of stages (one copy where the rows are contiguous), are
 // normed and turned where they lie, and go out by bulk copies from there; 16-bit value rows go through untouched.
 // A row is d / 16 lanes of 16 elements, chosen so that both elements of a pair lie in one lane (elements 8 j .. and
 // rot / 2 + 8 j .. of a half layout, 16 j .. of an interleaved one), and the lanes of a row sum its squares by shuffles.
@@ -19,15 +19,18 @@
 //     every row: (a, b) -> r (A a - B b, C b + D a) with A = w_a cos, B = w_b sin, C = w_b cos, D = w_a sin and r
 //     the row's norm;
 //   - two pairs share an instruction (packed fp32);
-//   - frequencies in turns are formed once per CTA (64-bit floating point is slow on this GPU).
+//   - frequencies in turns are formed once per CTA (64-bit floating point is slow on this GPU), a token's slot and
+//     position are read a token ahead.
 //
-// Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 39 us (202 MB, 5.2 TB/s; the copies
-// without the arithmetic 35 us); 32768 tokens of 64 + 8 + 8 heads into e4m3, 222 us (1276 MB, 5.8 TB/s; copies alone
-// 205 us); one token 4.7 us.  With rows in registers instead (steps of 4 rows, 16 warps per SM): 52 and 288 us.
+// Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 38 us (202 MB, 5.3 TB/s; the copies
+// without the arithmetic 35 us); 32768 tokens of 64 + 8 + 8 heads into e4m3, 211 us (1276 MB, 6.0 TB/s; copies alone
+// 205 us); one token 4.5 us.  With rows in registers instead (steps of 4 rows, 16 warps per SM): 52 and 288 us.  Few
+// heads leave little to a unit: 8200 tokens of 8 + 1 + 1 heads take 21 us, issue-bound (42 MB, 2.0 TB/s).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -35,10 +38,11 @@
 namespace kvsel {
 namespace {
 
-constexpr int kWarps = 5;             // per CTA
+constexpr int kWarps = 5;              // per CTA
 constexpr int kRopeThreads = 32 * kWarps;
-constexpr int kStages = 3;            // per warp: one loading, one turned, one leaving
-constexpr int kStageBytes = 4096;
+constexpr int kUnitBytes = 4096;       // of a unit at most
+constexpr int kRingBytes = 3 * kUnitBytes;   // of a warp's stages: three of that, or up to kMaxStages of smaller ones
+constexpr int kMaxStages = 12;
 
 template <typename T>
 struct Pair;
@@ -122,12 +126,12 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float* f) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// Shared memory, in this order: the warps' stages, the warps' matrices of a token's pairs ([2 kinds][8][chunks] float4:
+// Shared memory, in this order: the warps' stages, the warps' matrices of a token's pairs ([2 kinds][8][chunks + 1] float4:
 // entry 2 m of chunk j holds (A, -B) of its pairs 2 m and 2 m + 1, entry 2 m + 1 holds (C, D)), weights [2][d], turns
 // [rot / 2], the stages' barriers.
 __host__ __device__ inline size_t rope_smem(int d, int rot) {
-  return (size_t)kWarps * (kStages * kStageBytes + 2 * 8 * (d / 16) * 16) + (size_t)2 * d * 4 + (size_t)rot / 2 * 8 +
-         (size_t)kWarps * kStages * 8;
+  return (size_t)kWarps * (kRingBytes + 2 * 8 * (d / 16 + 1) * 16) + (size_t)2 * d * 4 + (size_t)rot / 2 * 8 +
+         (size_t)kWarps * kMaxStages * 8;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -140,16 +144,16 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 
 // GROUP: lanes of a head row (the power of two >= d / 16), or 0: found at run time.
 template <typename T, bool HALF, int GROUP>
-__global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_constant__ RopeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  const int chunks = a.d / 16, pairs = a.rot / 2;
+  const int chunks = a.d / 16, pitch = chunks + 1, pairs = a.rot / 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint8_t* stages = smem + (size_t)warp * kStages * kStageBytes;
-  uint8_t* after = smem + (size_t)kWarps * kStages * kStageBytes;
-  float4* mats = reinterpret_cast<float4*>(after) + warp * 2 * 8 * chunks;
-  float* wts = reinterpret_cast<float*>(after + (size_t)kWarps * 2 * 8 * chunks * 16);
+  uint8_t* stages = smem + (size_t)warp * kRingBytes;
+  uint8_t* after = smem + (size_t)kWarps * kRingBytes;
+  float4* mats = reinterpret_cast<float4*>(after) + warp * 2 * 8 * pitch;
+  float* wts = reinterpret_cast<float*>(after + (size_t)kWarps * 2 * 8 * pitch * 16);
   int64_t* turns = reinterpret_cast<int64_t*>(wts + 2 * a.d);
-  const uint32_t bar0 = sm100::smem_addr(turns + pairs) + warp * kStages * 8;
+  const uint32_t bar0 = sm100::smem_addr(turns + pairs) + warp * kMaxStages * 8;
   const uint32_t st0 = sm100::smem_addr(stages);
   int group = GROUP;
   if (GROUP == 0)
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
   const int o0 = HALF && rotate ? 8 * j : 16 * j, o1 = HALF && rotate ? pairs + 8 * j : 16 * j + 8;
 
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) sm100::mbar_init(bar0 + 8 * i, 1);
+    for (int i = 0; i < a.stages; ++i) sm100::mbar_init(bar0 + 8 * i, 1);
     sm100::fence_barrier_init();
   }
   __syncwarp();
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
   int i = (first >> 31) == 0 ? (int)first / total : (int)(first / total);   // (a 32-bit division where it will do)
   int u = (int)(first - (int64_t)i * total);
 
-  // ---- the units' loads, kStages - 1 ahead
+  // ---- the units' loads, a.stages - 2 ahead: the stage between them is the one whose rows are leaving
   int64_t lleft = left;
   int li = i, lu = u, lst = 0;                                // next unit to load, its stage
   auto load = [&]() {
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
     const int64_t ts = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
     const int64_t hs = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
     const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + li * ts + h0 * hs;
-    const uint32_t dst = st0 + lst * kStageBytes, bar = bar0 + 8 * lst;
+    const uint32_t dst = st0 + lst * a.stage_bytes, bar = bar0 + 8 * lst;
     if (lane == 0) sm100::mbar_expect_tx(bar, n * row_bytes);
     if (hs == a.d) {
       if (lane == 0) bulk_load(dst, src, n * row_bytes, bar);
@@ -201,14 +205,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
       __syncwarp();
       for (int h = lane; h < n; h += 32) bulk_load(dst + h * row_bytes, src + h * hs, row_bytes, bar);
     }
-    lst = lst == kStages - 1 ? 0 : lst + 1;
+    lst = lst == a.stages - 1 ? 0 : lst + 1;
     if (++lu == total) {
       lu = 0;
       ++li;
     }
   };
-#pragma unroll
-  for (int e = 0; e < kStages - 1; ++e) load();
+  for (int e = 0; e < a.stages - 2; ++e) load();
 
   // ---- what all tokens share, while those land
   for (int x = threadIdx.x; x < 2 * a.d; x += kRopeThreads) {
@@ -226,8 +229,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
   for (int x = lane; x < 2 * 8 * (chunks - a.rot / 16); x += 32) {
     const int kind = x / (8 * (chunks - a.rot / 16)), y = x % (8 * (chunks - a.rot / 16));
     const int c = a.rot / 16 + y / 8, p = y % 8;
-    float* ab = reinterpret_cast<float*>(mats + (kind * 8 + p / 2 * 2) * chunks + c) + (p & 1);
-    float* cd = reinterpret_cast<float*>(mats + (kind * 8 + p / 2 * 2 + 1) * chunks + c) + (p & 1);
+    float* ab = reinterpret_cast<float*>(mats + (kind * 8 + p / 2 * 2) * pitch + c) + (p & 1);
+    float* cd = reinterpret_cast<float*>(mats + (kind * 8 + p / 2 * 2 + 1) * pitch + c) + (p & 1);
     ab[0] = wts[kind * a.d + 16 * c + (HALF ? p : 2 * p)];
     cd[0] = wts[kind * a.d + 16 * c + (HALF ? 8 + p : 2 * p + 1)];
     ab[2] = cd[2] = 0.f;
@@ -235,8 +238,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
 
 
   int st = 0, phase = 0;
+  int64_t next_slot = 0, next_pos = 0;                          // of the next token, read while this one is worked on
+  auto look = [&](int token) {
+    next_slot = a.slots != nullptr ? a.slots[token] : 0;
+    next_pos = pairs > 0 ? a.positions[token] : 0;
+  };
+  if (left > 0) look(i);
   while (left > 0) {
-    const int64_t slot = a.slots != nullptr ? a.slots[i] : 0, pos = pairs > 0 ? a.positions[i] : 0;
+    const int64_t slot = next_slot, pos = next_pos;
+    if (left > total - u) look(i + 1);
     const bool cached = slot >= 0 && slot < a.n_slots;
     if (a.k != nullptr && !cached && slot != -1 && lane == 0 && u == 0) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)i);
     int64_t at = 0;                                             // of the slot in the pool
@@ -250,7 +260,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
         float sn[2], cs[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sincospif((float)(int32_t)((turns[2 * c + e] * pos) >> 32) * 4.656612873077393e-10f, &sn[e], &cs[e]);
+          // the turn's top 32 bits as an angle in [-pi, pi), where the fast sine and cosine are within 2^-21
+          __sincosf((float)(int32_t)((turns[2 * c + e] * pos) >> 32) * 1.4629180792671596e-9f, &sn[e], &cs[e]);
           sn[e] *= a.factor;
           cs[e] *= a.factor;
         }
@@ -266,9 +277,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
             wa = make_float2(v.x, v.z);
             wb = make_float2(v.y, v.w);
           }
-          float4* to = mats + (kind * 8 + c % 4 * 2) * chunks + c / 4;
+          float4* to = mats + (kind * 8 + c % 4 * 2) * pitch + c / 4;
           to[0] = make_float4(wa.x * cs[0], wa.y * cs[1], -(wb.x * sn[0]), -(wb.y * sn[1]));
-          to[chunks] = make_float4(wb.x * cs[0], wb.y * cs[1], wa.x * sn[0], wa.y * sn[1]);
+          to[pitch] = make_float4(wb.x * cs[0], wb.y * cs[1], wa.x * sn[0], wa.y * sn[1]);
         }
       }
       __syncwarp();
@@ -276,35 +287,35 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
     for (; u < total && left > 0; ++u, --left) {
       int kind, h0, n;
       unit(u, kind, h0, n);
-      // the unit two ahead goes into the stage stored last: its bytes have left before it is written again
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      // the next load goes into the stage stored before the last one: its bytes have left
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       __syncwarp();
       load();
       if (!__all_sync(0xffffffffu, sm100::mbar_wait(bar0 + 8 * st, phase))) {
         // the copies in flight land (or their own wait runs out) before the warp leaves
         if (lane == 0) set_device_error(a.err, KVSEL_ERR_TIMEOUT, 6u);
-        for (int e = 1; e < kStages; ++e) {
-          const int x = (st + e) % kStages;
-          if (x != lst) sm100::mbar_wait(bar0 + 8 * x, phase ^ (x < st ? 1 : 0));
-        }
+        for (int x = st + 1 < a.stages ? st + 1 : 0; x != lst; x = x + 1 < a.stages ? x + 1 : 0)
+          sm100::mbar_wait(bar0 + 8 * x, phase ^ (x < st ? 1 : 0));
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         return;
       }
       const bool e8 = kind > 0 && a.e4m3;
-      uint8_t* stage = stages + st * kStageBytes;
+      uint8_t* stage = stages + st * a.stage_bytes;
       const bool skip = slot == -1 || (kind > 0 && !cached);
       if (!skip && (kind < 2 || e8)) {
         const bool norm = kind < 2 && (kind == 0 ? a.q_weight : a.k_weight) != nullptr;
-        const float4* mt = mats + kind * 8 * chunks + j;
-        // two rows of every lane at once: their sums and shuffles overlap, and they share the matrices' reads
-        for (int hb = sub; hb - sub < n; hb += 2 * rows) {
-          bool on[2];
-          float scale[2] = {1.f, 1.f};
-          F2 x[2][4], y[2][4];
+        const float4* mt = mats + kind * 8 * pitch + j;
+        // R rows of every lane at once, hb and on: their sums and shuffles overlap, and they share the matrices' reads
+        auto turn = [&](auto r_const, int hb) {
+          constexpr int R = decltype(r_const)::value;
+          bool on[R];
+          float scale[R];
+          F2 x[R][4], y[R][4];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < R; ++t) {
             const int h = hb + t * rows;
             on[t] = live && h < n;
+            scale[t] = 1.f;
             uint4 r[2];
             r[0] = r[1] = make_uint4(0, 0, 0, 0);
             if (on[t]) {
@@ -315,9 +326,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
             unpack16<T, HALF>(r, x[t], y[t]);
           }
           if (norm) {
-            float ss[2];
+            float ss[R];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < R; ++t) {
               F2 s2 = mul(x[t][0], x[t][0]), t2 = mul(y[t][0], y[t][0]);
 #pragma unroll
               for (int m = 1; m < 4; ++m) {
@@ -331,21 +342,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
 #pragma unroll
               for (int o = GROUP / 2; o > 0; o >>= 1)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
+                for (int t = 0; t < R; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
             } else {
               for (int o = group >> 1; o > 0; o >>= 1)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
+                for (int t = 0; t < R; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
             }
 #pragma unroll
-            for (int t = 0; t < 2; ++t) scale[t] *= rsqrtf(fmaf(ss[t], inv_d, a.eps));
+            for (int t = 0; t < R; ++t) scale[t] *= rsqrtf(fmaf(ss[t], inv_d, a.eps));
           }
           if (kind < 2 && live) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              const float4 ab = mt[2 * m * chunks], cd = mt[(2 * m + 1) * chunks];
+              const float4 ab = mt[2 * m * pitch], cd = mt[(2 * m + 1) * pitch];
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
+              for (int t = 0; t < R; ++t) {
                 const F2 p = x[t][m], q = y[t][m];
                 x[t][m] = mul(p, f2(ab.x, ab.y));
                 y[t][m] = mul(q, f2(cd.x, cd.y));
@@ -358,7 +369,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
           }
           if (e8) __syncwarp();                                 // a row's bytes lie over its lanes' values
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < R; ++t) {
             const F2 s2 = f2(scale[t], scale[t]);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -377,12 +388,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
               *reinterpret_cast<uint4*>(row + 2 * o1) = pack8<T>(f + 8);
             }
           }
-        }
+        };
+        int hb = sub;
+        for (; hb - sub + rows < n; hb += 2 * rows) turn(std::integral_constant<int, 2>(), hb);
+        if (hb - sub < n) turn(std::integral_constant<int, 1>(), hb);
       }
       sm100::fence_proxy_async_smem();
       __syncwarp();
       if (!skip) {
-        const uint32_t src = st0 + st * kStageBytes;
+        const uint32_t src = st0 + st * a.stage_bytes;
         if (kind == 0) {
           if (lane == 0) bulk_store(static_cast<T*>(a.q_out) + ((int64_t)i * a.h_q + h0) * a.d, src, n * row_bytes);
         } else {
@@ -396,7 +410,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append(const __grid_constan
         }
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      if (++st == kStages) {
+      if (++st == a.stages) {
         st = 0;
         phase ^= 1;
       }
@@ -414,8 +428,11 @@ kvsel_status launch_rope_append(const RopeArgs& in, int32_t dtype, int32_t layou
   RopeArgs a = in;
   int group = 1;
   while (group < a.d / 16) group <<= 1;
-  const int rows = 32 / group, fit = kStageBytes / (2 * a.d);
+  const int rows = 32 / group, fit = kUnitBytes / (2 * a.d);
   a.unit_rows = fit >= rows ? fit / rows * rows : fit;
+  const int most = std::min(a.unit_rows, std::max(a.q != nullptr ? a.h_q : 0, a.k != nullptr ? a.h_kv : 0));
+  a.stage_bytes = most * 2 * a.d;
+  a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
   const bool half = layout == KVSEL_ROPE_HALF;
   auto pick = [&](auto t) -> Kernel {
     using T = decltype(t);

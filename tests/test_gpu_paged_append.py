@@ -2,8 +2,8 @@
 
 Tolerances (u = 2^-24).  With a norm the mean square of d values is off by (16 + log2 d) u relative, its root's
 reciprocal by half of that and 2 u of rsqrtf, the scaled value by 3 u more: under 2^-19 relative.  cos and sin are
-off by 2^-32 of a turn, the rounding of the angle in turns to fp32 (u / 2 of a half turn at most), sincospif's own
-2 ulp, and the factor's product: under 2^-21; a turned value is two such products.  With size = factor (|a| + |b|) of
+off by 2^-32 of a turn, the rounding of the angle to fp32 (at most pi u < 2^-22) and the fast functions' 2^-21:
+under 2^-20; a turned value is two such products.  With size = factor (|a| + |b|) of
 its pair, |y - ref| <= 2^-18 size before the rounding to the output's type, which adds eps / 2 |y| (and half a step
 of the type's smallest numbers).  Values that pass unturned without a norm, and the v rows of a 16-bit pool, are
 exact.
