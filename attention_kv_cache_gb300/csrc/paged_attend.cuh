@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
           const int e0 = KIND == kE4m3 ? 2 * tq : tq, e1 = KIND == kE4m3 ? 2 * tq + 1 : 4 + tq;
-          to[nt][c][0] = live ? __ldg(qrow + 8 * c + e0) : 0u;
-          to[nt][c][1] = live ? __ldg(qrow + 8 * c + e1) : 0u;
+          to[nt][c][0] = live ? qrow[8 * c + e0] : 0u;
+          to[nt][c][1] = live ? qrow[8 * c + e1] : 0u;
         }
       }
     };
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
         if (r.seen) {
           const int blk = (int)((__umulhi(a.p_mul, (uint32_t)t) + (uint32_t)t) >> a.p_shift);   // t / P
           r.within = t - blk * a.P;
-          r.id = __ldg(a.tables + (int64_t)pb * a.max_blocks + blk);
+          r.id = a.tables[(int64_t)pb * a.max_blocks + blk];
         }
         ++px;
       }

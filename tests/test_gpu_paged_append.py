@@ -121,11 +121,24 @@ class Case:
     dict(n=20, d=64, h_q=3, h_kv=3, scaling="linear"), dict(n=20, d=80, rot=80), dict(n=20, d=96, rot=48, dtype="f16"),
     dict(n=20, d=112, layout="interleaved"), dict(n=20, d=256, cache="e4m3"), dict(n=20, d=256, layout="interleaved"),
     dict(n=20, d=32, h_q=33, h_kv=11), dict(n=40, fused=False), dict(n=40, bias=1.0), dict(n=50, pos_max=2 ** 31),
-    dict(n=3000, h_q=32, h_kv=8), dict(n=3001, h_q=16, h_kv=1, d=64, dtype="f16", layout="interleaved", rot=16),
+    dict(n=3000, h_q=32, h_kv=8), dict(n=5, h_q=600, h_kv=300), dict(n=700, h_q=1, h_kv=1, pad=99),
+    dict(n=100, h_q=5, h_kv=1, cache="e4m3", d=48, rot=48), dict(n=3001, h_q=16, h_kv=1, d=64, dtype="f16", layout="interleaved", rot=16),
 ], ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
 def test_rows(cuda, kw):
     from attention_kv_cache_gb300 import kvsel as K
     Case(K, cuda, **kw).run().check()
+
+
+def test_broadcast_heads_and_tokens(cuda):
+    """Strides of zero: one row for every head, one token's rows for every token."""
+    from attention_kv_cache_gb300 import kvsel as K
+    c = Case(K, cuda, 50, h_q=4, h_kv=4)
+    c.k = c.k[:, :1].expand(-1, 4, -1)
+    c.v = c.v[:1].expand(50, -1, -1)
+    c.rope.k_head_stride, c.rope.v_stride = c.k.stride(1), c.v.stride(0)
+    assert c.rope.k_head_stride == 0 and c.rope.v_stride == 0
+    c.in_h[1:] = [C.f64(c.k), C.f64(c.v)]
+    c.run().check()
 
 
 def test_far_positions_lose_nothing(cuda):

@@ -124,6 +124,9 @@ SHAPES = [
     dict(lens=[64] * 40 + [0] + [2000], h_kv=8, G=1, P=16),       # more requests than some lanes
     dict(lens=list(range(0, 200)), h_kv=5, G=2, d=64),             # more requests than lanes
     dict(lens=list(range(1, 300)), h_kv=8, G=16, d=64, P=32, dtype="f16"),
+    dict(lens=[40, 0, 70], h_kv=1300, G=1, d=64),                  # more KV heads than warps
+    dict(lens=[i % 37 for i in range(4096)], h_kv=1, G=2, d=64, P=8),
+    dict(lens=[i % 5 for i in range(4095)] + [700], h_kv=1, G=1, P=16, cache="e4m3"),
 ]
 
 
