@@ -58,7 +58,8 @@ kvsel_status launch_page_assign(const AssignArgs& a, cudaStream_t s);
 struct RopeArgs {
   int32_t h_q, h_kv, d, P, rot, e4m3;
   int32_t unit_rows, stage_bytes, stages;   // head rows of a unit, a warp's ring (set by the launcher)
-  int64_t share, extra; // units of every warp, and warps with one more (set by the launcher)
+  int32_t rounds;       // whole tokens of every warp; then its units of the rest, and the warps with one more (the same)
+  int64_t share, extra;
   int64_t n, n_slots, page_stride, head_stride, row_stride;
   int64_t q_stride, q_head, k_stride, k_head, v_stride, v_head;
   float factor, eps, bias;

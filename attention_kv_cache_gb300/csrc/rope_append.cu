@@ -7,7 +7,8 @@
 // position, modulo 2^64, is the fraction of a turn exactly up to position * 2^-65, so a far position loses
 // nothing that a 32-bit product of position and frequency would lose.
 //
-// One pass over the data, by single warps: a unit is up to kUnitBytes of a token's query, key or value rows.  Every
+// One pass over the data, by single warps: a unit is up to kUnitBytes of a token's rows, queries,
+// keys and values end to end.  Every
 // warp has an equal share of all units; its units come by bulk copies into a ring of stages (one copy where the rows are contiguous), are
 // normed and turned where they lie, and go out by bulk copies from there; 16-bit value rows go through untouched.
 // A row is d / 16 lanes of 16 elements, chosen so that both elements of a pair lie in one lane (elements 8 j .. and
@@ -19,13 +20,15 @@
 //     every row: (a, b) -> r (A a - B b, C b + D a) with A = w_a cos, B = w_b sin, C = w_b cos, D = w_a sin and r
 //     the row's norm;
 //   - two pairs share an instruction (packed fp32);
+//   - units of queries alone share the matrices' reads between rows (32768 tokens 227 -> 219 us);
 //   - frequencies in turns are formed once per CTA (64-bit floating point is slow on this GPU), a token's slot and
 //     position are read a token ahead.
 //
-// Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 38 us (202 MB, 5.3 TB/s; the copies
-// without the arithmetic 35 us); 32768 tokens of 64 + 8 + 8 heads into e4m3, 211 us (1276 MB, 6.0 TB/s; copies alone
+// Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 37.5 us (202 MB, 5.4 TB/s; the copies
+// without the arithmetic 35 us); 32768 tokens of 64 + 8 + 8 heads into e4m3, 214 us (1276 MB, 6.0 TB/s; copies alone
 // 205 us); one token 4.5 us.  With rows in registers instead (steps of 4 rows, 16 warps per SM): 52 and 288 us.  Few
-// heads leave little to a unit: 8200 tokens of 8 + 1 + 1 heads take 21 us, issue-bound (42 MB, 2.0 TB/s).
+// heads leave little to a unit: 8200 tokens of 8 + 1 + 1 heads take 18 us (42 MB, 2.3 TB/s; with a unit for each kind of
+// row 21 us).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -170,45 +173,49 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
   wait_for_earlier_kernels();
   const float inv_d = 1.f / (float)a.d;
   const int row_bytes = a.d * 2;
-  const int iq = a.q != nullptr ? (a.h_q + a.unit_rows - 1) / a.unit_rows : 0;
-  const int ik = a.k != nullptr ? (a.h_kv + a.unit_rows - 1) / a.unit_rows : 0;
-  const int total = iq + 2 * ik;
-  // kind (query, key, value rows), first row and rows of unit u
-  auto unit = [&](int u, int& kind, int& h0, int& n) {
-    kind = u < iq ? 0 : u < iq + ik ? 1 : 2;
-    h0 = (u - (kind == 0 ? 0 : kind == 1 ? iq : iq + ik)) * a.unit_rows;
-    n = min(a.unit_rows, (kind == 0 ? a.h_q : a.h_kv) - h0);
-  };
-  // this warp's share of all tokens' units, laid end to end: from unit u of token i, `left` of them
-  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t first = a.share * w + min(w, a.extra);
-  int64_t left = a.share + (w < a.extra ? 1 : 0);
-  int i = (first >> 31) == 0 ? (int)first / total : (int)(first / total);   // (a 32-bit division where it will do)
-  int u = (int)(first - (int64_t)i * total);
+  // a token's rows, end to end: queries from 0, keys from bk, values from bv, `all` in all; a unit is unit_rows of them
+  const int bk = a.q != nullptr ? a.h_q : 0, bv = bk + (a.k != nullptr ? a.h_kv : 0), all = bv + (a.k != nullptr ? a.h_kv : 0);
+  const int total = (all + a.unit_rows - 1) / a.unit_rows;
+  // This warp's units: a.rounds whole tokens, one in every n_w (so that all warps read and write near each other), then an
+  // equal share of the units of the tokens that remain, `left` in all.  (i, u) is a unit, r the tokens before it.
+  const int n_w = gridDim.x * kWarps, w = blockIdx.x * kWarps + warp;
+  const int64_t first = a.share * w + min((int64_t)w, a.extra);
+  const int rest_i = (first >> 31) == 0 ? (int)first / total : (int)(first / total);   // (a 32-bit division where it will do)
+  const int rest_u = (int)(first - (int64_t)rest_i * total);
+  int64_t left = (int64_t)a.rounds * total + a.share + (w < a.extra ? 1 : 0);
+  auto next_token = [&](int i, int r) { return r < a.rounds ? i + n_w : r == a.rounds ? a.rounds * n_w + rest_i : i + 1; };
+  int i = a.rounds > 0 ? w : rest_i, u = a.rounds > 0 ? 0 : rest_u, r = 0;
 
   // ---- the units' loads, a.stages - 2 ahead: the stage between them is the one whose rows are leaving
   int64_t lleft = left;
-  int li = i, lu = u, lst = 0;                                // next unit to load, its stage
+  int li = i, lu = u, lr = 0, lst = 0;                        // next unit to load, its stage
   auto load = [&]() {
     if (lleft == 0) return;
     --lleft;
-    int kind, h0, n;
-    unit(lu, kind, h0, n);
-    const int64_t ts = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
-    const int64_t hs = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
-    const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + li * ts + h0 * hs;
+    const int r0 = lu * a.unit_rows, r1 = min(r0 + a.unit_rows, all);
     const uint32_t dst = st0 + lst * a.stage_bytes, bar = bar0 + 8 * lst;
-    if (lane == 0) sm100::mbar_expect_tx(bar, n * row_bytes);
-    if (hs == a.d) {
-      if (lane == 0) bulk_load(dst, src, n * row_bytes, bar);
-    } else {
-      __syncwarp();
-      for (int h = lane; h < n; h += 32) bulk_load(dst + h * row_bytes, src + h * hs, row_bytes, bar);
-    }
+    if (lane == 0) sm100::mbar_expect_tx(bar, (r1 - r0) * row_bytes);
+    __syncwarp();
+    // rows lo .. hi - 1 of the unit, heads lo - base and on: one copy where they are contiguous
+    auto part = [&](const void* p, int64_t ts, int64_t hs, int base, int end) {
+      const int lo = max(r0, base), hi = min(r1, end);
+      if (lo >= hi) return;
+      const T* src = static_cast<const T*>(p) + li * ts + (lo - base) * hs;
+      const uint32_t to = dst + (lo - r0) * row_bytes;
+      if (hs == a.d) {
+        if (lane == 0) bulk_load(to, src, (hi - lo) * row_bytes, bar);
+      } else {
+        for (int h = lane; h < hi - lo; h += 32) bulk_load(to + h * row_bytes, src + h * hs, row_bytes, bar);
+      }
+    };
+    part(a.q, a.q_stride, a.q_head, 0, bk);
+    part(a.k, a.k_stride, a.k_head, bk, bv);
+    part(a.v, a.v_stride, a.v_head, bv, all);
     lst = lst == a.stages - 1 ? 0 : lst + 1;
     if (++lu == total) {
-      lu = 0;
-      ++li;
+      ++lr;
+      li = next_token(li, lr);
+      lu = lr == a.rounds ? rest_u : 0;
     }
   };
   for (int e = 0; e < a.stages - 2; ++e) load();
@@ -246,7 +253,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
   if (left > 0) look(i);
   while (left > 0) {
     const int64_t slot = next_slot, pos = next_pos;
-    if (left > total - u) look(i + 1);
+    if (left > total - u) look(next_token(i, r + 1));
     const bool cached = slot >= 0 && slot < a.n_slots;
     if (a.k != nullptr && !cached && slot != -1 && lane == 0 && u == 0) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)i);
     int64_t at = 0;                                             // of the slot in the pool
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
       const int64_t page = (slot >> 31) == 0 ? (int)slot / a.P : slot / a.P;
       at = page * a.page_stride + (slot - page * a.P) * a.row_stride;
     }
-    if (pairs > 0 && u < iq + ik && slot != -1) {
+    if (pairs > 0 && u * a.unit_rows < bv && slot != -1) {
       __syncwarp();                                             // the last token's matrices are read
       for (int c = lane; c < pairs / 2; c += 32) {              // pairs 2 c and 2 c + 1
         float sn[2], cs[2];
@@ -285,8 +292,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
       __syncwarp();
     }
     for (; u < total && left > 0; ++u, --left) {
-      int kind, h0, n;
-      unit(u, kind, h0, n);
+      const int r0 = u * a.unit_rows, r1 = min(r0 + a.unit_rows, all);
       // the next load goes into the stage stored before the last one: its bytes have left
       asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       __syncwarp();
@@ -299,33 +305,34 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         return;
       }
-      const bool e8 = kind > 0 && a.e4m3;
       uint8_t* stage = stages + st * a.stage_bytes;
-      const bool skip = slot == -1 || (kind > 0 && !cached);
-      if (!skip && (kind < 2 || e8)) {
-        const bool norm = kind < 2 && (kind == 0 ? a.q_weight : a.k_weight) != nullptr;
-        const float4* mt = mats + kind * 8 * pitch + j;
-        // R rows of every lane at once, hb and on: their sums and shuffles overlap, and they share the matrices' reads
-        auto turn = [&](auto r_const, int hb) {
+      if (slot != -1) {                                         // (else padding)
+        const int n = min(r1, a.e4m3 ? all : bv) - r0;          // 16-bit values go through as they are
+        // R rows of every lane at once, hb and on: their sums and shuffles overlap.  Units of queries alone, the most of
+        // them where there are many heads, share the matrices' reads and know no 8-bit rows.
+        auto turn = [&](auto r_const, auto q_const, int hb) {
           constexpr int R = decltype(r_const)::value;
+          constexpr bool Q = decltype(q_const)::value;
           bool on[R];
+          int kind[R];                                          // a query, key or value row
           float scale[R];
           F2 x[R][4], y[R][4];
 #pragma unroll
           for (int t = 0; t < R; ++t) {
             const int h = hb + t * rows;
             on[t] = live && h < n;
+            kind[t] = Q || r0 + h < bk ? 0 : r0 + h < bv ? 1 : 2;
             scale[t] = 1.f;
             uint4 r[2];
             r[0] = r[1] = make_uint4(0, 0, 0, 0);
             if (on[t]) {
               r[0] = *reinterpret_cast<const uint4*>(stage + h * row_bytes + 2 * o0);
               r[1] = *reinterpret_cast<const uint4*>(stage + h * row_bytes + 2 * o1);
-              if (e8) scale[t] = 1.f / (kind == 1 ? a.k_scale : a.v_scale)[h0 + h];
+              if (!Q && kind[t] > 0 && a.e4m3) scale[t] = 1.f / (kind[t] == 1 ? a.k_scale[r0 + h - bk] : a.v_scale[r0 + h - bv]);
             }
             unpack16<T, HALF>(r, x[t], y[t]);
           }
-          if (norm) {
+          if (a.q_weight != nullptr || (!Q && a.k_weight != nullptr)) {
             float ss[R];
 #pragma unroll
             for (int t = 0; t < R; ++t) {
@@ -349,25 +356,36 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
                 for (int t = 0; t < R; ++t) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
             }
 #pragma unroll
-            for (int t = 0; t < R; ++t) scale[t] *= rsqrtf(fmaf(ss[t], inv_d, a.eps));
+            for (int t = 0; t < R; ++t)
+              if (kind[t] < 2 && (kind[t] == 0 ? a.q_weight : a.k_weight) != nullptr) scale[t] *= rsqrtf(fmaf(ss[t], inv_d, a.eps));
           }
-          if (kind < 2 && live) {
+          auto apply = [&](int t, int m, float4 ab, float4 cd) {
+            const F2 p = x[t][m], q = y[t][m];
+            x[t][m] = mul(p, f2(ab.x, ab.y));
+            y[t][m] = mul(q, f2(cd.x, cd.y));
+            if (rotate) {
+              x[t][m] = fma(q, f2(ab.z, ab.w), x[t][m]);
+              y[t][m] = fma(p, f2(cd.z, cd.w), y[t][m]);
+            }
+          };
+          if (Q) {
+            if (live)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const float4 ab = mt[2 * m * pitch], cd = mt[(2 * m + 1) * pitch];
+              for (int m = 0; m < 4; ++m) {
+                const float4 ab = mats[2 * m * pitch + j], cd = mats[(2 * m + 1) * pitch + j];
 #pragma unroll
-              for (int t = 0; t < R; ++t) {
-                const F2 p = x[t][m], q = y[t][m];
-                x[t][m] = mul(p, f2(ab.x, ab.y));
-                y[t][m] = mul(q, f2(cd.x, cd.y));
-                if (rotate) {
-                  x[t][m] = fma(q, f2(ab.z, ab.w), x[t][m]);
-                  y[t][m] = fma(p, f2(cd.z, cd.w), y[t][m]);
-                }
+                for (int t = 0; t < R; ++t) apply(t, m, ab, cd);
               }
+          } else {
+#pragma unroll
+            for (int t = 0; t < R; ++t) {
+              const float4* mt = mats + kind[t] * 8 * pitch + j;
+              if (live && kind[t] < 2)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) apply(t, m, mt[2 * m * pitch], mt[(2 * m + 1) * pitch]);
             }
           }
-          if (e8) __syncwarp();                                 // a row's bytes lie over its lanes' values
+          if (!Q && a.e4m3) __syncwarp();                             // a row's bytes lie over its lanes' values
 #pragma unroll
           for (int t = 0; t < R; ++t) {
             const F2 s2 = f2(scale[t], scale[t]);
@@ -380,7 +398,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
             order16<HALF>(x[t], y[t], f);
             if (!on[t]) continue;
             uint8_t* row = stage + (hb + t * rows) * row_bytes;
-            if (e8) {
+            if (!Q && kind[t] > 0 && a.e4m3) {
               *reinterpret_cast<uint2*>(row + o0) = pack8_e4m3(f);
               *reinterpret_cast<uint2*>(row + o1) = pack8_e4m3(f + 8);
             } else {
@@ -389,25 +407,34 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
             }
           }
         };
-        int hb = sub;
-        for (; hb - sub + rows < n; hb += 2 * rows) turn(std::integral_constant<int, 2>(), hb);
-        if (hb - sub < n) turn(std::integral_constant<int, 1>(), hb);
+        auto turn_all = [&](auto q_const) {
+          int hb = sub;
+          for (; hb - sub + rows < n; hb += 2 * rows) turn(std::integral_constant<int, 2>(), q_const, hb);
+          if (hb - sub < n) turn(std::integral_constant<int, 1>(), q_const, hb);
+        };
+        if (r1 <= bk) turn_all(std::true_type());
+        else turn_all(std::false_type());
       }
       sm100::fence_proxy_async_smem();
       __syncwarp();
-      if (!skip) {
-        const uint32_t src = st0 + st * a.stage_bytes;
-        if (kind == 0) {
-          if (lane == 0) bulk_store(static_cast<T*>(a.q_out) + ((int64_t)i * a.h_q + h0) * a.d, src, n * row_bytes);
-        } else {
-          const int eb = e8 ? 1 : 2;
-          uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + (at + h0 * a.head_stride) * eb;
-          if (a.head_stride == a.d && !e8) {
-            if (lane == 0) bulk_store(dst, src, n * row_bytes);
+      if (slot != -1) {
+        const uint32_t from = st0 + st * a.stage_bytes;
+        const int hi = min(r1, bk);
+        if (r0 < hi && lane == 0) bulk_store(static_cast<T*>(a.q_out) + ((int64_t)i * a.h_q + r0) * a.d, from, (hi - r0) * row_bytes);
+        const int eb = a.e4m3 ? 1 : 2;
+        auto part = [&](void* pool, int base, int end) {
+          const int lo = max(r0, base), hi = min(r1, end);
+          if (lo >= hi || !cached) return;
+          uint8_t* dst = static_cast<uint8_t*>(pool) + (at + (lo - base) * a.head_stride) * eb;
+          const uint32_t src = from + (lo - r0) * row_bytes;
+          if (a.head_stride == a.d && !a.e4m3) {
+            if (lane == 0) bulk_store(dst, src, (hi - lo) * row_bytes);
           } else {
-            for (int h = lane; h < n; h += 32) bulk_store(dst + h * a.head_stride * eb, src + h * row_bytes, a.d * eb);
+            for (int h = lane; h < hi - lo; h += 32) bulk_store(dst + h * a.head_stride * eb, src + h * row_bytes, a.d * eb);
           }
-        }
+        };
+        part(a.k_cache, bk, bv);
+        part(a.v_cache, bv, all);
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       if (++st == a.stages) {
@@ -415,8 +442,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
         phase ^= 1;
       }
     }
-    u = 0;
-    ++i;
+    ++r;
+    i = next_token(i, r);
+    u = r == a.rounds ? rest_u : 0;
   }
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // written before the kernel ends
 }
@@ -428,10 +456,13 @@ kvsel_status launch_rope_append(const RopeArgs& in, int32_t dtype, int32_t layou
   RopeArgs a = in;
   int group = 1;
   while (group < a.d / 16) group <<= 1;
-  const int rows = 32 / group, fit = kUnitBytes / (2 * a.d);
-  a.unit_rows = fit >= rows ? fit / rows * rows : fit;
-  const int most = std::min(a.unit_rows, std::max(a.q != nullptr ? a.h_q : 0, a.k != nullptr ? a.h_kv : 0));
-  a.stage_bytes = most * 2 * a.d;
+  // units of equal size, whole steps of `rows` rows where there are several
+  const int rows = 32 / group, all = (a.q != nullptr ? a.h_q : 0) + (a.k != nullptr ? 2 * a.h_kv : 0);
+  const int fit = std::max(1, kUnitBytes / (2 * a.d) / rows) * rows;
+  const int each = (int)ceil_div(all, ceil_div(all, fit));
+  a.unit_rows = std::min(fit, (int)ceil_div(each, rows) * rows);
+  const int64_t units = ceil_div(all, a.unit_rows);
+  a.stage_bytes = std::min(a.unit_rows, all) * 2 * a.d;
   a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
   const bool half = layout == KVSEL_ROPE_HALF;
   auto pick = [&](auto t) -> Kernel {
@@ -444,10 +475,11 @@ kvsel_status launch_rope_append(const RopeArgs& in, int32_t dtype, int32_t layou
   const size_t smem = rope_smem(a.d, a.rot);
   const int64_t resident = resident_ctas((const void*)kern, kRopeThreads, smem);
   if (resident <= 0) return KVSEL_ERR_CUDA;
-  const int64_t units = (a.q != nullptr ? ceil_div(a.h_q, a.unit_rows) : 0) + (a.k != nullptr ? 2 * ceil_div(a.h_kv, a.unit_rows) : 0);
   const int64_t grid = std::min(resident, ceil_div(a.n * units, kWarps));
-  a.share = a.n * units / (grid * kWarps);
-  a.extra = a.n * units % (grid * kWarps);
+  const int64_t n_w = grid * kWarps;
+  a.rounds = (int32_t)(a.n / n_w);
+  a.share = a.n % n_w * units / n_w;
+  a.extra = a.n % n_w * units % n_w;
   TraceScope ts("rope_append", s);
   return launch_after(kern, dim3((unsigned)grid), kRopeThreads, smem, s, a);
 }
