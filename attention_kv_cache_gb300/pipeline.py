@@ -208,8 +208,8 @@ _KIND = {torch.bfloat16: K.DTYPE_BF16, torch.float16: K.DTYPE_F16, torch.float8_
 class PagedDecoder:
     """Decoding on from compacted caches: a pool of pages per layer, block tables, and one step's calls.
 
-    ``admit`` puts the kept rows of a batch's compacted caches into pages.  Each step then calls ``begin``
-    once (pages, slots and positions of one new row per request) and ``layer`` for every layer (norm,
+    ``admit`` puts the kept rows of a batch's compacted caches into pages, once.  Each step then calls ``begin``
+    once (pages, slots and positions of one new row for every request) and ``layer`` for every layer (norm,
     rotation and write of the new rows, attention over the request's rows).  A step's calls update the
     lengths in place and synchronise nothing, so a step can be captured and replayed.
 
