@@ -198,13 +198,13 @@ kvsel_status launch_page_assign(const AssignArgs& a, cudaStream_t s) {
   const bool one = in_place && a.max_tokens <= kOneCta;
   const unsigned threads = std::max<int64_t>(a.max_tokens, a.batch) <= 256 ? 256 : kThreads;
   const unsigned grid = one ? 1 : (unsigned)std::min<int64_t>(std::max<int64_t>(1, ceil_div(a.max_tokens, threads)), 1 << 12);
-  if (set_smem((const void*)page_assign, smem) != cudaSuccess || set_smem((const void*)page_assign_plan, smem) != cudaSuccess ||
-      set_smem((const void*)page_assign_fill, smem) != cudaSuccess)
-    return KVSEL_ERR_CUDA;
   if (one || !in_place) {
+    if (set_smem((const void*)page_assign, smem) != cudaSuccess) return KVSEL_ERR_CUDA;
     TraceScope ts("page_assign", s);
     return launch_after(page_assign, dim3(grid), threads, smem, s, a);
   }
+  if (set_smem((const void*)page_assign_plan, smem) != cudaSuccess || set_smem((const void*)page_assign_fill, smem) != cudaSuccess)
+    return KVSEL_ERR_CUDA;
   {
     TraceScope ts("page_assign", s);
     const kvsel_status st = launch_after(page_assign_plan, dim3(1), kThreads, smem, s, a);
