@@ -11,19 +11,18 @@ namespace {
 // o of a request that several lanes hold: sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over its pieces i.
 // blockIdx.y is the request (or the lane) whose span says which pieces; blockIdx.x takes `heads` query heads of it.
 // A request of few pieces gives a warp to each head; of many, all warps to one head after another, each warp every
-// kJoinWarps-th piece.  A warp loads kJoinLoads pieces at once, offsets and rows together, and keeps its own running
+// WARPS-th piece.  A warp loads kJoinLoads pieces at once, offsets and rows together, and keeps its own running
 // offset: latency is what this costs, so nothing waits for anything but the span.
 //
 // Launched while the attention runs (its CTAs fit beside it) and waiting for its end, so that no launch lies between.
-constexpr int kJoinWarps = 16;
 constexpr int kJoinLoads = 10;
 constexpr int kFewPieces = 16;
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join(const __grid_constant__ PagedArgs a, int nt8, int heads) {
+template <int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) paged_join(const __grid_constant__ PagedArgs a, int nt8, int heads) {
   constexpr int V = D / 32;                         // values of a row per lane
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
-  __shared__ Vec red[kJoinWarps][32];
-  __shared__ float2 redml[kJoinWarps];
+  __shared__ Vec red[WARPS][32];
+  __shared__ float2 redml[WARPS];
   wait_for_earlier_kernels();
   const int2 span = a.span[blockIdx.y];
   const int b = a.by_lane ? span.x : blockIdx.y, i0 = a.by_lane ? blockIdx.y : span.x, i1 = span.y;
@@ -31,7 +30,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join(const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int padded = a.h_kv * a.tiles * nt8;
   const bool few = heads > 1 && i1 - i0 < kFewPieces;
-  for (int hh = few ? warp : 0; hh < heads; hh += few ? kJoinWarps : 1) {
+  for (int hh = few ? warp : 0; hh < heads; hh += few ? WARPS : 1) {
     const int h = blockIdx.x * heads + hh;
     if (h >= a.h_q) return;                         // (the whole CTA where its warps share a head)
     const int g = h / a.G;
@@ -48,7 +47,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join(const __grid_const
 #pragma unroll
       for (int e = 0; e < V; ++e) num[e] = num[e] * wo + v[e] * wn;
     };
-    const int step = few ? 1 : kJoinWarps;
+    const int step = few ? 1 : WARPS;
     for (int i = i0 + (few ? 0 : warp); i <= i1; i += kJoinLoads * step) {
       float2 ml[kJoinLoads];
       Vec v[kJoinLoads];
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join(const __grid_const
       __syncthreads();
       if (warp != 0) continue;
 #pragma unroll
-      for (int i = 1; i < kJoinWarps; ++i) take(redml[i], reinterpret_cast<const float*>(&red[i][lane]));
+      for (int i = 1; i < WARPS; ++i) take(redml[i], reinterpret_cast<const float*>(&red[i][lane]));
     }
     const float s = den == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / den;
     const int64_t oh = (int64_t)b * a.h_q + h;
@@ -118,7 +117,7 @@ int sm_count() {
 }
 
 struct Geometry {
-  int nt, tiles, lanes, grid, by_lane;
+  int nt, tiles, lanes, grid, by_lane, solo;
   size_t span_off, ml_off, part_off, total;
 };
 // One CTA per SM, fewer when the bound on the steps needs fewer warps.
@@ -136,6 +135,13 @@ bool geometry(const PagedShape& p, Geometry* out) {
                                           std::max<int64_t>(1, most * p.batch / kMinSteps));
   o.lanes = (int)lanes;
   o.grid = (int)std::min<int64_t>(sms, ceil_div(lanes * units, v.warps));
+  // Short calls, all of whose CTAs run at once.  Lanes use every SM, a CTA per request and unit `ctas` of them, which
+  // takes about (most / warps) (1 - ctas / SMs) steps longer; the join and its launch take about as long as 4 (us, by
+  // requests x rows, 8 KV heads of 128: 1 x 400 7.0 against 7.3 by lanes, 16 x 400 7.5 / 17, 16 x 800 13.3 / 17.3,
+  // 1 x 800 9.9 / 7.5, 1 x 1600 15.2 / 7.9).  kSoloSteps bounds what one long request among short ones can cost.
+  const int64_t ctas = units * p.batch;
+  o.solo = ctas <= sms && most <= (int64_t)kSoloSteps * v.warps && most * (sms - ctas) <= (int64_t)4 * v.warps * sms;
+  if (o.solo) o.grid = (int)ctas;
   const int64_t heads = units * 8 * o.nt;
   auto up = [](size_t x) { return (x + KVSEL_WS_ALIGN - 1) / KVSEL_WS_ALIGN * KVSEL_WS_ALIGN; };
   o.by_lane = p.batch > lanes;
@@ -197,18 +203,22 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.tiles = geo.tiles;
   a.lanes = geo.lanes;
   a.by_lane = geo.by_lane;
+  a.solo = geo.solo;
   const size_t smem = var.smem + sizeof(int2) * (size_t)p.batch;
   if (set_smem((const void*)var.kern, smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   {
     TraceScope ts("paged_attend", s);
     const kvsel_status st = launch_after(var.kern, dim3(geo.grid), 32 * var.warps, smem, s, a);
-    if (st != KVSEL_OK) return st;
+    if (st != KVSEL_OK || geo.solo) return st;
   }
   TraceScope ts("paged_join", s);
   const int rows = geo.by_lane ? geo.lanes : p.batch;
-  const int heads = (int64_t)rows * p.h_q > 4 * 152 ? kJoinWarps : 1;    // a CTA per head while those are few
-  const dim3 grid((unsigned)ceil_div(p.h_q, heads), (unsigned)rows);
-  return launch_after(p.d == 64 ? paged_join<64> : paged_join<128>, grid, 32 * kJoinWarps, 0, s, a, 8 * geo.nt, heads);
+  // requests of many pieces: a CTA of 16 warps for each head, while those are few; else a warp per head in CTAs of 4
+  const bool split = geo.lanes / rows >= kFewPieces && (int64_t)rows * p.h_q <= 4 * 152;
+  using Join = void (*)(const PagedArgs, int, int);
+  const Join join = p.d == 64 ? (split ? paged_join<64, 16> : paged_join<64, 4>) : (split ? paged_join<128, 16> : paged_join<128, 4>);
+  const int warps = split ? 16 : 4, heads = split ? 1 : 4;
+  return launch_after(join, dim3((unsigned)ceil_div(p.h_q, heads), (unsigned)rows), 32 * warps, 0, s, a, 8 * geo.nt, heads);
 }
 
 }  // namespace kvsel

@@ -18,6 +18,10 @@
 // A request cut between lanes leaves one partial (O, offset, sum) per piece, which paged_join merges; a request within
 // one lane is written at once.
 //
+// A call whose tables hold few rows is a CTA per (request, unit) instead: its warps share the request's steps and merge
+// their parts in shared memory, one launch and no partials.  (A CTA holds an SM whatever its request's length, so the
+// tables' size and not the lengths decide: see geometry().)
+//
 // Stages: 192 KB of an SM's shared memory, four warps of three 16 KB steps (16-bit pools, d = 128) or eight of 8 KB.  At
 // 128 KB in flight a read of the whole cache runs at the copy rate; three or six warps lose 5-15 %, twelve warps of two
 // stages 8 %.  cp.async by all lanes, rows without a source zero-filled, rather than boxes of a tensor map: the boxes
@@ -25,7 +29,8 @@
 //
 // Measured (GB300, device time, both kernels): 32 requests of 2048-65536 rows, 8 KV heads of 128, bf16, 647 us (4430 MB,
 // 6.8 TB/s); 1 x 131072 rows 86 us (537 MB, 6.3 TB/s); 256 requests of 1-4095 rows, e4m3, capped, window 2048, 141 us
-// (813 MB, 5.8 TB/s; 550 instructions per step of 8 KB against 512 of 16 KB); 1 x 517 rows 7.4 us.
+// (813 MB, 5.8 TB/s; 550 instructions per step of 8 KB against 512 of 16 KB); 1 x 517 rows 5.4 us (by lanes
+// 7.2), 16 x 800 rows 13.3 us (17.3).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -37,6 +42,7 @@
 namespace kvsel {
 
 constexpr int kKeys = 32;             // rows per step: one per lane
+constexpr int kSoloSteps = 8;         // steps per warp of a short call at most
 constexpr int kMinSteps = 1;          // a lane is not given fewer steps than this
 constexpr float kLog2e = 1.4426950408889634f;
 enum Kind { kBf16 = 0, kF16 = 1, kE4m3 = 2 };
@@ -61,6 +67,7 @@ struct PagedArgs {
   int32_t tiles;        // tiles of query heads per KV head
   int32_t lanes;        // lanes the grid can hold
   int32_t by_lane;
+  int32_t solo;         // a CTA per request and unit (no lanes, no join)
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -158,6 +165,16 @@ __device__ __forceinline__ uint32_t chunk_from(uint32_t at, int mt, int c) {
   else return (at ^ (uint32_t)(c << 4)) + mt * 16 * 64;
 }
 
+// two output values in the output's type
+__device__ __forceinline__ uint32_t pack_out(const PagedArgs& a, float u, float v) {
+  if (a.out_f16) {
+    const __half2 y = __floats2half2_rn(u, v);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+  const __nv_bfloat162 y = __floats2bfloat162_rn(u, v);
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
 // First visible row of a request of n rows.
 __device__ __forceinline__ int first_row(int n, int window) { return window > 0 && n > window ? n - window : 0; }
 // First step of lane i of N over T steps.
@@ -210,6 +227,24 @@ __device__ int step_sums(const PagedArgs& a, int2* cum) {
   return total;
 }
 
+// The same for request b alone.
+template <int THREADS>
+__device__ int one_request(const PagedArgs& a, int b, int2* cum) {
+  int64_t L = a.lens[b];
+  if (L < 0 || L > (int64_t)a.max_blocks * a.P) {
+    if (threadIdx.x == 0) set_device_error(a.err, KVSEL_ERR_INVALID_ARG, (uint32_t)b);
+    L = 0;
+  }
+  const int n = (int)L;
+  const int steps = (n + kKeys - 1) / kKeys - first_row(n, a.window) / kKeys;
+  if (threadIdx.x == 0) {
+    cum[0] = make_int2(0, n);
+    cum[1] = make_int2(steps, 0);
+  }
+  __syncthreads();
+  return steps;
+}
+
 __device__ __forceinline__ int find_request(const int2* cum, int batch, int x) {
   int lo = 0, hi = batch;
   while (hi - lo > 1) {
@@ -236,14 +271,24 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
   const uint32_t v_lane = KIND == kE4m3 ? k_lane : chunk_at<RB>(((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
 
   wait_for_earlier_kernels();
-  let_later_kernels_start();                        // (paged_join: it waits for this grid's end)
-  const int T = step_sums<32 * W>(a, cum);
-  const int N = max(1, min(a.lanes, T / kMinSteps));
+  const int units = a.h_kv * a.tiles;
+  // A short call is a CTA per (request, unit), which knows its one request alone; requests are counted from b0.
+  const bool solo = a.solo != 0;
+  const int b0 = solo ? blockIdx.x / units : 0;
+  const int batch = solo ? 1 : a.batch;
+  int T, N = 1;
+  if (solo) {
+    T = one_request<32 * W>(a, b0, cum);
+  } else {
+    let_later_kernels_start();                      // (paged_join: it waits for this grid's end)
+    T = step_sums<32 * W>(a, cum);
+    N = max(1, min(a.lanes, T / kMinSteps));
+  }
   if (a.by_lane && blockIdx.x == 0)                 // lanes without a step
     for (int i = threadIdx.x; i < a.lanes; i += 32 * W)
       if (i >= N || lane_begin(i, T, N) == lane_begin(i + 1, T, N)) a.span[i] = make_int2(0, -1);
   // requests without a row: o = 0, lse = -inf
-  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+  for (int b = blockIdx.x; b < a.batch && !solo; b += gridDim.x) {
     if (cum[b].x != cum[b + 1].x) continue;
     uint32_t* ob = reinterpret_cast<uint32_t*>(a.o) + (int64_t)b * a.h_q * (D / 2);
     for (int x = threadIdx.x; x < a.h_q * (D / 2); x += 32 * W) ob[x] = 0u;
@@ -251,13 +296,18 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       for (int x = threadIdx.x; x < a.h_q; x += 32 * W) a.lse[(int64_t)b * a.h_q + x] = -INFINITY;
     if (!a.by_lane && threadIdx.x == 0) a.span[b] = make_int2(0, -1);
   }
-  const int units = a.h_kv * a.tiles;
   const int heads_pad = units * 8 * NT;
-  for (int64_t w = (int64_t)blockIdx.x * W + warp; w < (int64_t)N * units; w += (int64_t)gridDim.x * W) {
-    const int li = (int)(w / units), unit = (int)(w - (int64_t)li * units);
+  // a warp's part of a short call: O of its steps by head, offset and sum
+  constexpr int kSoloPitch = D + 4, kSoloHeads = 8 * NT;
+  float* solo_o = reinterpret_cast<float*>(sbase + warp * NS * stage_bytes<D, KIND>());
+  float2* solo_ml = reinterpret_cast<float2*>(solo_o + kSoloHeads * kSoloPitch);
+  static_assert(kSoloHeads * (kSoloPitch * 4 + 8) <= NS * stage_bytes<D, KIND>(), "a warp's part fits its stages");
+  const int first_w = solo ? 0 : (int)blockIdx.x * W + warp, n_w = solo ? 1 : N * units, step_w = solo ? 1 : (int)gridDim.x * W;
+  for (int w = first_w; w < n_w; w += step_w) {
+    const int li = solo ? 0 : w / units, unit = solo ? (int)blockIdx.x - b0 * units : w - li * units;
     const int g = unit / a.tiles, tile = unit - g * a.tiles;
-    const int x0 = lane_begin(li, T, N), x1 = lane_begin(li + 1, T, N);
-    if (x0 >= x1) continue;
+    const int x0 = solo ? T * warp / W : lane_begin(li, T, N), x1 = solo ? T * (warp + 1) / W : lane_begin(li + 1, T, N);
+    if (x0 >= x1 && !solo) continue;
     const uint8_t* kbase = static_cast<const uint8_t*>(a.k) + (int64_t)g * a.head_stride * elem_bytes<KIND>();
     const uint8_t* vbase = static_cast<const uint8_t*>(a.v) + (int64_t)g * a.head_stride * elem_bytes<KIND>();
 
@@ -285,7 +335,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
         const int hl = (tile * NT + nt) * 8 + gq;
         const bool live = hl < a.G;
         const uint32_t* qrow = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
-                                                                 (int64_t)request * a.q_stride +
+                                                                 (int64_t)(b0 + request) * a.q_stride +
                                                                  (int64_t)(live ? g * a.G + hl : 0) * D);
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
@@ -295,7 +345,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
         }
       }
     };
-    int b = find_request(cum, a.batch, x0);         // request of the next piece
+    int b = find_request(cum, batch, x0);           // request of the next piece
     if (NT == 1) load_q(b, qn);
 
     // ---- the steps' rows, ahead of the arithmetic -----------------------------------------------
@@ -318,7 +368,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
         if (r.seen) {
           const int blk = (int)((__umulhi(a.p_mul, (uint32_t)t) + (uint32_t)t) >> a.p_shift);   // t / P
           r.within = t - blk * a.P;
-          r.id = a.tables[(int64_t)pb * a.max_blocks + blk];
+          r.id = a.tables[(int64_t)(b0 + pb) * a.max_blocks + blk];
         }
         ++px;
       }
@@ -328,7 +378,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
     // rows without a source are zeros.
     auto issue = [&](const Row& r, int buf) -> uint32_t {
       const bool ok = r.seen && r.id >= 0 && r.id < a.n_pages;
-      if (r.seen && !ok) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)r.b);
+      if (r.seen && !ok) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)(b0 + r.b));
       const int64_t off = (ok ? (int64_t)r.id * a.page_stride + (int64_t)r.within * a.row_stride : 0) * elem_bytes<KIND>();
       const uint32_t seen = __ballot_sync(0xffffffffu, ok);
       constexpr int KPI = 32 / CPR;                 // rows per copy instruction
@@ -369,7 +419,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       const int f = first_row(n, a.window);
       const int row_end = min(x1, last);
       const bool starts = x == first, ends = row_end == last;
-      if (unit == 0 && lane == 0) {                 // (one warp of the lane speaks for all)
+      if (unit == 0 && lane == 0 && !solo) {        // (one warp of the lane speaks for all)
         if (!a.by_lane && starts) a.span[b] = make_int2(li, ends ? li : lane_of(last - 1, T, N));
         if (a.by_lane && row_end == x1) a.span[li] = make_int2(b, starts && !ends ? lane_of(last - 1, T, N) : -1);
       }
@@ -411,7 +461,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       }
       const int now = b;
       if (ends) {                                   // on to the next request with a row; its queries are fetched by then
-        do ++b; while (b < a.batch && cum[b + 1].x == last);
+        do ++b; while (b < batch && cum[b + 1].x == last);
         if (NT == 1 && row_end < x1) load_q(b, qn);
       }
       bool fresh = true;                            // one of this lane's heads has no offset yet
@@ -607,7 +657,20 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
           for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
       // d of accumulator element e of slice c: rows gq and gq + 8 of the slice, or 2 gq and 2 gq + 1 from bytes
       const int d0 = KIND == kE4m3 ? 2 * gq : gq, d1 = KIND == kE4m3 ? 2 * gq + 1 : gq + 8;
-      if (starts && ends) {
+      if (solo) {                                   // to the warp's own stages, all read by now
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float* to = solo_o + (nt * 8 + 2 * tq + e) * kSoloPitch;
+#pragma unroll
+            for (int c = 0; c < KS; ++c) {
+              to[16 * c + d0] = o[c][nt][e];
+              to[16 * c + d1] = o[c][nt][e + 2];
+            }
+            if (gq == 0) solo_ml[nt * 8 + 2 * tq + e] = make_float2(m[nt][e], l[nt][e]);
+          }
+      } else if (starts && ends) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float inv[2];
@@ -621,18 +684,10 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
           // transposed back, a lane holds consecutive d of one head: 2 tq, +1 of both halves of a slice, or 4 tq .. + 3
           const int hl = (tile * NT + nt) * 8 + gq;
           uint32_t* orow = static_cast<uint32_t*>(a.o) + ((int64_t)now * a.h_q + g * a.G + hl) * (D / 2);
-          auto pack = [&](float u, float v) -> uint32_t {
-            if (a.out_f16) {
-              const __half2 y = __floats2half2_rn(u, v);
-              return *reinterpret_cast<const uint32_t*>(&y);
-            }
-            const __nv_bfloat162 y = __floats2bfloat162_rn(u, v);
-            return *reinterpret_cast<const uint32_t*>(&y);
-          };
 #pragma unroll
           for (int c = 0; c < KS; ++c) {
-            const uint32_t y0 = transpose8x8(pack(o[c][nt][0] * inv[0], o[c][nt][1] * inv[1]));
-            const uint32_t y1 = transpose8x8(pack(o[c][nt][2] * inv[0], o[c][nt][3] * inv[1]));
+            const uint32_t y0 = transpose8x8(pack_out(a, o[c][nt][0] * inv[0], o[c][nt][1] * inv[1]));
+            const uint32_t y1 = transpose8x8(pack_out(a, o[c][nt][2] * inv[0], o[c][nt][3] * inv[1]));
             if (hl >= a.G) continue;
             if constexpr (KIND == kE4m3) {
               *reinterpret_cast<uint2*>(orow + 8 * c + 2 * tq) = make_uint2(__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632));
@@ -660,6 +715,36 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
+    if (!solo) continue;
+    // the warps' parts merged as paged_join does, here
+    if (x0 >= x1 && lane < kSoloHeads) solo_ml[lane] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
+    constexpr int part = NS * stage_bytes<D, KIND>() / 4;         // floats from one warp's part to the next
+    const float* o0 = reinterpret_cast<const float*>(sbase);
+    for (int y = threadIdx.x; y < kSoloHeads * (D / 2); y += 32 * W) {
+      const int h = y / (D / 2), d = 2 * (y - h * (D / 2)), hl = tile * kSoloHeads + h;
+      if (hl >= a.G) continue;
+      float2 ml[W];
+      float M = -INFINITY, num0 = 0.f, num1 = 0.f, den = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        ml[i] = reinterpret_cast<const float2*>(o0 + i * part + kSoloHeads * kSoloPitch)[h];
+        M = fmaxf(M, ml[i].x);
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;     // no step, or no score
+        const float wt = ml[i].x == M ? 1.f : exp2f(ml[i].x - M);
+        const float2 v = *reinterpret_cast<const float2*>(o0 + i * part + h * kSoloPitch + d);
+        num0 = fmaf(wt, v.x, num0);
+        num1 = fmaf(wt, v.y, num1);
+        den = fmaf(wt, ml[i].y, den);
+      }
+      const float inv = den == 0.f ? 0.f : vsc / den;
+      const int64_t oh = (int64_t)b0 * a.h_q + g * a.G + hl;
+      static_cast<uint32_t*>(a.o)[(oh * D + d) / 2] = pack_out(a, num0 * inv, num1 * inv);
+      if (a.lse != nullptr && d == 0) a.lse[oh] = (M + log2f(den)) * 0.6931471805599453f;
+    }
   }
 }
 

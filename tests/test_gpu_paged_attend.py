@@ -148,6 +148,30 @@ def test_options(cuda, kw, cache, dtype):
     Case(K, cuda, [0, 1, 40, 700, 2049], cache=cache, dtype=dtype, seed=9, **kw).run().check()
 
 
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("kw", [
+    dict(), dict(G=16), dict(G=1, d=64, h_kv=3), dict(G=20, h_kv=1), dict(softcap=9.0, slopes=True), dict(window=40),
+    dict(P=7), dict(order="row", q_pad=2), dict(lens=[1]), dict(lens=[0, 0]), dict(lens=[3] * 70, h_kv=2, G=2, d=64),
+    dict(qmul=50.0), dict(lens=[64, 380], G=9, P=32),
+], ids=lambda k: "-".join(f"{a}{b if not isinstance(b, list) else len(b)}" for a, b in k.items()) or "plain")
+def test_short_calls(cuda, kw, cache, dtype):
+    """Tables that hold few rows: a CTA per request and KV head, no join."""
+    from attention_kv_cache_gb300 import kvsel as K
+    before = K.kvsel_launch_count()
+    c = Case(K, cuda, **{**dict(lens=[0, 1, 33, 129, 380], cache=cache, dtype=dtype, seed=21), **kw}).run()
+    assert K.kvsel_launch_count() == before + 1
+    c.check()
+    bad = Case(K, cuda, [100, 50, 70], cache=cache, dtype=dtype)
+    bad.l[1] = -3
+    bad.t[2, 1] = bad.n_pages
+    gone = set(range(16, 32))
+    torch.cuda.synchronize()
+    bad.run()
+    torch.cuda.synchronize()
+    assert K.kvsel_read_device_error(bad.ws) in (K.ERR_INVALID_ARG, K.ERR_DEVICE)
+    bad.check(lens=[100, 0, 70], keep=lambda b: [t for t in range((100, 0, 70)[b]) if b < 2 or t not in gone])
+
+
 def test_bf16_queries_of_any_size_over_an_8_bit_pool(cuda):
     """The fp16 copy of a bf16 query row is scaled by its own power of two."""
     from attention_kv_cache_gb300 import kvsel as K
