@@ -130,7 +130,9 @@ bool geometry(const PagedShape& p, Geometry* out) {
   o.tiles = (int)ceil_div(G, 8 * o.nt);
   const PagedVariant v = variant(p, o.nt);
   const int64_t units = (int64_t)p.h_kv * o.tiles;
-  const int64_t most = ceil_div((int64_t)p.max_blocks * p.P, kKeys) + 1;     // steps of one request, bounded
+  // steps of one request at most, by its table and by the window (whose rows may begin and end inside a step)
+  int64_t most = ceil_div((int64_t)p.max_blocks * p.P, kKeys);
+  if (p.window > 0) most = std::min<int64_t>(most, ceil_div((int64_t)p.window + kKeys - 1, kKeys));
   const int64_t lanes = std::min<int64_t>(std::max<int64_t>(1, (int64_t)sms * v.warps / units),
                                           std::max<int64_t>(1, most * p.batch / kMinSteps));
   o.lanes = (int)lanes;

@@ -152,7 +152,8 @@ def test_options(cuda, kw, cache, dtype):
 @pytest.mark.parametrize("kw", [
     dict(), dict(G=16), dict(G=1, d=64, h_kv=3), dict(G=20, h_kv=1), dict(softcap=9.0, slopes=True), dict(window=40),
     dict(P=7), dict(order="row", q_pad=2), dict(lens=[1]), dict(lens=[0, 0]), dict(lens=[3] * 70, h_kv=2, G=2, d=64),
-    dict(qmul=50.0), dict(lens=[64, 380], G=9, P=32),
+    dict(qmul=50.0), dict(lens=[64, 380], G=9, P=32), dict(lens=[4000, 4001, 4031, 4032, 4033, 31, 32], window=33),
+    dict(lens=[3000 + 7 * i for i in range(14)], window=64, h_kv=2), dict(lens=[2500, 2530], window=1),
 ], ids=lambda k: "-".join(f"{a}{b if not isinstance(b, list) else len(b)}" for a, b in k.items()) or "plain")
 def test_short_calls(cuda, kw, cache, dtype):
     """Tables that hold few rows: a CTA per request and KV head, no join."""
