@@ -134,7 +134,7 @@ bool geometry(const PagedShape& p, Geometry* out) {
   int64_t most = ceil_div((int64_t)p.max_blocks * p.P, kKeys);
   if (p.window > 0) most = std::min<int64_t>(most, ceil_div((int64_t)p.window + kKeys - 1, kKeys));
   const int64_t lanes = std::min<int64_t>(std::max<int64_t>(1, (int64_t)sms * v.warps / units),
-                                          std::max<int64_t>(1, most * p.batch / kMinSteps));
+                                          std::max<int64_t>(1, most * p.batch));
   o.lanes = (int)lanes;
   o.grid = (int)std::min<int64_t>(sms, ceil_div(lanes * units, v.warps));
   // Short calls, all of whose CTAs run at once.  Lanes use every SM, a CTA per request and unit `ctas` of them, which
@@ -146,7 +146,7 @@ bool geometry(const PagedShape& p, Geometry* out) {
   if (o.solo) o.grid = (int)ctas;
   const int64_t heads = units * 8 * o.nt;
   auto up = [](size_t x) { return (x + KVSEL_WS_ALIGN - 1) / KVSEL_WS_ALIGN * KVSEL_WS_ALIGN; };
-  o.by_lane = p.batch > lanes;
+  o.by_lane = !o.solo && p.batch > lanes;
   o.span_off = sizeof(DeviceError);
   o.ml_off = up(o.span_off + sizeof(int2) * (size_t)(o.by_lane ? lanes : p.batch));
   o.part_off = up(o.ml_off + sizeof(float2) * 2 * (size_t)(lanes * heads));

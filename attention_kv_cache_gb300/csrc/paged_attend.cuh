@@ -27,7 +27,7 @@
 // stages 8 %.  cp.async by all lanes, rows without a source zero-filled, rather than boxes of a tensor map: the boxes
 // took 2-4 % longer, and left V rows that are not seen to be cleared by hand.
 //
-// Measured (GB300, device time, both kernels): 32 requests of 2048-65536 rows, 8 KV heads of 128, bf16, 647 us (4430 MB,
+// Measured (GB300, device time, join included): 32 requests of 2048-65536 rows, 8 KV heads of 128, bf16, 647 us (4430 MB,
 // 6.8 TB/s); 1 x 131072 rows 86 us (537 MB, 6.3 TB/s); 256 requests of 1-4095 rows, e4m3, capped, window 2048, 141 us
 // (813 MB, 5.8 TB/s; 550 instructions per step of 8 KB against 512 of 16 KB); 1 x 517 rows 5.4 us (by lanes
 // 7.2), 16 x 800 rows 13.3 us (17.3).
@@ -43,7 +43,6 @@ namespace kvsel {
 
 constexpr int kKeys = 32;             // rows per step: one per lane
 constexpr int kSoloSteps = 8;         // steps per warp of a short call at most
-constexpr int kMinSteps = 1;          // a lane is not given fewer steps than this
 constexpr float kLog2e = 1.4426950408889634f;
 enum Kind { kBf16 = 0, kF16 = 1, kE4m3 = 2 };
 
@@ -282,7 +281,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
   } else {
     let_later_kernels_start();                      // (paged_join: it waits for this grid's end)
     T = step_sums<32 * W>(a, cum);
-    N = max(1, min(a.lanes, T / kMinSteps));
+    N = max(1, min(a.lanes, T));
   }
   if (a.by_lane && blockIdx.x == 0)                 // lanes without a step
     for (int i = threadIdx.x; i < a.lanes; i += 32 * W)
