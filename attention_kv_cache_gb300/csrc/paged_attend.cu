@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * WARPS) paged_join(const __grid_constant__
       }
       static_cast<uint32_t*>(a.o)[(oh * D + V * lane + e) / 2] = u;
     }
-    if (a.lse != nullptr && lane == 0) a.lse[oh] = (M + log2f(den)) * 0.6931471805599453f;
+    if (a.lse != nullptr && lane == 0) a.lse[oh] = lse_of(M, den, a.up);
   }
 }
 
@@ -189,6 +189,7 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.q_stride = p.q_stride;
   a.scale = p.scale;
   a.softcap = p.softcap;
+  a.up = p.cache_dtype == KVSEL_DTYPE_BF16 ? weight_up<kBf16>() : weight_up<kF16>();
   a.h_q = p.h_q;
   a.h_kv = p.h_kv;
   a.G = p.h_q / p.h_kv;

@@ -12,8 +12,12 @@
 // Arithmetic: the step's rows are the M side of mma.sync m16n8k16 and 8 query heads the N side, so
 // S^T = K Q^T needs no padding at G = 8; P^T moves from the accumulator to the B operand by movmatrix, and
 // O^T += V^T P^T with V transposed by ldmatrix.  P is taken as a high and a low 16-bit part.  The softmax
-// keeps an exponent offset that moves only when a score passes it by 2^8, so the common step forms no
-// maximum, and the sums stay in the lanes until a row ends.
+// keeps an exponent offset that moves only when a weight passes 2^lag times the largest when it last moved, so the
+// common step forms no maximum, and the sums stay in the lanes until a row ends.
+// An fp16 part is a multiple of 2^-24, so weights near 1 would leave those below 2^-25 out of O while their sum counts
+// them: a long tail behind one high score would be lost.  Over fp16 products the weights are held 2^13 times as large
+// (the offset lies 13 below the score it is taken from) and the lag is 2, so that they end at 2^15, inside fp16, and what is lost of
+// a weight is below 2^-38 of the largest.  bf16 parts have fp32's exponents: a lag of 8 and no factor.
 //
 // A request cut between lanes leaves one partial (O, offset, sum) per piece, which paged_join merges; a request within
 // one lane is written at once.
@@ -61,6 +65,7 @@ struct PagedArgs {
   DeviceError* err;
   int64_t page_stride, head_stride, row_stride, q_stride;
   float scale, softcap;
+  float up;             // weight_up() of the kernel (paged_join's lse)
   int32_t h_q, h_kv, G, P, batch, max_blocks, n_pages, window, out_f16;
   uint32_t p_mul, p_shift;   // division of a row below 2^31 by P: (mulhi(p_mul, t) + t) >> p_shift
   int32_t tiles;        // tiles of query heads per KV head
@@ -132,6 +137,17 @@ __device__ __forceinline__ uint32_t pack_hi(float a, float b, float& ra, float& 
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(x));
+}
+
+// Binary orders that a weight may pass the largest one by before the offset moves, and by which weights are held larger.
+template <int KIND>
+__host__ __device__ constexpr float weight_lag() { return KIND == kBf16 ? 8.f : 2.f; }
+template <int KIND>
+__host__ __device__ constexpr float weight_up() { return KIND == kBf16 ? 0.f : 13.f; }
+// log sum exp from an offset (base 2) and the sum of weights held 2^up as large.  Taking that off both first keeps
+// the result exact where one score is all there is.
+__device__ __forceinline__ float lse_of(float m, float l, float up) {
+  return ((m + up) + log2f(l * __uint_as_float((uint32_t)(127 - (int)up) << 23))) * 0.6931471805599453f;
 }
 
 template <int KIND>
@@ -551,7 +567,8 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
                 s[mt][nt][e] = ok ? s[mt][nt][e] * (plain ? sc[nt][e & 1] : 1.f) : -INFINITY;
             }
         }
-        // distances to the offset; where one passes 2^8 the offset moves to the step's largest score
+        // distances to the offset; where one passes the limit the offset moves to the step's largest score
+        constexpr float kUp = weight_up<KIND>(), kLimit = kUp + weight_lag<KIND>();
         float z[2][NT][4], top = -INFINITY;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
               z[mt][nt][e] = fmaf(s[mt][nt][e], mul[nt][e & 1], -mo[nt][e & 1]);
               top = fmaxf(top, z[mt][nt][e]);
             }
-        if (__any_sync(0xffffffffu, top > (fresh ? -INFINITY : 8.f))) {
+        if (__any_sync(0xffffffffu, top > (fresh ? -INFINITY : kLimit))) {
           fresh = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -572,9 +589,10 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
               float mx = fmaxf(fmaxf(s[0][nt][e] * mm, s[0][nt][e + 2] * mm), fmaxf(s[1][nt][e] * mm, s[1][nt][e + 2] * mm));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              if (mx > m[nt][e] + 8.f) {
-                const float alpha = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mx);
-                m[nt][e] = mo[nt][e] = mx;
+              if (mx > m[nt][e] + kLimit) {
+                const float to = mx - kUp;
+                const float alpha = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - to);
+                m[nt][e] = mo[nt][e] = to;
                 l[nt][e] *= alpha;
 #pragma unroll
                 for (int c = 0; c < KS; ++c) {
@@ -678,7 +696,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
             inv[e] = l[nt][e] == 0.f ? 0.f : vsc / l[nt][e];
             const int hl = (tile * NT + nt) * 8 + 2 * tq + e;
             if (a.lse != nullptr && gq == 0 && hl < a.G)
-              a.lse[(int64_t)now * a.h_q + g * a.G + hl] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
+              a.lse[(int64_t)now * a.h_q + g * a.G + hl] = lse_of(m[nt][e], l[nt][e], weight_up<KIND>());
           }
           // transposed back, a lane holds consecutive d of one head: 2 tq, +1 of both halves of a slice, or 4 tq .. + 3
           const int hl = (tile * NT + nt) * 8 + gq;
@@ -742,7 +760,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       const float inv = den == 0.f ? 0.f : vsc / den;
       const int64_t oh = (int64_t)b0 * a.h_q + g * a.G + hl;
       static_cast<uint32_t*>(a.o)[(oh * D + d) / 2] = pack_out(a, num0 * inv, num1 * inv);
-      if (a.lse != nullptr && d == 0) a.lse[oh] = (M + log2f(den)) * 0.6931471805599453f;
+      if (a.lse != nullptr && d == 0) a.lse[oh] = lse_of(M, den, weight_up<KIND>());
     }
   }
 }

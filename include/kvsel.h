@@ -591,8 +591,9 @@ KVSEL_API kvsel_status kvsel_rope_append(const kvsel_cache_desc* cache, const kv
  * rows are left out.
  *
  * Arithmetic: products of the 16-bit values (e4m3 values as fp16, exactly) accumulated in fp32 on the
- * tensor cores, softmax statistics in fp32, P taken as a high and a low 16-bit part.  With an e4m3 pool
- * the query row is held in fp16 scaled by a power of two of its own (2^-24 of the row's largest value).
+ * tensor cores, softmax statistics in fp32, P taken as a high and a low 16-bit part (2^-17 of a weight; with fp16
+ * and e4m3 pools also 2^-38 of the row's largest weight).  With an e4m3 pool the query row is held in fp16
+ * scaled by a power of two of its own (2^-24 of the row's largest value).
  */
 typedef struct {
   int32_t batch;          /* requests: 1 .. KVSEL_PAGED_MAX_BATCH */
