@@ -93,6 +93,21 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
   return r;
 }
 
+// Two quotients x / s, correctly rounded, of the negated x: q = x (1 / s) and its residual s q - x, which one fused
+// multiply-add forms exactly, correct one another (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990, whose condition is a correctly rounded reciprocal).  A product with 1 / s alone can miss a quotient
+// that lies between two e4m3 numbers, and then goes to the wrong one; plain divisions take 10 to 23 % of an append into an
+// 8-bit pool, this 1 to 5 %.  An infinite q has no residual: NaN, which the minimum makes finite, and q stays.  Scales below
+// 2^-60 (inv_res zero) leave q as it is.  The signs keep a negative zero.
+struct Divisor {
+  F2 s, inv, inv_res;        // s, -1 / s, and -1 / s on the residual
+};
+__device__ __forceinline__ F2 divide_neg(F2 neg_x, const Divisor& d) {
+  const F2 q = mul(neg_x, d.inv);
+  const float2 r = get(fma(q, d.s, neg_x));
+  return fma(f2(fminf(r.x, 0x1p60f), fminf(r.y, 0x1p60f)), d.inv_res, q);
+}
+
 // A lane's 16 elements as four packed pairs of first elements and four of second ones.
 template <typename T, bool HALF>
 __device__ __forceinline__ void unpack16(const uint4* r, F2* a, F2* b) {
@@ -315,20 +330,20 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
           constexpr bool Q = decltype(q_const)::value;
           bool on[R];
           int kind[R];                                          // a query, key or value row
-          float scale[R];
+          float scale[R], held[R];                              // held: what a row of an 8-bit pool is divided by
           F2 x[R][4], y[R][4];
 #pragma unroll
           for (int t = 0; t < R; ++t) {
             const int h = hb + t * rows;
             on[t] = live && h < n;
             kind[t] = Q || r0 + h < bk ? 0 : r0 + h < bv ? 1 : 2;
-            scale[t] = 1.f;
+            scale[t] = held[t] = 1.f;
             uint4 r[2];
             r[0] = r[1] = make_uint4(0, 0, 0, 0);
             if (on[t]) {
               r[0] = *reinterpret_cast<const uint4*>(stage + h * row_bytes + 2 * o0);
               r[1] = *reinterpret_cast<const uint4*>(stage + h * row_bytes + 2 * o1);
-              if (!Q && kind[t] > 0 && a.e4m3) scale[t] = 1.f / (kind[t] == 1 ? a.k_scale[r0 + h - bk] : a.v_scale[r0 + h - bv]);
+              if (!Q && kind[t] > 0 && a.e4m3) held[t] = kind[t] == 1 ? a.k_scale[r0 + h - bk] : a.v_scale[r0 + h - bv];
             }
             unpack16<T, HALF>(r, x[t], y[t]);
           }
@@ -388,17 +403,28 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
           if (!Q && a.e4m3) __syncwarp();                             // a row's bytes lie over its lanes' values
 #pragma unroll
           for (int t = 0; t < R; ++t) {
-            const F2 s2 = f2(scale[t], scale[t]);
+            const bool quotient = !Q && kind[t] > 0 && a.e4m3;
+            const float s1 = quotient ? -scale[t] : scale[t];
+            const F2 s2 = f2(s1, s1);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               x[t][m] = mul(x[t][m], s2);
               y[t][m] = mul(y[t][m], s2);
             }
+            if (quotient) {
+              const float inv = -1.f / held[t], res = fabsf(held[t]) < 0x1p-60f ? 0.f : inv;
+              const Divisor by = {f2(held[t], held[t]), f2(inv, inv), f2(res, res)};
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                x[t][m] = divide_neg(x[t][m], by);
+                y[t][m] = divide_neg(y[t][m], by);
+              }
+            }
             float f[16];
             order16<HALF>(x[t], y[t], f);
             if (!on[t]) continue;
             uint8_t* row = stage + (hb + t * rows) * row_bytes;
-            if (!Q && kind[t] > 0 && a.e4m3) {
+            if (quotient) {
               *reinterpret_cast<uint2*>(row + o0) = pack8_e4m3(f);
               *reinterpret_cast<uint2*>(row + o1) = pack8_e4m3(f + 8);
             } else {
