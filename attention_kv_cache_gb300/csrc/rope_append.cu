@@ -3,9 +3,9 @@
 // y = x rsqrt(mean(x^2) + eps) (w + bias), then the pairs (a, b) of the first `rot` elements become
 // factor (a cos - b sin, b cos + a sin) of the angle position * inv_freq.
 //
-// The angle is formed in turns as a 64-bit fraction: inv_freq / (2 pi) as a multiple of 2^-64 times the
-// position, modulo 2^64, is the fraction of a turn exactly up to position * 2^-65, so a far position loses
-// nothing that a 32-bit product of position and frequency would lose.
+// The angle is formed in turns as a 64-bit fraction: inv_freq / (2 pi) as a multiple of 2^-64 (off by less than one of
+// them) times the position, modulo 2^64.  So it is off by less than position * 2^-64 and the rounding to its top 32
+// bits: 2^-32 of a turn at any position below 2^31.
 //
 // One pass over the data, by single warps: a unit is up to kUnitBytes of a token's rows, queries,
 // keys and values end to end.  Every
@@ -21,7 +21,7 @@
 //     the row's norm;
 //   - two pairs share an instruction (packed fp32);
 //   - units of queries alone share the matrices' reads between rows (32768 tokens 227 -> 219 us);
-//   - frequencies in turns are formed once per CTA (64-bit floating point is slow on this GPU), a token's slot and
+//   - frequencies in turns are formed once per CTA, a token's slot and
 //     position are read a token ahead.
 //
 // Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 38 us (202 MB, 5.3 TB/s; the copies
@@ -144,6 +144,22 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float* f) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
+// Turns per position, inv_freq / (2 pi), as a multiple of 2^-64 modulo 2^64 (whole turns drop out; below 0: its complement):
+// the frequency's mantissa times 130 bits of 1 / (2 pi), shifted by its exponent, off by less than one multiple for
+// frequencies below 2^54 (0 above).  In whole numbers, because a double product is off by 2^-25 of a turn at 2^31
+// positions and its correction in doubles takes 0.2 us of a small call.
+__device__ __forceinline__ uint64_t turns_of(double inv_freq) {
+  constexpr uint64_t kHi = 0xa2f9836e4e441529ull, kLo = 0xfc2757d1f534ddc0ull;      // 2^130 / (2 pi)
+  const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
+  const uint64_t m = (bits & ((uint64_t(1) << 52) - 1)) | (uint64_t(1) << 52);
+  const uint64_t part = m * kHi, lo = part + __umul64hi(m, kLo), hi = __umul64hi(m, kHi) + (lo < part ? 1 : 0);
+  const int shift = 1077 - (int)((bits >> 52) & 0x7ff);                  // (hi, lo) 2^-shift
+  uint64_t t = 0;
+  if (shift >= 64 && shift < 128) t = hi >> (shift - 64);
+  else if (shift > 0 && shift < 64) t = (lo >> shift) | (hi << (64 - shift));
+  return (bits >> 63) != 0 ? 0 - t : t;
+}
+
 // Shared memory, in this order: the warps' stages, the warps' matrices of a token's pairs ([2 kinds][8][chunks + 1] float4:
 // entry 2 m of chunk j holds (A, -B) of its pairs 2 m and 2 m + 1, entry 2 m + 1 holds (C, D)), weights [2][d], turns
 // [rot / 2], the stages' barriers.
@@ -170,7 +186,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
   uint8_t* after = smem + (size_t)kWarps * kRingBytes;
   float4* mats = reinterpret_cast<float4*>(after) + warp * 2 * 8 * pitch;
   float* wts = reinterpret_cast<float*>(after + (size_t)kWarps * 2 * 8 * pitch * 16);
-  int64_t* turns = reinterpret_cast<int64_t*>(wts + 2 * a.d);
+  uint64_t* turns = reinterpret_cast<uint64_t*>(wts + 2 * a.d);
   const uint32_t bar0 = sm100::smem_addr(turns + pairs) + warp * kMaxStages * 8;
   const uint32_t st0 = sm100::smem_addr(stages);
   int group = GROUP;
@@ -240,12 +256,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
     const T* w = static_cast<const T*>(x < a.d ? a.q_weight : a.k_weight);
     wts[x] = w != nullptr ? (float)w[x < a.d ? x : x - a.d] + a.bias : 1.f;
   }
-  // turns per position as signed multiples of 2^-64 (whole turns drop out)
-  for (int x = threadIdx.x; x < pairs; x += kRopeThreads) {
-    double f = a.inv_freq[x] * 0.15915494309189533577;
-    f -= rint(f);
-    turns[x] = __double2ll_rn(f * 18446744073709551616.0);
-  }
+  for (int x = threadIdx.x; x < pairs; x += kRopeThreads) turns[x] = turns_of(a.inv_freq[x]);
   __syncthreads();
   // the matrices of the elements that pass: their weights alone
   for (int x = lane; x < 2 * 8 * (chunks - a.rot / 16); x += 32) {
@@ -282,8 +293,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append(const __grid_cons
         float sn[2], cs[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // the turn's top 32 bits as an angle in [-pi, pi), where the fast sine and cosine are within 2^-21
-          __sincosf((float)(int32_t)((turns[2 * c + e] * pos) >> 32) * 1.4629180792671596e-9f, &sn[e], &cs[e]);
+          // the turn to 32 bits as an angle in [-pi, pi), where the fast sine and cosine are within 2^-21
+          __sincosf((float)(int32_t)((turns[2 * c + e] * (uint64_t)pos + 0x80000000u) >> 32) * 1.4629180792671596e-9f, &sn[e], &cs[e]);
           sn[e] *= a.factor;
           cs[e] *= a.factor;
         }
