@@ -80,3 +80,31 @@ def test_any_frequency_at_any_position(cuda, top, layout):
     y[0][..., first], y[0][..., second] = a * np.cos(angle) - b * np.sin(angle), b * np.cos(angle) + a * np.sin(angle)
     y[1][..., first] = y[1][..., second] = np.abs(a) + np.abs(b)
     near(rotate(cuda, q, POSITIONS, freq, layout), *y, "f16", "turned")
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_cosines_and_sines_to_2_22(cuda, layout):
+    """Pairs of whole numbers with a cos ~ b sin: what is left of the turned pair shows the cosine's and the sine's errors.
+
+    With each off by at most 2^-22, a cos rounded (2^-24 |a|) and everything else exact or a rounding of the small result, the
+    result is off by 2^-22 (|a| + |b|) + 2^-24 |a| and half a step of its own."""
+    d = 256
+    freq = 500000.0 ** (-np.arange(d // 2) / (d // 2))
+    angle = angles(POSITIONS, freq)
+    cos, sin = np.cos(angle), np.sin(angle)
+    many = np.arange(1024, 2048)[:, None, None]
+    steep = np.abs(sin) > np.abs(cos)                     # the larger of the two numbers is `many`, the other follows
+    other = np.rint(many * np.where(steep, cos / np.where(steep, sin, 1.0), sin / np.where(steep, 1.0, cos)))
+    a, b = np.where(steep, many, other), np.where(steep, other, many)
+    best = np.abs(a * cos - b * sin).argmin(0)[None]
+    a, b = (np.take_along_axis(x, best, 0)[0] for x in (a, b))
+    q = torch.empty(len(POSITIONS), 1, d, dtype=torch.half)
+    first, second = (slice(0, d // 2), slice(d // 2, d)) if layout == "half" else (slice(0, d, 2), slice(1, d, 2))
+    q[:, 0, first], q[:, 0, second] = torch.from_numpy(a).half(), torch.from_numpy(b).half()
+    assert np.array_equal(C.f64(q[:, 0, first]), a) and np.array_equal(C.f64(q[:, 0, second]), b)
+    got = rotate(cuda, q, POSITIONS, freq, layout)[:, 0]
+    for part, want, mul in ((first, a * cos - b * sin, a), (second, b * cos + a * sin, b)):
+        tol = 2.0 ** -22 * (np.abs(a) + np.abs(b)) + 2.0 ** -24 * np.abs(mul)
+        tol += 2.0 ** -11 * (np.abs(want) + tol) + 2.0 ** -25
+        bad = ~(np.abs(got[:, part] - want) <= tol)
+        assert not bad.any(), (bad.sum(), (np.abs(got[:, part] - want) / tol).max())
