@@ -205,6 +205,15 @@ class ClaaPipeline:
 _KIND = {torch.bfloat16: K.DTYPE_BF16, torch.float16: K.DTYPE_F16, torch.float8_e4m3fn: K.DTYPE_E4M3}
 
 
+def _torch_stream(stream):
+    """A call's `stream` (None, a torch stream or a handle) as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream()
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return stream
+
+
 class PagedDecoder:
     """Decoding on from compacted caches: a pool of pages per layer, block tables, and one step's calls.
 
@@ -263,19 +272,27 @@ class PagedDecoder:
 
     def admit(self, k_out, v_out, text_lens, rows: Optional[int] = None, stream=None):
         """The first ``rows`` rows (all by default) of compacted caches [batch, n_layers, h_kv, rows, d] into pages;
-        ``text_lens`` [batch] positions each request's text has, so that its next row gets the next position."""
+        ``text_lens`` [batch] positions each request's text has, so that its next row gets the next position.
+
+        All of it runs on ``stream``, behind what torch's current stream holds by now (the buffers' first
+        values, ``text_lens``); as with every call, who uses another stream next orders it behind this one."""
         rows = k_out.shape[3] if rows is None else rows
         n = self.batch * rows
-        self.pos_offset.copy_(torch.as_tensor(text_lens, dtype=torch.int64) - rows)
-        slots = torch.empty(n, dtype=torch.int64, device=self.device)
-        self._assign(torch.full_like(self.lens, rows), slots, None, stream)
-        for layer in range(self.n_layers):
-            ks, vs = self._scale(layer)
-            for b in range(self.batch):
-                k, v = (x[b, layer, :, :rows].transpose(0, 1) for x in (k_out, v_out))     # [rows, h_kv, d]
-                desc = K.make_rope_desc(rot_dim=0, k=k, v=v)
-                K.kvsel_rope_append(self.cache, desc, None, k, v, None, slots[b * rows:(b + 1) * rows], None, None, None,
-                                    None, self.k_cache[layer], self.v_cache[layer], ks, vs, self.ws, stream=stream)
+        current, stream = torch.cuda.current_stream(), _torch_stream(stream)
+        if stream != current:
+            stream.wait_stream(current)
+        with torch.cuda.stream(stream):            # the temporaries are that stream's too: reused behind its kernels alone
+            self.pos_offset.copy_(torch.as_tensor(text_lens, dtype=torch.int64) - rows)
+            slots = torch.empty(n, dtype=torch.int64, device=self.device)
+            self._assign(torch.full_like(self.lens, rows), slots, None, stream)
+            for layer in range(self.n_layers):
+                ks, vs = self._scale(layer)
+                for b in range(self.batch):
+                    k, v = (x[b, layer, :, :rows].transpose(0, 1) for x in (k_out, v_out))     # [rows, h_kv, d]
+                    desc = K.make_rope_desc(rot_dim=0, k=k, v=v)
+                    K.kvsel_rope_append(self.cache, desc, None, k, v, None, slots[b * rows:(b + 1) * rows], None, None,
+                                        None, None, self.k_cache[layer], self.v_cache[layer], ks, vs, self.ws,
+                                        stream=stream)
 
     def begin(self, stream=None):
         """Pages, slots and positions of one new row per request."""
