@@ -215,7 +215,7 @@ def _torch_stream(stream):
 
 
 class PagedDecoder:
-    """Decoding on from compacted caches: a pool of pages per layer, block tables, and one step's calls.
+    """One batch's decoding on from compacted caches: a pool of pages per layer, block tables, and one step's calls.
 
     ``admit`` puts the kept rows of a batch's compacted caches into pages, once.  Each step then calls ``begin``
     once (pages, slots and positions of one new row for every request) and ``layer`` for every layer (norm,
@@ -236,6 +236,7 @@ class PagedDecoder:
         self.n_layers, self.batch, self.n_pages, self.P = n_layers, batch, n_pages, P
         self.h_q, self.h_kv, self.d, self.device = h_q, h_kv, head_dim, device
         self.norms, self.scales, self.slopes, self.norm_eps, self.rope_layout = norms, scales, slopes, norm_eps, rope_layout
+        self.dtype, self._q_shape, self._kv_shape = dtype, (batch, h_q, head_dim), (batch, h_kv, head_dim)
         self.cache = K.make_cache_desc(h_q=h_q, h_kv=h_kv, head_dim=head_dim, page_size=P, n_pages=n_pages,
                                        dtype=_KIND[dtype], cache_dtype=_KIND[cache_dtype])
         self.rot_dim, self.factor, self.inv_freq = 0, 1.0, None
@@ -270,19 +271,32 @@ class PagedDecoder:
     def _scale(self, layer):
         return (None, None) if self.scales is None else (self.scales[0][layer], self.scales[1][layer])
 
+    def _checked(self, what: str, t, shape):
+        """The kernels read the rows of a whole batch: a tensor of another shape, type or device is refused."""
+        if t.shape != shape or t.dtype != self.dtype or t.device != self.lens.device:
+            raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}, not {shape} {self.dtype} on {self.lens.device}")
+
     def admit(self, k_out, v_out, text_lens, rows: Optional[int] = None, stream=None):
         """The first ``rows`` rows (all by default) of compacted caches [batch, n_layers, h_kv, rows, d] into pages;
         ``text_lens`` [batch] positions each request's text has, so that its next row gets the next position.
 
         All of it runs on ``stream``, behind what torch's current stream holds by now (the buffers' first
         values, ``text_lens``); as with every call, who uses another stream next orders it behind this one."""
-        rows = k_out.shape[3] if rows is None else rows
+        held = k_out.shape[3] if k_out.dim() == 5 else 0
+        for what, x in (("k_out", k_out), ("v_out", v_out)):
+            self._checked(what, x, (self.batch, self.n_layers, self.h_kv, held, self.d))
+        rows = held if rows is None else rows
+        if not 0 <= rows <= held:
+            raise ValueError(f"{rows} rows of caches that hold {held}")
         n = self.batch * rows
         current, stream = torch.cuda.current_stream(), _torch_stream(stream)
         if stream != current:
             stream.wait_stream(current)
         with torch.cuda.stream(stream):            # the temporaries are that stream's too: reused behind its kernels alone
-            self.pos_offset.copy_(torch.as_tensor(text_lens, dtype=torch.int64) - rows)
+            text = torch.as_tensor(text_lens, dtype=torch.int64)
+            if text.shape != (self.batch,):
+                raise ValueError(f"text_lens of {tuple(text.shape)}, not one per request of {self.batch}")
+            self.pos_offset.copy_(text - rows)
             slots = torch.empty(n, dtype=torch.int64, device=self.device)
             self._assign(torch.full_like(self.lens, rows), slots, None, stream)
             for layer in range(self.n_layers):
@@ -301,6 +315,9 @@ class PagedDecoder:
     def layer(self, layer: int, q, k, v, stream=None):
         """q [batch, h_q, d], k and v [batch, h_kv, d] (any row strides) of the step's rows; returns o [batch, h_q, d],
         which the next call overwrites."""
+        self._checked("q", q, self._q_shape)
+        self._checked("k", k, self._kv_shape)
+        self._checked("v", v, self._kv_shape)
         ks, vs = self._scale(layer)
         desc = K.make_rope_desc(rot_dim=self.rot_dim, layout=self.rope_layout, factor=self.factor,
                                 norm_eps=self.norm_eps, q=q, k=k, v=v)

@@ -79,3 +79,60 @@ def test_admission_is_one_streams_work(monkeypatch):
     r.log.clear()
     dec.admit(*caches(), [30, 31, 32])
     assert all(e[1] == "main" for e in r.log)
+
+
+def step_rows(n=3, h_q=8, h_kv=2, d=64, dtype=torch.bfloat16):
+    return [torch.zeros(n, h, d, dtype=dtype) for h in (h_q, h_kv, h_kv)]
+
+
+@pytest.mark.parametrize("at,shape,dtype", [
+    (0, (4, 8, 64), torch.bfloat16), (0, (2, 8, 64), torch.bfloat16), (0, (3, 9, 64), torch.bfloat16),
+    (0, (3, 8, 128), torch.bfloat16), (0, (3, 8, 64), torch.float16), (0, (3, 8 * 64), torch.bfloat16),
+    (1, (4, 2, 64), torch.bfloat16), (1, (3, 1, 64), torch.bfloat16), (1, (3, 2, 32), torch.bfloat16),
+    (1, (3, 2, 64), torch.float32), (2, (4, 2, 64), torch.bfloat16), (2, (3, 1, 64), torch.bfloat16)])
+def test_rows_of_another_batch_are_refused(monkeypatch, at, shape, dtype):
+    """More rows than the batch has would be read past its slots and written past its queries."""
+    r = Recorder(monkeypatch)
+    dec = decoder()
+    x = step_rows()
+    r.log.clear()
+    dec.layer(0, *x)
+    assert [e[0] for e in r.log] == ["kvsel_rope_append", "kvsel_paged_attend"]
+    r.log.clear()
+    x[at] = torch.zeros(shape, dtype=dtype)
+    with pytest.raises(ValueError):
+        dec.layer(0, *x)
+    x[at] = torch.zeros(step_rows()[at].shape, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError):
+        dec.layer(0, *x)
+    assert not any(e[0].startswith("kvsel") for e in r.log)
+
+
+@pytest.mark.parametrize("kw", [dict(batch=4), dict(batch=2), dict(n_layers=1), dict(h_kv=1), dict(d=32),
+                                dict(dtype=torch.float16)])
+def test_caches_of_another_shape_are_refused(monkeypatch, kw):
+    r = Recorder(monkeypatch)
+    dec = decoder()
+    good, bad = caches(), caches(**kw)
+    r.log.clear()
+    for pair in (bad, (good[0], bad[1]), (bad[0], good[1])):
+        with pytest.raises(ValueError):
+            dec.admit(*pair, [30, 31, 32])
+    assert not any(e[0].startswith("kvsel") for e in r.log)
+
+
+def test_admission_checks_rows_and_texts(monkeypatch):
+    r = Recorder(monkeypatch)
+    dec = decoder()
+    r.log.clear()
+    for rows in (-1, 21):
+        with pytest.raises(ValueError):
+            dec.admit(*caches(), [30, 31, 32], rows=rows)
+    for text in ([30, 31], [30, 31, 32, 33], [[30, 31, 32]], 30):
+        with pytest.raises(ValueError):
+            dec.admit(*caches(), text)
+    with pytest.raises(ValueError):
+        dec.admit(caches(rows=20)[0], caches(rows=19)[1], [30, 31, 32])
+    assert not any(e[0].startswith("kvsel") for e in r.log)
+    dec.admit(*caches(), [30, 31, 32], rows=7)
+    assert sum(e[0] == "kvsel_rope_append" for e in r.log) == 6
