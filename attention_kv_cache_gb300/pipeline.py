@@ -217,7 +217,7 @@ def _torch_stream(stream):
 class PagedDecoder:
     """One batch's decoding on from compacted caches: a pool of pages per layer, block tables, and one step's calls.
 
-    ``admit`` puts the kept rows of a batch's compacted caches into pages, once.  Each step then calls ``begin``
+    ``admit`` puts the kept rows of a batch's compacted caches into pages.  Each step then calls ``begin``
     once (pages, slots and positions of one new row for every request) and ``layer`` for every layer (norm,
     rotation and write of the new rows, attention over the request's rows).  A step's calls update the
     lengths in place and synchronise nothing, so a step can be captured and replayed.
@@ -279,6 +279,7 @@ class PagedDecoder:
     def admit(self, k_out, v_out, text_lens, rows: Optional[int] = None, stream=None):
         """The first ``rows`` rows (all by default) of compacted caches [batch, n_layers, h_kv, rows, d] into pages;
         ``text_lens`` [batch] positions each request's text has, so that its next row gets the next position.
+        Rows that the requests hold already stay: the new ones come behind them.
 
         All of it runs on ``stream``, behind what torch's current stream holds by now (the buffers' first
         values, ``text_lens``); as with every call, who uses another stream next orders it behind this one."""
@@ -296,9 +297,10 @@ class PagedDecoder:
             text = torch.as_tensor(text_lens, dtype=torch.int64)
             if text.shape != (self.batch,):
                 raise ValueError(f"text_lens of {tuple(text.shape)}, not one per request of {self.batch}")
-            self.pos_offset.copy_(text - rows)
             slots = torch.empty(n, dtype=torch.int64, device=self.device)
             self._assign(torch.full_like(self.lens, rows), slots, None, stream)
+            self.pos_offset.copy_(text)                # (slots alone were assigned: positions begin with the next row)
+            self.pos_offset.sub_(self.lens)
             for layer in range(self.n_layers):
                 ks, vs = self._scale(layer)
                 for b in range(self.batch):

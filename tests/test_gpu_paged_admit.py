@@ -77,3 +77,26 @@ def test_a_captured_admission(cuda):
     assert dec.lens.tolist() == [0, 0, 0]
     g.replay()
     _check(dec, k, v, texts.tolist())
+
+
+@pytest.mark.parametrize("first", [1, 16, 20])
+def test_a_second_admission_goes_on_behind_the_first(cuda, first):
+    """Rows in two parts are rows at once, and the next row's position is that of the whole text."""
+    dec, k, v = _decoder(cuda)
+    dec.admit(k, v, [40, 41, 42], rows=first)
+    torch.cuda.synchronize()
+    assert (dec.lens + dec.pos_offset).tolist() == [40, 41, 42]
+    dec.admit(k[:, :, :, first:], v[:, :, :, first:], [90, 55, 37])
+    _check(dec, k, v, [90, 55, 37])
+
+
+def test_admission_behind_decoded_rows(cuda):
+    dec, k, v = _decoder(cuda)
+    dec.admit(k, v, [90, 55, 37], rows=10)
+    for _ in range(5):
+        dec.begin()
+    dec.admit(k[:, :, :, 10:20], v[:, :, :, 10:20], [200, 201, 202])
+    torch.cuda.synchronize()
+    assert dec.lens.tolist() == [25] * 3 and (dec.lens + dec.pos_offset).tolist() == [200, 201, 202]
+    for b in range(3):
+        assert torch.equal(_rows(dec, dec.k_cache, 1, b, 25)[:, 15:], k[b, 1, :, 10:20])
