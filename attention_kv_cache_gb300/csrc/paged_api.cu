@@ -210,6 +210,9 @@ kvsel_status kvsel_rope_append(const kvsel_cache_desc* cache, const kvsel_rope_d
   if (!std::isfinite(r.factor) || !std::isfinite(r.weight_bias) || !std::isfinite(r.norm_eps) || r.norm_eps < 0.f)
     return KVSEL_ERR_INVALID_ARG;
   if (r.rot_dim % 16 != 0) return KVSEL_ERR_UNSUPPORTED;
+  for (int64_t s : {r.q_stride, r.q_head_stride, r.k_stride, r.k_head_stride, r.v_stride, r.v_head_stride})
+    if (s < 0 || s % 8 != 0 || s > (int64_t(1) << 40)) return KVSEL_ERR_INVALID_ARG;
+  if (n_tokens == 0) return KVSEL_OK;             // (arrays of no tokens may have no address)
   const bool has_q = q != nullptr, has_kv = k != nullptr;
   if (!has_q && !has_kv) return KVSEL_ERR_INVALID_ARG;
   if (has_q != (q_out != nullptr) || has_kv != (v != nullptr) || has_kv != (k_cache != nullptr) ||
@@ -220,13 +223,10 @@ kvsel_status kvsel_rope_append(const kvsel_cache_desc* cache, const kvsel_rope_d
   for (const void* p : {q, k, v, (const void*)q_out, (const void*)k_cache, (const void*)v_cache, q_weight, k_weight})
     if (!aligned(p, 16)) return KVSEL_ERR_INVALID_ARG;
   if (!aligned(positions, 8) || !aligned(slots, 8) || !aligned(inv_freq, 8)) return KVSEL_ERR_INVALID_ARG;
-  for (int64_t s : {r.q_stride, r.q_head_stride, r.k_stride, r.k_head_stride, r.v_stride, r.v_head_stride})
-    if (s < 0 || s % 8 != 0 || s > (int64_t(1) << 40)) return KVSEL_ERR_INVALID_ARG;
   // in place only where every row is written over itself
   if (has_q && q_out == q && (r.q_head_stride != c.head_dim || r.q_stride != (int64_t)c.h_q * c.head_dim))
     return KVSEL_ERR_INVALID_ARG;
   if (ws != nullptr && !aligned(ws, KVSEL_WS_ALIGN)) return KVSEL_ERR_WORKSPACE;
-  if (n_tokens == 0) return KVSEL_OK;
   RopeArgs a;
   a.h_q = c.h_q;
   a.h_kv = c.h_kv;

@@ -534,6 +534,7 @@ KVSEL_API kvsel_status kvsel_rope_freqs(int32_t rot_dim, const kvsel_rope_scalin
  * as x / scale of its head, rounded to nearest and clamped to +-448.  Tokens with slot -1 are padding:
  * nothing of theirs is written.  All arithmetic is fp32 with one rounding at the end; angles are formed
  * to 2^-32 of a turn at any frequency below 2^50 and position below 2^31, their cosines and sines to 2^-22.
+ * No tokens (n_tokens 0): nothing to do, whatever the pointers.
  *
  *   q          [device] dtype, element (i, h, c) at i * q_stride + h * q_head_stride + c; NULL with q_out:
  *              keys and values only (rows of a compacted cache: rot_dim 0, no weights)

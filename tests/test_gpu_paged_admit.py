@@ -100,3 +100,11 @@ def test_admission_behind_decoded_rows(cuda):
     assert dec.lens.tolist() == [25] * 3 and (dec.lens + dec.pos_offset).tolist() == [200, 201, 202]
     for b in range(3):
         assert torch.equal(_rows(dec, dec.k_cache, 1, b, 25)[:, 15:], k[b, 1, :, 10:20])
+
+
+def test_an_admission_of_no_rows(cuda):
+    dec, k, v = _decoder(cuda)
+    dec.admit(k, v, [5, 6, 7], rows=0)
+    dec.begin()
+    torch.cuda.synchronize()
+    assert dec.lens.tolist() == [1, 1, 1] and dec.positions.tolist() == [5, 6, 7]
