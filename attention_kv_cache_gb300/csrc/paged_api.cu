@@ -1,5 +1,6 @@
 // C ABI of the calls over a paged cache: argument checks and the kernels' arguments.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -41,7 +42,8 @@ kvsel_status check_attend(const kvsel_cache_desc* cache, const kvsel_paged_atten
   if (((int64_t)p->max_blocks + 1) * c.page_size >= (int64_t(1) << 31)) return KVSEL_ERR_INVALID_ARG;
   if (p->q_stride < 0 || p->q_stride % 8 != 0) return KVSEL_ERR_INVALID_ARG;
   if (!std::isfinite(p->scale) || p->scale < 0.f) return KVSEL_ERR_INVALID_ARG;
-  if (!std::isfinite(p->softcap) || p->softcap < 0.f || p->window < 0) return KVSEL_ERR_INVALID_ARG;
+  // (the kernel divides by the cap and multiplies it by log2 e, in fp32)
+  if (!(p->softcap == 0.f || (p->softcap >= FLT_MIN && p->softcap <= 0x1p127f)) || p->window < 0) return KVSEL_ERR_INVALID_ARG;
   if (c.head_dim != 64 && c.head_dim != 128) return KVSEL_ERR_UNSUPPORTED;
   // the steps of a call are numbered in 32 bits
   if ((((int64_t)p->max_blocks * c.page_size) / 32 + 2) * p->batch >= (int64_t(1) << 31)) return KVSEL_ERR_UNSUPPORTED;

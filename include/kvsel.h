@@ -601,7 +601,7 @@ typedef struct {
   int32_t max_blocks;     /* columns of the block tables >= 1, (max_blocks + 1) * P < 2^31 */
   int64_t q_stride;       /* elements between requests' queries, a multiple of 8; 0: h_q * d */
   float scale;            /* on the scores; 0: 1 / sqrt(d) */
-  float softcap;          /* c > 0, or 0: none */
+  float softcap;          /* c in [2^-126, 2^127], or 0: none */
   int32_t window;         /* rows seen, >= 1, or 0: all */
 } kvsel_paged_attend_desc;
 KVSEL_API kvsel_status kvsel_paged_attend_workspace_size(const kvsel_cache_desc* cache,

@@ -26,3 +26,18 @@ def test_a_step_of_no_tokens_has_nothing_to_append(queries, kv, cache_dtype):
     r.rot_dim = 65                                       # the descriptors are checked all the same
     with pytest.raises(K.KvselError):
         K.kvsel_rope_append(c, r, q, k, v, empty, empty, None, None, 16, q, 16, 32, stream=0)
+
+
+def _attend_size(**kw):
+    c = K.make_cache_desc(h_q=8, h_kv=2, head_dim=128, page_size=16, n_pages=4)
+    p = K.make_paged_attend_desc(batch=2, max_blocks=4, **kw)
+    n = ctypes.c_size_t(0)
+    return K.raw_call("kvsel_paged_attend_workspace_size", ctypes.byref(c), ctypes.byref(p), ctypes.byref(n))
+
+
+def test_caps_that_fp32_cannot_divide_by_are_refused():
+    """Below 2^-126 the reciprocal is infinite, and 0 of it no number; above 2^127 the cap in base 2 is infinite."""
+    for cap in (2.0 ** -127, 1e-45, 1.5 * 2.0 ** 127, math.inf, -math.inf, math.nan, -1.0):
+        assert _attend_size(softcap=cap) == K.ERR_INVALID_ARG, cap
+    for cap in (0.0, 2.0 ** -126, 2.0 ** 127):
+        assert _attend_size(softcap=cap) in (K.OK, K.ERR_CUDA), cap        # (without a GPU its SMs cannot be asked for)
