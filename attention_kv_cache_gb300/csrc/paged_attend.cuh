@@ -192,6 +192,10 @@ __device__ __forceinline__ uint32_t pack_out(const PagedArgs& a, float u, float 
 
 // First visible row of a request of n rows.
 __device__ __forceinline__ int first_row(int n, int window) { return window > 0 && n > window ? n - window : 0; }
+// Steps of a request of n rows (n may be 2^31 - 2: what is added to it is not 32-bit signed).
+__device__ __forceinline__ int steps_of(int n, int window) {
+  return (int)(((uint32_t)n + kKeys - 1) / kKeys) - first_row(n, window) / kKeys;
+}
 // First step of lane i of N over T steps.
 __device__ __forceinline__ int quotient(uint64_t x, int y) { return (x >> 32) == 0 ? (int)((uint32_t)x / (uint32_t)y) : (int)(x / y); }
 __device__ __forceinline__ int lane_begin(int i, int T, int N) { return quotient((uint64_t)i * T, N); }
@@ -214,7 +218,7 @@ __device__ int step_sums(const PagedArgs& a, int2* cum) {
       L = 0;
     }
     const int n = (int)L;
-    const int steps = (n + kKeys - 1) / kKeys - first_row(n, a.window) / kKeys;
+    const int steps = steps_of(n, a.window);
     cum[b] = make_int2(steps, n);
     sum += steps;
   }
@@ -251,7 +255,7 @@ __device__ int one_request(const PagedArgs& a, int b, int2* cum) {
     L = 0;
   }
   const int n = (int)L;
-  const int steps = (n + kKeys - 1) / kKeys - first_row(n, a.window) / kKeys;
+  const int steps = steps_of(n, a.window);
   if (threadIdx.x == 0) {
     cum[0] = make_int2(0, n);
     cum[1] = make_int2(steps, 0);
