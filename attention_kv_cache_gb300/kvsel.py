@@ -179,15 +179,21 @@ _current_stream = None      # () -> handle of torch's current stream on the curr
 
 def _find_current_stream():
     """torch.cuda.current_stream() builds a Stream object (2.8 us of a call); where torch has them, its own getters of
-    the handle take 0.2 us."""
+    the handle take 0.2 us.  They are no public names, so they are taken only where they follow a stream that is not the
+    default one (whose handle is 0, as much else is); in a capture, where no stream should be made, that waits."""
     global _current_stream
     import torch
     handle = torch.cuda.current_stream().cuda_stream          # (initialises CUDA on the first call)
-    device, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if device is not None and raw is not None and raw(device()) == handle:
-        _current_stream = lambda: raw(device())
-    else:
-        _current_stream = lambda: torch.cuda.current_stream().cuda_stream
+    if not torch.cuda.is_current_stream_capturing():
+        device, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        side = torch.cuda.Stream()
+        try:
+            with torch.cuda.stream(side):
+                follows = raw(device()) == side.cuda_stream != 0
+            follows = follows and raw(device()) == handle
+        except Exception:                                     # (other arguments than these, or no such function)
+            follows = False
+        _current_stream = (lambda: raw(device())) if follows else (lambda: torch.cuda.current_stream().cuda_stream)
     return handle
 
 
