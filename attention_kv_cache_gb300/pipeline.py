@@ -276,10 +276,18 @@ class PagedDecoder:
         if t.shape != shape or t.dtype != self.dtype or t.device != self.lens.device:
             raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}, not {shape} {self.dtype} on {self.lens.device}")
 
+    def _whole(self, text, rows: int):
+        """A window or a distance bias counts a request's rows: its text's positions only where every one has its row."""
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("an admission under a window or a distance bias reads lengths on the host: not in a capture")
+        if (text.cpu() != self.lens.cpu() + rows).any():
+            raise ValueError("a window or a distance bias over rows of a compacted cache is not one over its text's positions")
+
     def admit(self, k_out, v_out, text_lens, rows: Optional[int] = None, stream=None):
         """The first ``rows`` rows (all by default) of compacted caches [batch, n_layers, h_kv, rows, d] into pages;
         ``text_lens`` [batch] positions each request's text has, so that its next row gets the next position.
-        Rows that the requests hold already stay: the new ones come behind them.
+        Rows that the requests hold already stay: the new ones come behind them.  With a window or slopes every
+        position of a text must have its row (``text_lens`` the rows held and admitted, checked on the host).
 
         All of it runs on ``stream``, behind what torch's current stream holds by now (the buffers' first
         values, ``text_lens``); as with every call, who uses another stream next orders it behind this one."""
@@ -297,6 +305,8 @@ class PagedDecoder:
             text = torch.as_tensor(text_lens, dtype=torch.int64)
             if text.shape != (self.batch,):
                 raise ValueError(f"text_lens of {tuple(text.shape)}, not one per request of {self.batch}")
+            if self.attend.window or self.slopes is not None:
+                self._whole(text, rows)
             slots = torch.empty(n, dtype=torch.int64, device=self.device)
             self._assign(torch.full_like(self.lens, rows), slots, None, stream)
             self.pos_offset.copy_(text)                # (slots alone were assigned: positions begin with the next row)

@@ -108,3 +108,19 @@ def test_an_admission_of_no_rows(cuda):
     dec.begin()
     torch.cuda.synchronize()
     assert dec.lens.tolist() == [1, 1, 1] and dec.positions.tolist() == [5, 6, 7]
+
+
+def test_whole_texts_under_a_window(cuda):
+    dec, k, v = _decoder(cuda, window=20, slopes=torch.ones(4, device=cuda))
+    with pytest.raises(ValueError):
+        dec.admit(k, v, [38, 37, 37])
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(BUSY)
+    dec.admit(k, v, [37, 37, 37], stream=side)
+    torch.cuda.synchronize()
+    dec.begin()
+    dec.admit(k, v, torch.tensor([45, 45, 45], device=cuda), rows=7)
+    with pytest.raises(ValueError):
+        dec.admit(k, v, [45, 45, 45], rows=1)
+    torch.cuda.synchronize()
+    assert dec.lens.tolist() == [45, 45, 45] and dec.pos_offset.tolist() == [0, 0, 0]

@@ -136,3 +136,27 @@ def test_admission_checks_rows_and_texts(monkeypatch):
     assert not any(e[0].startswith("kvsel") for e in r.log)
     dec.admit(*caches(), [30, 31, 32], rows=7)
     assert sum(e[0] == "kvsel_rope_append" for e in r.log) == 6
+
+
+@pytest.mark.parametrize("kw", [dict(window=16), dict(slopes=torch.ones(8)), dict(window=16, slopes=torch.ones(8))])
+def test_a_window_over_a_compacted_cache_is_refused(monkeypatch, kw):
+    """It would count kept rows, not the positions of the text they were kept from."""
+    r = Recorder(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    dec = decoder(**kw)
+    for text in ([30, 31, 32], [20, 20, 21], torch.tensor([20, 19, 20])):
+        r.log.clear()
+        with pytest.raises(ValueError):
+            dec.admit(*caches(), text)
+        assert not any(e[0].startswith("kvsel") for e in r.log)
+    dec.admit(*caches(), [20, 20, 20])                       # whole texts
+    assert sum(e[0] == "kvsel_rope_append" for e in r.log) == 6
+    dec.lens += 25                                           # (20 rows, and 5 steps since)
+    dec.admit(*caches(), [45, 45, 45])
+    with pytest.raises(ValueError):
+        dec.admit(*caches(), [46, 45, 45])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(ValueError):
+        dec.admit(*caches(), [45, 45, 45])
+    plain = decoder()
+    plain.admit(*caches(), [30, 31, 32])                     # and neither: any text, in a capture too
