@@ -91,3 +91,31 @@ def test_the_longest_request_is_assigned(cuda):
                             lens_out, head_out, torch.empty(2, **i64), slots, pos, ids, ws)
         torch.cuda.synchronize()
         assert K.kvsel_read_device_error(ws) == K.ERR_INVALID_ARG and slots.tolist() == [-1] * 12
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_capped_scores_over_every_argument(cuda, sign):
+    """The lse of one row is its capped score: every bf16 argument from 2^-7 to 16, across the change of form at 1/4.
+
+    tanh is off by 2^-20 of itself below 1/4 and by 2^-21 above; three fp32 roundings follow (the cap in base 2, the product
+    with it and with ln 2)."""
+    from attention_kv_cache_gb300 import kvsel as K
+    x = torch.cat([(1 + torch.arange(128).float() / 128) * 2.0 ** e for e in range(-7, 4)]) * sign
+    h_q, d, P = 16, 128, 16
+    q = torch.zeros(len(x) // h_q, h_q, d)
+    q[:, :, 0] = x.reshape(-1, h_q)
+    k = torch.zeros(1, 1, P, d)
+    k[..., 0] = 1.0
+    for cap in (1.0, 8.0):                               # (a power of two: the scores are exact multiples of it)
+        qd, kd = (q * cap).bfloat16().to(cuda), k.bfloat16().to(cuda)
+        desc = K.make_cache_desc(h_q=h_q, h_kv=1, head_dim=d, page_size=P, n_pages=1)
+        p = K.make_paged_attend_desc(batch=len(q), max_blocks=1, scale=1.0, softcap=cap)
+        ws = C.workspace(K, K.kvsel_paged_attend_workspace_size(desc, p), cuda)
+        o, lse = torch.empty(len(q), h_q, d, dtype=torch.bfloat16, device=cuda), torch.empty(len(q), h_q, device=cuda)
+        K.kvsel_paged_attend(desc, p, qd, kd, kd, torch.zeros(len(q), 1, dtype=torch.int32, device=cuda),
+                             torch.ones(len(q), dtype=torch.int64, device=cuda), None, None, None, o, lse, ws)
+        torch.cuda.synchronize()
+        got, want = C.f64(lse).reshape(-1) / cap, np.tanh(C.f64(x))
+        tol = np.where(np.abs(C.f64(x)) < 0.25, 2.0 ** -20 * np.abs(want), 2.0 ** -21) + 3 * U * np.abs(want)
+        bad = ~(np.abs(got - want) <= tol)
+        assert not bad.any(), (x[bad][:5], (np.abs(got - want) / tol).max())
