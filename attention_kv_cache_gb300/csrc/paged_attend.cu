@@ -116,7 +116,7 @@ int sm_count() {
 }
 
 struct Geometry {
-  int nt, tiles, lanes, grid, by_lane, solo;
+  int sms, nt, tiles, lanes, grid, by_lane, solo;
   size_t span_off, ml_off, part_off, total;
 };
 // One CTA per SM, fewer when the bound on the steps needs fewer warps.
@@ -125,6 +125,7 @@ bool geometry(const PagedShape& p, Geometry* out) {
   if (sms <= 0) return false;
   const int G = p.h_q / p.h_kv;
   Geometry& o = *out;
+  o.sms = sms;
   o.nt = G <= 8 ? 1 : 2;
   o.tiles = (int)ceil_div(G, 8 * o.nt);
   const PagedVariant v = variant(p, o.nt);
@@ -215,10 +216,11 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   }
   TraceScope ts("paged_join", s);
   const int rows = geo.by_lane ? geo.lanes : p.batch;
-  // Requests of many pieces: a CTA of 16 warps for each head, while those are few; else a warp per head in CTAs of 4.
+  // Requests of many pieces: a CTA of 16 warps for each head, while those are at most four to an SM; else a warp per head in
+  // CTAs of 4.
   // More requests than lanes have two or three pieces each: few loads at once, few registers, all CTAs at once (256
   // requests of 1-300 rows 33.7 -> 29.7 us, of 1-4095 rows 141 -> 136).
-  const bool split = geo.lanes / rows >= kFewPieces && (int64_t)rows * p.h_q <= 4 * 152;
+  const bool split = geo.lanes / rows >= kFewPieces && (int64_t)rows * p.h_q <= 4 * geo.sms;
   using Join = void (*)(const PagedArgs, int, int);
   Join join;
   if (p.d == 64) join = split ? paged_join<64, 16, 10> : geo.by_lane ? paged_join<64, 4, 2> : paged_join<64, 4, 10>;
