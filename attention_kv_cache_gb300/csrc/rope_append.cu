@@ -97,15 +97,21 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 // multiply-add forms exactly, correct one another (Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990, whose condition is a correctly rounded reciprocal).  A product with 1 / s alone can miss a quotient
 // that lies between two e4m3 numbers, and then goes to the wrong one; plain divisions take 10 to 23 % of an append into an
-// 8-bit pool, this 1 to 5 %.  An infinite q has no residual: NaN, which the minimum makes finite, and q stays.  Scales below
-// 2^-60 (inv_res zero) leave q as it is.  The signs keep a negative zero.
+// 8-bit pool, this 1 to 5 %.  A q that is infinite (of a finite x too) has an infinite residual or none: its magnitude is
+// limited, and q stays.  Scales below 2^-60 (inv_res zero) leave q as it is.  The signs keep a negative zero.
 struct Divisor {
   F2 s, inv, inv_res;        // s, -1 / s, and -1 / s on the residual
 };
+// x with its magnitude at most 2^60; NaN is 2^60
+__device__ __forceinline__ float limited(float x) {
+  float r;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(0x1p60f));
+  return r;
+}
 __device__ __forceinline__ F2 divide_neg(F2 neg_x, const Divisor& d) {
   const F2 q = mul(neg_x, d.inv);
   const float2 r = get(fma(q, d.s, neg_x));
-  return fma(f2(fminf(r.x, 0x1p60f), fminf(r.y, 0x1p60f)), d.inv_res, q);
+  return fma(f2(limited(r.x), limited(r.y)), d.inv_res, q);
 }
 
 // A lane's 16 elements as four packed pairs of first elements and four of second ones.

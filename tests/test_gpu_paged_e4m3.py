@@ -74,3 +74,30 @@ def test_values_are_those_of_a_rounded_quotient(cuda, dtype):
     for i, pool in enumerate(pools):
         got = pool.view(torch.uint8).reshape(-1, h_kv, d)[:n].cpu()
         assert torch.equal(got, want[:, i * h_kv:(i + 1) * h_kv])
+
+
+@pytest.mark.parametrize("scale", [0.01, 1.0, 77.0, 2.0 ** -59, 2.0 ** -62, 1e-30, 2.0 ** 59, 2.0 ** 62, 1e30, -0.01])
+@pytest.mark.parametrize("turned", [False, True])
+def test_quotients_of_any_size(cuda, scale, turned):
+    """Finite values whose quotient passes fp32 end at +-448 like infinities, tiny ones at zero, and NaN stays."""
+    from attention_kv_cache_gb300 import kvsel as K
+    g = torch.Generator().manual_seed(7)
+    n, h_kv, d, P = 20, 2, 64, 16
+    big = torch.tensor([3e38, 1e38, 1e30, 449.0, 448.0, 17.0, 1.0, 1e-3, 1e-30, 1e-38, 0.0, float("inf"), float("nan")])
+    x = torch.cat([big, -big, torch.randn(d - 26, generator=g)]).bfloat16().expand(n, h_kv, d).contiguous().to(cuda)
+    pools = [C.empty_pool(2, P, h_kv, d, "row", torch.float8_e4m3fn, cuda) for _ in range(2)]
+    desc = K.make_cache_desc(h_q=h_kv, h_kv=h_kv, head_dim=d, page_size=P, n_pages=2, cache_dtype=K.DTYPE_E4M3,
+                             order=K.ORDER_ROW)
+    s = torch.full((h_kv,), scale, device=cuda)
+    zero = torch.zeros(n, dtype=torch.int64, device=cuda)              # position 0: cosines 1 and sines 0
+    freq = torch.ones(d // 2, dtype=torch.float64, device=cuda)
+    K.kvsel_rope_append(desc, K.make_rope_desc(rot_dim=0 if not turned else d, k=x, v=x), None, x, x, zero if turned else None,
+                        torch.arange(n, device=cuda), None, None, freq if turned else None, None, pools[0], pools[1], s, s)
+    torch.cuda.synchronize()
+    want = (x.float().cpu() / s.cpu()[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    for i, pool in enumerate(pools):
+        if turned and i == 0:
+            continue                                                   # (0 times an infinity is NaN in a turned pair)
+        got = pool.view(torch.uint8).reshape(-1, h_kv, d)[:n].cpu().view(torch.float8_e4m3fn).float()
+        same = (got == want) | (got.isnan() & want.isnan())
+        assert same.all(), (x.cpu()[~same][:5], got[~same][:5], want[~same][:5])
