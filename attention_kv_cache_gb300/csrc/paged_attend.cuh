@@ -31,9 +31,9 @@
 // stages 8 %.  cp.async by all lanes, rows without a source zero-filled, rather than boxes of a tensor map: the boxes
 // took 2-4 % longer, and left V rows that are not seen to be cleared by hand.
 //
-// Measured (GB300, device time, join included): 32 requests of 2048-65536 rows, 8 KV heads of 128, bf16, 647 us (4430 MB,
-// 6.8 TB/s); 1 x 131072 rows 86 us (537 MB, 6.3 TB/s); 256 requests of 1-4095 rows, e4m3, capped, window 2048, 136 us
-// (813 MB, 6.0 TB/s; 550 instructions per step of 8 KB against 512 of 16 KB); 1 x 517 rows 5.4 us (by lanes
+// Measured (GB300, device time, join included): 32 requests of 2048-65536 rows, 8 KV heads of 128, bf16, 642 us (4430 MB,
+// 6.9 TB/s); 1 x 131072 rows 86 us (537 MB, 6.3 TB/s); 256 requests of 1-4095 rows, e4m3, capped, window 2048, 137 us
+// (813 MB, 5.9 TB/s; 558 instructions per step of 8 KB against 516 of 16 KB); 1 x 517 rows 5.5 us (by lanes
 // 7.2), 16 x 800 rows 13.3 us (17.3).
 #pragma once
 

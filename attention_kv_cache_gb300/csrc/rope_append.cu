@@ -24,10 +24,10 @@
 //   - frequencies in turns are formed once per CTA, a token's slot and
 //     position are read a token ahead.
 //
-// Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 38 us (202 MB, 5.3 TB/s; the copies
-// without the arithmetic 35 us); 32768 tokens of 64 + 8 + 8 heads into e4m3, 214 us (1276 MB, 6.0 TB/s; copies alone
-// 205 us); one token 4.5 us.  With rows in registers instead (steps of 4 rows, 16 warps per SM): 52 and 288 us.  Few
-// heads leave little to a unit: 8200 tokens of 8 + 1 + 1 heads take 18 us (42 MB, 2.3 TB/s; with a unit for each kind of
+// Measured (GB300, device time): 8200 tokens of 32 + 8 + 8 heads of 128, bf16, 37 us (202 MB, 5.5 TB/s; the copies
+// without the arithmetic 35 us); 32768 tokens of 64 + 8 + 8 heads into e4m3, 208 us (1276 MB, 6.1 TB/s; copies alone
+// 205 us); one token 4.8 us.  With rows in registers instead (steps of 4 rows, 16 warps per SM): 52 and 288 us.  Few
+// heads leave little to a unit: 8200 tokens of 8 + 1 + 1 heads take 19 us (42 MB, 2.2 TB/s; with a unit for each kind of
 // row 21 us).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
