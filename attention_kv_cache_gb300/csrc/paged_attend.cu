@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(32 * WARPS) paged_join(const __grid_constant__
 #pragma unroll
       for (int i = 1; i < WARPS; ++i) take(redml[i], reinterpret_cast<const float*>(&red[i][lane]));
     }
-    const float s = den == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / den;
+    const float s = den == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / a.unit / den;
     const int64_t oh = (int64_t)b * a.h_q + h;
 #pragma unroll
     for (int e = 0; e < V; e += 2) {
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * WARPS) paged_join(const __grid_constant__
       }
       static_cast<uint32_t*>(a.o)[(oh * D + V * lane + e) / 2] = u;
     }
-    if (a.lse != nullptr && lane == 0) a.lse[oh] = lse_of(M, den, a.up);
+    if (a.lse != nullptr && lane == 0) a.lse[oh] = (M + log2f(den)) * 0.6931471805599453f;
   }
 }
 
@@ -190,7 +190,7 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.q_stride = p.q_stride;
   a.scale = p.scale;
   a.softcap = p.softcap;
-  a.up = p.cache_dtype == KVSEL_DTYPE_BF16 ? weight_up<kBf16>() : weight_up<kF16>();
+  a.unit = p.cache_dtype == KVSEL_DTYPE_BF16 ? weight_unit<kBf16>() : weight_unit<kF16>();
   a.h_q = p.h_q;
   a.h_kv = p.h_kv;
   a.G = p.h_q / p.h_kv;

@@ -12,12 +12,13 @@
 // Arithmetic: the step's rows are the M side of mma.sync m16n8k16 and 8 query heads the N side, so
 // S^T = K Q^T needs no padding at G = 8; P^T moves from the accumulator to the B operand by movmatrix, and
 // O^T += V^T P^T with V transposed by ldmatrix.  P is taken as a high and a low 16-bit part.  The softmax
-// keeps an exponent offset that moves only when a weight passes 2^lag times the largest when it last moved, so the
-// common step forms no maximum, and the sums stay in the lanes until a row ends.
-// An fp16 part is a multiple of 2^-24, so weights near 1 would leave those below 2^-25 out of O while their sum counts
-// them: a long tail behind one high score would be lost.  Over fp16 products the weights are held 2^13 times as large
-// (the offset lies 13 below the score it is taken from) and the lag is 2, so that they end at 2^15, inside fp16, and what is lost of
-// a weight is below 2^-38 of the largest.  bf16 parts have fp32's exponents: a lag of 8 and no factor.
+// keeps an exponent offset that moves only when a score passes it by 2^lag, so the common step forms no
+// maximum, and the sums stay in the lanes until a row ends.
+// The parts are of weights times a power of two, which O is divided by at the end.  An fp16 part is a multiple of 2^-24, so of
+// weights near 1 those below 2^-25 would be left out of O while their sum counts them: a long tail behind one high score
+// would be lost.  Over fp16 products the factor is 2^13 and the lag 2: weights end at 2^15, inside fp16, and what is lost of
+// one is below 2^-38 of the largest.  bf16 parts have fp32's exponents, and values up to fp32's largest: a lag of 8 and a
+// factor of 2^-8, so that none is above one.  (The factor taken by the offset instead would round every distance at 13 or 8.)
 //
 // A request cut between lanes leaves one partial (O, offset, sum) per piece, which paged_join merges; a request within
 // one lane is written at once.
@@ -33,7 +34,7 @@
 //
 // Measured (GB300, device time, join included): 32 requests of 2048-65536 rows, 8 KV heads of 128, bf16, 642 us (4430 MB,
 // 6.9 TB/s); 1 x 131072 rows 86 us (537 MB, 6.3 TB/s); 256 requests of 1-4095 rows, e4m3, capped, window 2048, 137 us
-// (813 MB, 5.9 TB/s; 558 instructions per step of 8 KB against 516 of 16 KB); 1 x 517 rows 5.5 us (by lanes
+// (813 MB, 5.9 TB/s; 566 instructions per step of 8 KB against 523 of 16 KB); 1 x 517 rows 5.5 us (by lanes
 // 7.2), 16 x 800 rows 13.3 us (17.3).
 #pragma once
 
@@ -65,7 +66,7 @@ struct PagedArgs {
   DeviceError* err;
   int64_t page_stride, head_stride, row_stride, q_stride;
   float scale, softcap;
-  float up;             // weight_up() of the kernel (paged_join's lse)
+  float unit;           // weight_unit() of the kernel (for paged_join)
   int32_t h_q, h_kv, G, P, batch, max_blocks, n_pages, window, out_f16;
   uint32_t p_mul, p_shift;   // division of a row below 2^31 by P: (mulhi(p_mul, t) + t) >> p_shift
   int32_t tiles;        // tiles of query heads per KV head
@@ -140,16 +141,11 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi) : "r"(x));
 }
 
-// Binary orders that a weight may pass the largest one by before the offset moves, and by which weights are held larger.
+// Binary orders that a score may pass the offset by before it moves, and the factor on the weights that are split.
 template <int KIND>
 __host__ __device__ constexpr float weight_lag() { return KIND == kBf16 ? 8.f : 2.f; }
 template <int KIND>
-__host__ __device__ constexpr float weight_up() { return KIND == kBf16 ? 0.f : 13.f; }
-// log sum exp from an offset (base 2) and the sum of weights held 2^up as large.  Taking that off both first keeps
-// the result exact where one score is all there is.
-__device__ __forceinline__ float lse_of(float m, float l, float up) {
-  return ((m + up) + log2f(l * __uint_as_float((uint32_t)(127 - (int)up) << 23))) * 0.6931471805599453f;
-}
+__host__ __device__ constexpr float weight_unit() { return KIND == kBf16 ? 0x1p-8f : 0x1p13f; }
 
 template <int KIND>
 __host__ __device__ constexpr int elem_bytes() { return KIND == kE4m3 ? 1 : 2; }
@@ -334,7 +330,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
     // ---- what all requests share: scales and slopes of the unit's heads (2 tq, 2 tq + 1 of each tile); in base 2, but for
     // capped scores, which get it with the cap
     const float ksc = a.scale * (a.k_scale != nullptr ? a.k_scale[g] : 1.f) * (a.softcap != 0.f ? 1.f : kLog2e);
-    const float vsc = a.v_scale != nullptr ? a.v_scale[g] : 1.f;
+    const float vsc = (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / weight_unit<KIND>();
     const float cap2 = a.softcap * kLog2e, icap = a.softcap != 0.f ? 1.f / a.softcap : 0.f;
     const bool plain = a.softcap == 0.f && a.slopes == nullptr;
     float sl[NT][2];
@@ -572,8 +568,8 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
                 s[mt][nt][e] = ok ? s[mt][nt][e] * (plain ? sc[nt][e & 1] : 1.f) : -INFINITY;
             }
         }
-        // distances to the offset; where one passes the limit the offset moves to the step's largest score
-        constexpr float kUp = weight_up<KIND>(), kLimit = kUp + weight_lag<KIND>();
+        // distances to the offset; where one passes the lag the offset moves to the step's largest score
+        constexpr float kLag = weight_lag<KIND>(), kUnit = weight_unit<KIND>();
         float z[2][NT][4], top = -INFINITY;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -584,7 +580,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
               z[mt][nt][e] = fmaf(s[mt][nt][e], mul[nt][e & 1], -mo[nt][e & 1]);
               top = fmaxf(top, z[mt][nt][e]);
             }
-        if (__any_sync(0xffffffffu, top > (fresh ? -INFINITY : kLimit))) {
+        if (__any_sync(0xffffffffu, top > (fresh ? -INFINITY : kLag))) {
           fresh = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -594,10 +590,9 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
               float mx = fmaxf(fmaxf(s[0][nt][e] * mm, s[0][nt][e + 2] * mm), fmaxf(s[1][nt][e] * mm, s[1][nt][e + 2] * mm));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              if (mx > m[nt][e] + kLimit) {
-                const float to = mx - kUp;
-                const float alpha = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - to);
-                m[nt][e] = mo[nt][e] = to;
+              if (mx > m[nt][e] + kLag) {
+                const float alpha = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mx);
+                m[nt][e] = mo[nt][e] = mx;
                 l[nt][e] *= alpha;
 #pragma unroll
                 for (int c = 0; c < KS; ++c) {
@@ -628,7 +623,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float r0, r1, d0, d1;
-              ph[mt][nt][h] = transpose8x8(pack_hi<KIND>(p[2 * h], p[2 * h + 1], r0, r1));
+              ph[mt][nt][h] = transpose8x8(pack_hi<KIND>(p[2 * h] * kUnit, p[2 * h + 1] * kUnit, r0, r1));
               pl[mt][nt][h] = transpose8x8(pack_hi<KIND>(r0, r1, d0, d1));
             }
           }
@@ -701,7 +696,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
             inv[e] = l[nt][e] == 0.f ? 0.f : vsc / l[nt][e];
             const int hl = (tile * NT + nt) * 8 + 2 * tq + e;
             if (a.lse != nullptr && gq == 0 && hl < a.G)
-              a.lse[(int64_t)now * a.h_q + g * a.G + hl] = lse_of(m[nt][e], l[nt][e], weight_up<KIND>());
+              a.lse[(int64_t)now * a.h_q + g * a.G + hl] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
           }
           // transposed back, a lane holds consecutive d of one head: 2 tq, +1 of both halves of a slice, or 4 tq .. + 3
           const int hl = (tile * NT + nt) * 8 + gq;
@@ -765,7 +760,7 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       const float inv = den == 0.f ? 0.f : vsc / den;
       const int64_t oh = (int64_t)b0 * a.h_q + g * a.G + hl;
       static_cast<uint32_t*>(a.o)[(oh * D + d) / 2] = pack_out(a, num0 * inv, num1 * inv);
-      if (a.lse != nullptr && d == 0) a.lse[oh] = lse_of(M, den, weight_up<KIND>());
+      if (a.lse != nullptr && d == 0) a.lse[oh] = (M + log2f(den)) * 0.6931471805599453f;
     }
   }
 }

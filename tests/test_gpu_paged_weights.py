@@ -120,3 +120,15 @@ def test_the_lse_of_one_page_of_equal_rows(cuda, cache, dtype):
         want = z + math.log(P)
         assert (np.abs(lse - want) <= 2.0 ** -20 * (1 + abs(want))).all(), (z, lse)
         assert (np.abs(o - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("rows_before", [64, 1000, 20000])
+def test_values_at_the_types_largest(cuda, rows_before):
+    """A weight is at most one whatever the offset was taken from: a value near bf16's largest stays finite under a later,
+    higher score (5 above the rows before it, whose weights e^-5 have values of zero)."""
+    pages = [1] * (rows_before // P) + [0]
+    v = torch.zeros(2, P, D)
+    v[0, 0] = torch.linspace(1e38, 3.3e38, D)
+    v[0, 0, 1::2] *= -1
+    check(*attend(cuda, "bf16", "bf16", pages, [0.0, 0.0, 5.0], v))
+    check(*attend(cuda, "bf16", "bf16", pages, [0.0, 0.0, 5.0], v, batch=300))
