@@ -34,6 +34,12 @@ __device__ __forceinline__ void let_later_kernels_start() { asm volatile("gridde
 // kernel and shared-memory size (paged_api.cu).
 int64_t resident_ctas(const void* kern, int threads, size_t smem);
 
+// ---- checks of the calls over a paged cache (paged_api.cu) -------------------------------
+inline bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+kvsel_status check_cache(const kvsel_cache_desc* c);
+// The e4m3 pool's scales are given exactly when it is one.
+bool scales_ok(const kvsel_cache_desc& c, const float* k_scale, const float* v_scale);
+
 // ---- page_assign.cu ----------------------------------------------------------------------
 struct AssignArgs {
   int32_t P, batch, max_blocks;

@@ -7,9 +7,6 @@
 #include "paged.cuh"
 
 namespace kvsel {
-namespace {
-
-bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 kvsel_status check_cache(const kvsel_cache_desc* c) {
   if (c == nullptr) return KVSEL_ERR_INVALID_ARG;
@@ -27,11 +24,12 @@ kvsel_status check_cache(const kvsel_cache_desc* c) {
   return KVSEL_OK;
 }
 
-// The e4m3 pool's scales are given exactly when it is one.
 bool scales_ok(const kvsel_cache_desc& c, const float* k_scale, const float* v_scale) {
   const bool want = c.cache_dtype == KVSEL_DTYPE_E4M3;
   return (k_scale != nullptr) == want && (v_scale != nullptr) == want && aligned(k_scale, 4) && aligned(v_scale, 4);
 }
+
+namespace {
 
 kvsel_status check_attend(const kvsel_cache_desc* cache, const kvsel_paged_attend_desc* p, PagedShape* out) {
   const kvsel_status st = check_cache(cache);

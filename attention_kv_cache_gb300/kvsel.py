@@ -23,7 +23,7 @@ SCORE_SOFTMAX, SCORE_LOGITS = 0, 1
 LAYERS_EACH, LAYERS_L1_MEAN, LAYERS_MAX = 0, 1, 2
 HEADS_EACH, HEADS_SUM = 0, 1
 MAX_BATCH, MAX_WINDOW, MAX_ROWS, MAX_PAGE, WS_ALIGN = 128, 64, 256, 256, 256
-DTYPE_BF16, DTYPE_F16, DTYPE_E4M3 = 0, 1, 2
+DTYPE_BF16, DTYPE_F16, DTYPE_E4M3, DTYPE_F32 = 0, 1, 2, 3
 ORDER_HEAD, ORDER_ROW = 0, 1            # order inside a page: heads outside rows, rows outside heads
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDED, ROPE_RAMP = 0, 1, 2, 3
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
@@ -90,6 +90,16 @@ class PagedAttendDesc(ctypes.Structure):
                 ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32)]
 
 
+class BeamSelectDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("beams", ctypes.c_int32), ("n_out", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("pad_token", ctypes.c_int32), ("row_stride", ctypes.c_int64)]
+
+
+class BeamReorderDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("beams", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("n_layers", ctypes.c_int32), ("layer_stride", ctypes.c_int64)]
+
+
 class TraceEntry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int64), ("ms", ctypes.c_double)]
 
@@ -126,6 +136,11 @@ def _load():
         "kvsel_paged_attend_workspace_size": (I32, [P(CacheDesc), P(PagedAttendDesc), P(SZ)]),
         "kvsel_paged_attend": (I32, [P(CacheDesc), P(PagedAttendDesc), VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ,
                                      VP]),
+        "kvsel_beam_select_workspace_size": (I32, [P(BeamSelectDesc), P(SZ)]),
+        "kvsel_beam_select": (I32, [P(BeamSelectDesc), VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
+        "kvsel_beam_reorder_workspace_size": (I32, [P(BeamReorderDesc), P(SZ)]),
+        "kvsel_beam_reorder": (I32, [P(CacheDesc), P(BeamReorderDesc), VP, VP, VP, VP, I64, VP, VP, VP, VP, VP, VP, VP, SZ,
+                                     VP]),
         "kvsel_read_device_error": (I32, [VP, VP]),
         "kvsel_noalloc_read_device_error": (I32, [VP]),
         "kvsel_selftest_bounded_wait": (I32, [VP, ctypes.c_uint32, I32, VP]),
@@ -148,7 +163,8 @@ EXPORTED = ("kvsel_workspace_size", "kvsel_score", "kvsel_score_noalloc", "kvsel
             "kvsel_aggregate", "kvsel_select", "kvsel_topk", "kvsel_compact", "kvsel_compact_layers",
             "kvsel_pagetable", "kvsel_claa_shape", "kvsel_claa_select", "kvsel_attend_workspace_size", "kvsel_attend",
             "kvsel_page_assign_workspace_size", "kvsel_page_assign", "kvsel_rope_freqs", "kvsel_rope_append",
-            "kvsel_paged_attend_workspace_size", "kvsel_paged_attend", "kvsel_read_device_error",
+            "kvsel_paged_attend_workspace_size", "kvsel_paged_attend", "kvsel_beam_select_workspace_size", "kvsel_beam_select",
+            "kvsel_beam_reorder_workspace_size", "kvsel_beam_reorder", "kvsel_read_device_error",
             "kvsel_noalloc_read_device_error", "kvsel_selftest_bounded_wait", "kvsel_status_string",
             "kvsel_version", "kvsel_trace_enable", "kvsel_trace_read", "kvsel_launch_count")
 
@@ -413,6 +429,45 @@ def kvsel_paged_attend(cache: CacheDesc, desc: PagedAttendDesc, q, k_cache, v_ca
     _check(_lib.kvsel_paged_attend(cache, desc, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                    _ptr(block_tables), _ptr(lens), _ptr(slopes), _ptr(k_scale), _ptr(v_scale),
                                    _ptr(o), _ptr(lse), _ptr(ws), nb, _stream(stream)), "kvsel_paged_attend")
+
+
+def make_beam_select_desc(*, batch: int, beams: int, n_out: int, vocab: int, dtype: int = DTYPE_BF16, row_stride: int = 0,
+                          pad_token: int = 0) -> BeamSelectDesc:
+    return BeamSelectDesc(batch, beams, n_out, vocab, dtype, pad_token, row_stride)
+
+
+def kvsel_beam_select_workspace_size(desc: BeamSelectDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kvsel_beam_select_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "kvsel_beam_select_workspace_size")
+    return n.value
+
+
+def kvsel_beam_select(desc: BeamSelectDesc, logits, scores, ended, scores_out, parents, tokens, lse, ws, ws_bytes=None,
+                      stream=None):
+    nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.kvsel_beam_select(desc, _ptr(logits), _ptr(scores), _ptr(ended), _ptr(scores_out), _ptr(parents),
+                                  _ptr(tokens), _ptr(lse), _ptr(ws), nb, _stream(stream)), "kvsel_beam_select")
+
+
+def make_beam_reorder_desc(*, batch: int, beams: int, max_blocks: int, n_layers: int = 1,
+                           layer_stride: int = 0) -> BeamReorderDesc:
+    return BeamReorderDesc(batch, beams, max_blocks, n_layers, layer_stride)
+
+
+def kvsel_beam_reorder_workspace_size(desc: BeamReorderDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kvsel_beam_reorder_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "kvsel_beam_reorder_workspace_size")
+    return n.value
+
+
+def kvsel_beam_reorder(cache: CacheDesc, desc: BeamReorderDesc, parents, lens, block_tables, free_pages, free_head,
+                       block_tables_out, lens_out, free_head_out, k_cache, v_cache, ws, ws_bytes=None, stream=None):
+    """The queue's size is that of free_pages."""
+    nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.kvsel_beam_reorder(cache, desc, _ptr(parents), _ptr(lens), _ptr(block_tables), _ptr(free_pages),
+                                   free_pages.numel(), _ptr(free_head), _ptr(block_tables_out), _ptr(lens_out),
+                                   _ptr(free_head_out), _ptr(k_cache), _ptr(v_cache), _ptr(ws), nb, _stream(stream)),
+           "kvsel_beam_reorder")
 
 
 def kvsel_read_device_error(ws, stream=None) -> int:

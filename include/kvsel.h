@@ -432,7 +432,7 @@ KVSEL_API kvsel_status kvsel_pagetable(const kvsel_desc* desc, const uint8_t* ma
  *
  * Row t of a request is row t % P of page block_table[t / P]; its slot is page * P + t % P.
  */
-enum { KVSEL_DTYPE_BF16 = 0, KVSEL_DTYPE_F16 = 1, KVSEL_DTYPE_E4M3 = 2 };
+enum { KVSEL_DTYPE_BF16 = 0, KVSEL_DTYPE_F16 = 1, KVSEL_DTYPE_E4M3 = 2, KVSEL_DTYPE_F32 = 3 };   /* F32: logits alone */
 
 #define KVSEL_PAGED_MAX_BATCH 4096
 
@@ -611,6 +611,83 @@ KVSEL_API kvsel_status kvsel_paged_attend(const kvsel_cache_desc* cache, const k
                                           const int32_t* block_tables, const int64_t* lens, const float* slopes,
                                           const float* k_scale, const float* v_scale, void* o, float* lse, void* ws,
                                           size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * kvsel_beam_select — the best continuations of every set of beams.
+ *
+ * With x the logits of beam k of a set and s_k the sum of log probabilities it has so far,
+ *   score(k, v) = s_k + x_v - log sum_u exp(x_u)
+ * An ended beam has one continuation, pad_token at s_k; its other tokens are at -inf.  A set's outputs are the n_out
+ * best of its beams * vocab continuations, best first; of equal scores the smaller beam first, in a beam the larger
+ * logit and then the smaller token.  A NaN logit counts as -inf; scores that are no finite number (a beam at -inf, whose
+ * log-sum is infinite, or whose s_k is not finite) count as -inf, and such a beam's tokens come in their order.
+ *
+ *   logits      [device] dtype, row batch * beams major: element (b, k, v) at (b * beams + k) * row_stride + v
+ *   scores      [device] fp32 [batch][beams]
+ *   ended       [device] uint8 [batch][beams], or NULL: none
+ *   scores_out  [device] fp32 [batch][n_out] out; must not overlap scores
+ *   parents     [device] int32 [batch][n_out] out: k
+ *   tokens      [device] int32 [batch][n_out] out: v
+ *   lse         [device] fp32 [batch][beams] out: log sum exp of the row, or NULL
+ *   ws          [device] workspace of kvsel_beam_select_workspace_size() bytes
+ *
+ * Scores are formed and compared in fp64, from log-sums whose exponentials are within 2^-22 each (of either sign, so that
+ * the sum of many is nearer) and are added exactly; they are rounded once.
+ */
+typedef struct {
+  int32_t batch;          /* sets >= 1; batch * beams at most KVSEL_PAGED_MAX_BATCH */
+  int32_t beams;          /* 1 .. 64 */
+  int32_t n_out;          /* 1 .. 64, at most beams * vocab */
+  int32_t vocab;          /* >= 1; beams * ceil(vocab / 8192) at most 8192 */
+  int32_t dtype;          /* KVSEL_DTYPE_BF16, KVSEL_DTYPE_F16 or KVSEL_DTYPE_F32 */
+  int32_t pad_token;      /* in [0, vocab) */
+  int64_t row_stride;     /* elements between rows, >= 0; 0: vocab */
+} kvsel_beam_select_desc;
+KVSEL_API kvsel_status kvsel_beam_select_workspace_size(const kvsel_beam_select_desc* desc, size_t* bytes);
+KVSEL_API kvsel_status kvsel_beam_select(const kvsel_beam_select_desc* desc, const void* logits, const float* scores,
+                                         const uint8_t* ended, float* scores_out, int32_t* parents, int32_t* tokens,
+                                         float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * kvsel_beam_reorder — the beams' pages after a selection.
+ *
+ * Set b's beams are requests b * beams .. + beams - 1 of the block tables.  Child j of a set goes on from beam
+ * p = parents[b][j]: it gets p's length and names p's pages.  Pages that the set named and names no more are freed, in
+ * the order (set, column, beam): put into free_pages in front of free_head.  Of the children of one parent every
+ * one but the first gets its own copy of the last page if that is part full (rows 0 .. len % P - 1 of every
+ * layer's K and V), in pages taken from the queue in the order (set, child), the freed ones first; so a page that is not
+ * full is always one beam's alone.  All parents 0 share a prompt's pages among beams that held none.
+ * Beams that share a page name it in the same column.  A page of several sets must be named by every beam of them.
+ *
+ *   cache             pools as in the other calls (head_dim any of its values); dtype is not looked at
+ *   parents           [device] int32 [batch][beams]
+ *   lens              [device] int64 [batch * beams]
+ *   block_tables      [device] int32 [batch * beams][max_blocks]
+ *   free_pages        [device] int32 [n_free], in and out
+ *   free_head         [device] int64 [1]: entries of free_pages taken so far
+ *   block_tables_out  [device] out: entries of the pages held (others are left as they were); may be block_tables
+ *   lens_out          [device] out; may be lens
+ *   free_head_out     [device] out; may be free_head
+ *   k_cache, v_cache  [device] pools of the first layer, layer l's layer_stride * l elements on
+ *   ws                [device] workspace of kvsel_beam_reorder_workspace_size() bytes
+ *
+ * A parent outside [0, beams), a length outside [0, max_blocks * P] (detail: the set's first request), a head outside the
+ * queue or with too few entries on either side (detail: batch * beams) records KVSEL_ERR_INVALID_ARG, a page id outside
+ * [0, n_pages) KVSEL_ERR_DEVICE; nothing is written then.
+ */
+typedef struct {
+  int32_t batch;          /* sets >= 1; batch * beams at most KVSEL_PAGED_MAX_BATCH */
+  int32_t beams;          /* 1 .. 64 */
+  int32_t max_blocks;     /* columns of the block tables >= 1, (max_blocks + 1) * P < 2^31 */
+  int32_t n_layers;       /* >= 1 */
+  int64_t layer_stride;   /* elements of the pool, a multiple of 16 bytes, >= 0 */
+} kvsel_beam_reorder_desc;
+KVSEL_API kvsel_status kvsel_beam_reorder_workspace_size(const kvsel_beam_reorder_desc* desc, size_t* bytes);
+KVSEL_API kvsel_status kvsel_beam_reorder(const kvsel_cache_desc* cache, const kvsel_beam_reorder_desc* desc,
+                                          const int32_t* parents, const int64_t* lens, const int32_t* block_tables,
+                                          int32_t* free_pages, int64_t n_free, const int64_t* free_head,
+                                          int32_t* block_tables_out, int64_t* lens_out, int64_t* free_head_out,
+                                          void* k_cache, void* v_cache, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * kvsel_score_noalloc — kvsel_score for callers that cannot allocate device memory.
