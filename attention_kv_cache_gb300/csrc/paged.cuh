@@ -86,11 +86,19 @@ struct PagedShape {
   float scale, softcap;
   int32_t window;
 };
+kvsel_status check_attend(const kvsel_cache_desc* cache, const kvsel_paged_attend_desc* p, PagedShape* out);   // paged_api.cu
 // Workspace bytes of a call on the current device (0: the device cannot be queried).
 size_t paged_attend_ws(const PagedShape& p);
+// With o32, fp32 [batch][h_q][d], the output goes there as it is instead of rounded to o.
 kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void* k, const void* v,
                                  const int32_t* tables, const int64_t* lens, const float* slopes,
                                  const float* k_scale, const float* v_scale, void* o, float* lse, void* ws,
-                                 cudaStream_t s);
+                                 cudaStream_t s, float* o32 = nullptr);
+// (mulhi(mul, t) + t) >> shift is t / P for rows t below 2^31.
+inline void page_division(int32_t P, uint32_t* mul, uint32_t* shift) {
+  *shift = 0;
+  while ((1 << *shift) < P) ++*shift;
+  *mul = (uint32_t)((((uint64_t)1 << 32) * ((1u << *shift) - (uint32_t)P)) / (uint32_t)P + 1);
+}
 
 }  // namespace kvsel

@@ -29,8 +29,6 @@ bool scales_ok(const kvsel_cache_desc& c, const float* k_scale, const float* v_s
   return (k_scale != nullptr) == want && (v_scale != nullptr) == want && aligned(k_scale, 4) && aligned(v_scale, 4);
 }
 
-namespace {
-
 kvsel_status check_attend(const kvsel_cache_desc* cache, const kvsel_paged_attend_desc* p, PagedShape* out) {
   const kvsel_status st = check_cache(cache);
   if (st != KVSEL_OK) return st;
@@ -64,8 +62,6 @@ kvsel_status check_attend(const kvsel_cache_desc* cache, const kvsel_paged_atten
   o.window = p->window;
   return KVSEL_OK;
 }
-
-}  // namespace
 
 int64_t resident_ctas(const void* kern, int threads, size_t smem) {
   struct Entry {

@@ -34,7 +34,8 @@ __global__ void __launch_bounds__(32 * WARPS) paged_join(const __grid_constant__
     if (h >= a.h_q) return;                         // (the whole CTA where its warps share a head)
     const int g = h / a.G;
     const int at = g * a.tiles * nt8 + (h - g * a.G);                    // the head among the padded heads
-    float M = -INFINITY, den = 0.f, num[V];
+    float M = -INFINITY, den = 0.f;
+    alignas(16) float num[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) num[e] = 0.f;
     // (offset, sum, row) taken into the warp's own; a piece whose scores were all NaN, or none, has offset -inf
@@ -73,8 +74,13 @@ __global__ void __launch_bounds__(32 * WARPS) paged_join(const __grid_constant__
     }
     const float s = den == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / a.unit / den;
     const int64_t oh = (int64_t)b * a.h_q + h;
+    if (a.o32 != nullptr) {
 #pragma unroll
-    for (int e = 0; e < V; e += 2) {
+      for (int e = 0; e < V; ++e) num[e] *= s;
+      reinterpret_cast<Vec*>(a.o32 + oh * D)[lane] = *reinterpret_cast<const Vec*>(num);
+    }
+#pragma unroll
+    for (int e = 0; e < V && a.o32 == nullptr; e += 2) {
       uint32_t u;
       if (a.out_f16) {
         const __half2 y = __floats2half2_rn(num[e] * s, num[e + 1] * s);
@@ -164,7 +170,7 @@ size_t paged_attend_ws(const PagedShape& p) {
 kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void* k, const void* v,
                                  const int32_t* tables, const int64_t* lens, const float* slopes,
                                  const float* k_scale, const float* v_scale, void* o, float* lse, void* ws,
-                                 cudaStream_t s) {
+                                 cudaStream_t s, float* o32) {
   Geometry geo;
   if (!geometry(p, &geo)) return KVSEL_ERR_CUDA;
   const PagedVariant var = variant(p, geo.nt);
@@ -179,6 +185,7 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.o = o;
+  a.o32 = o32;
   a.lse = lse;
   a.span = reinterpret_cast<int2*>(base + geo.span_off);
   a.part_ml = reinterpret_cast<float2*>(base + geo.ml_off);
@@ -195,9 +202,7 @@ kvsel_status launch_paged_attend(const PagedShape& p, const void* q, const void*
   a.h_kv = p.h_kv;
   a.G = p.h_q / p.h_kv;
   a.P = p.P;
-  a.p_shift = 0;
-  while ((1 << a.p_shift) < p.P) ++a.p_shift;
-  a.p_mul = (uint32_t)((((uint64_t)1 << 32) * ((1u << a.p_shift) - (uint32_t)p.P)) / (uint32_t)p.P + 1);
+  page_division(p.P, &a.p_mul, &a.p_shift);
   a.batch = p.batch;
   a.max_blocks = p.max_blocks;
   a.n_pages = p.n_pages;

@@ -57,6 +57,7 @@ struct PagedArgs {
   const int64_t* lens;
   const float *slopes, *k_scale, *v_scale;
   void* o;
+  float* o32;           // the output unrounded instead, or NULL
   float* lse;
   float* part;          // [2 * lanes][h_kv * tiles * 8 * NT][d]: partial O
   float2* part_ml;      // [2 * lanes][h_kv * tiles * 8 * NT]: its offset (base 2) and sum
@@ -306,8 +307,9 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
   // requests without a row: o = 0, lse = -inf
   for (int b = blockIdx.x; b < a.batch && !solo; b += gridDim.x) {
     if (cum[b].x != cum[b + 1].x) continue;
-    uint32_t* ob = reinterpret_cast<uint32_t*>(a.o) + (int64_t)b * a.h_q * (D / 2);
-    for (int x = threadIdx.x; x < a.h_q * (D / 2); x += 32 * W) ob[x] = 0u;
+    const int words = a.h_q * (a.o32 != nullptr ? D : D / 2);
+    uint32_t* ob = reinterpret_cast<uint32_t*>(a.o32 != nullptr ? a.o32 : a.o) + (int64_t)b * words;
+    for (int x = threadIdx.x; x < words; x += 32 * W) ob[x] = 0u;
     if (a.lse != nullptr)
       for (int x = threadIdx.x; x < a.h_q; x += 32 * W) a.lse[(int64_t)b * a.h_q + x] = -INFINITY;
     if (!a.by_lane && threadIdx.x == 0) a.span[b] = make_int2(0, -1);
@@ -698,6 +700,20 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
             if (a.lse != nullptr && gq == 0 && hl < a.G)
               a.lse[(int64_t)now * a.h_q + g * a.G + hl] = (m[nt][e] + log2f(l[nt][e])) * 0.6931471805599453f;
           }
+          if (a.o32 != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int hl = (tile * NT + nt) * 8 + 2 * tq + e;
+              if (hl >= a.G) continue;
+              float* orow = a.o32 + ((int64_t)now * a.h_q + g * a.G + hl) * D;
+#pragma unroll
+              for (int c = 0; c < KS; ++c) {
+                orow[16 * c + d0] = o[c][nt][e] * inv[e];
+                orow[16 * c + d1] = o[c][nt][e + 2] * inv[e];
+              }
+            }
+            continue;
+          }
           // transposed back, a lane holds consecutive d of one head: 2 tq, +1 of both halves of a slice, or 4 tq .. + 3
           const int hl = (tile * NT + nt) * 8 + gq;
           uint32_t* orow = static_cast<uint32_t*>(a.o) + ((int64_t)now * a.h_q + g * a.G + hl) * (D / 2);
@@ -759,7 +775,8 @@ __global__ void __launch_bounds__(32 * n_warps<D, KIND>(), 1) paged_attend(const
       }
       const float inv = den == 0.f ? 0.f : vsc / den;
       const int64_t oh = (int64_t)b0 * a.h_q + g * a.G + hl;
-      static_cast<uint32_t*>(a.o)[(oh * D + d) / 2] = pack_out(a, num0 * inv, num1 * inv);
+      if (a.o32 != nullptr) *reinterpret_cast<float2*>(a.o32 + oh * D + d) = make_float2(num0 * inv, num1 * inv);
+      else static_cast<uint32_t*>(a.o)[(oh * D + d) / 2] = pack_out(a, num0 * inv, num1 * inv);
       if (a.lse != nullptr && d == 0) a.lse[oh] = (M + log2f(den)) * 0.6931471805599453f;
     }
   }

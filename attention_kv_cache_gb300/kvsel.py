@@ -90,6 +90,12 @@ class PagedAttendDesc(ctypes.Structure):
                 ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32)]
 
 
+class ChunkAttendDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("max_tokens", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int32)]
+
+
 class BeamSelectDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("beams", ctypes.c_int32), ("n_out", ctypes.c_int32), ("vocab", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("pad_token", ctypes.c_int32), ("row_stride", ctypes.c_int64)]
@@ -136,6 +142,12 @@ def _load():
         "kvsel_paged_attend_workspace_size": (I32, [P(CacheDesc), P(PagedAttendDesc), P(SZ)]),
         "kvsel_paged_attend": (I32, [P(CacheDesc), P(PagedAttendDesc), VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ,
                                      VP]),
+        "kvsel_chunk_attend_workspace_size": (I32, [P(CacheDesc), P(ChunkAttendDesc), P(SZ)]),
+        "kvsel_chunk_attend": (I32, [P(CacheDesc), P(ChunkAttendDesc), VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ,
+                                     VP]),
+        "kvsel_prefix_attend_workspace_size": (I32, [P(CacheDesc), P(PagedAttendDesc), I32, P(SZ)]),
+        "kvsel_prefix_attend": (I32, [P(CacheDesc), P(PagedAttendDesc), I32, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP,
+                                      VP, SZ, VP]),
         "kvsel_beam_select_workspace_size": (I32, [P(BeamSelectDesc), P(SZ)]),
         "kvsel_beam_select": (I32, [P(BeamSelectDesc), VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
         "kvsel_beam_reorder_workspace_size": (I32, [P(BeamReorderDesc), P(SZ)]),
@@ -163,7 +175,8 @@ EXPORTED = ("kvsel_workspace_size", "kvsel_score", "kvsel_score_noalloc", "kvsel
             "kvsel_aggregate", "kvsel_select", "kvsel_topk", "kvsel_compact", "kvsel_compact_layers",
             "kvsel_pagetable", "kvsel_claa_shape", "kvsel_claa_select", "kvsel_attend_workspace_size", "kvsel_attend",
             "kvsel_page_assign_workspace_size", "kvsel_page_assign", "kvsel_rope_freqs", "kvsel_rope_append",
-            "kvsel_paged_attend_workspace_size", "kvsel_paged_attend", "kvsel_beam_select_workspace_size", "kvsel_beam_select",
+            "kvsel_paged_attend_workspace_size", "kvsel_paged_attend", "kvsel_chunk_attend_workspace_size",
+            "kvsel_chunk_attend", "kvsel_prefix_attend_workspace_size", "kvsel_prefix_attend", "kvsel_beam_select_workspace_size", "kvsel_beam_select",
             "kvsel_beam_reorder_workspace_size", "kvsel_beam_reorder", "kvsel_read_device_error",
             "kvsel_noalloc_read_device_error", "kvsel_selftest_bounded_wait", "kvsel_status_string",
             "kvsel_version", "kvsel_trace_enable", "kvsel_trace_read", "kvsel_launch_count")
@@ -429,6 +442,43 @@ def kvsel_paged_attend(cache: CacheDesc, desc: PagedAttendDesc, q, k_cache, v_ca
     _check(_lib.kvsel_paged_attend(cache, desc, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                    _ptr(block_tables), _ptr(lens), _ptr(slopes), _ptr(k_scale), _ptr(v_scale),
                                    _ptr(o), _ptr(lse), _ptr(ws), nb, _stream(stream)), "kvsel_paged_attend")
+
+
+def make_chunk_attend_desc(*, batch: int, max_blocks: int, max_tokens: int, q_stride: int = 0, scale: float = 0.0,
+                           softcap: float = 0.0, window: int = 0) -> ChunkAttendDesc:
+    return ChunkAttendDesc(batch, max_blocks, max_tokens, q_stride, scale, softcap, window)
+
+
+def kvsel_chunk_attend_workspace_size(cache: CacheDesc, desc: ChunkAttendDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kvsel_chunk_attend_workspace_size(ctypes.byref(cache), ctypes.byref(desc), ctypes.byref(n)),
+           "kvsel_chunk_attend_workspace_size")
+    return n.value
+
+
+def kvsel_chunk_attend(cache: CacheDesc, desc: ChunkAttendDesc, q, k_cache, v_cache, block_tables, lens, indptr, slopes,
+                       k_scale, v_scale, o, lse, ws, ws_bytes=None, stream=None):
+    nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.kvsel_chunk_attend(cache, desc, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(lens),
+                                   _ptr(indptr), _ptr(slopes), _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(lse), _ptr(ws),
+                                   nb, _stream(stream)), "kvsel_chunk_attend")
+
+
+def kvsel_prefix_attend_workspace_size(cache: CacheDesc, desc: PagedAttendDesc, n_groups: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kvsel_prefix_attend_workspace_size(ctypes.byref(cache), ctypes.byref(desc), n_groups, ctypes.byref(n)),
+           "kvsel_prefix_attend_workspace_size")
+    return n.value
+
+
+def kvsel_prefix_attend(cache: CacheDesc, desc: PagedAttendDesc, q, k_cache, v_cache, block_tables, lens, group_indptr,
+                        shared_lens, slopes, k_scale, v_scale, o, lse, ws, ws_bytes=None, stream=None):
+    """The number of groups is that of shared_lens."""
+    nb = ws_bytes if ws_bytes is not None else ws.numel() * ws.element_size()
+    _check(_lib.kvsel_prefix_attend(cache, desc, shared_lens.numel(), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                    _ptr(block_tables), _ptr(lens), _ptr(group_indptr), _ptr(shared_lens), _ptr(slopes),
+                                    _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(lse), _ptr(ws), nb, _stream(stream)),
+           "kvsel_prefix_attend")
 
 
 def make_beam_select_desc(*, batch: int, beams: int, n_out: int, vocab: int, dtype: int = DTYPE_BF16, row_stride: int = 0,

@@ -613,6 +613,84 @@ KVSEL_API kvsel_status kvsel_paged_attend(const kvsel_cache_desc* cache, const k
                                           size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * kvsel_chunk_attend — attention of many new tokens of each request over its rows in the pool.
+ *
+ * Request b's new tokens are indptr[b] .. indptr[b + 1] - 1 of q (kvsel_page_assign's offsets), the last
+ * n_b = indptr[b + 1] - indptr[b] of its lens[b] rows, whose K and V rows are in the pool already.  Token i of
+ * them is row p = lens[b] - n_b + i and sees rows t in [max(0, p + 1 - window), p], or all up to p without a window:
+ *   z_t = scale <q, k_t>;  with softcap c: z_t = c tanh(z_t / c);  with slopes: z_t += slope_h (t - p)
+ *   o = sum_t softmax(z)_t v_t,  lse = log sum_t exp(z_t)
+ * A prompt's chunk, a whole prompt and the tokens of a draft are such calls.  Query head h reads KV head
+ * h / (h_q / h_kv).  Rows that a token does not see take no part in its output whatever the pool holds there
+ * (infinities and NaN too), and rows of o and lse that belong to no request's tokens are left as they were.
+ *
+ *   q             [device] dtype, element (i, h, c) at i * q_stride + h * d + c, max_tokens rows
+ *   k_cache, v_cache  [device] pools
+ *   block_tables  [device] int32 [batch][max_blocks]; entries behind a request's last page are not read
+ *   lens          [device] int64 [batch], the new tokens among them
+ *   indptr        [device] int64 [batch + 1], rising, within [0, max_tokens]
+ *   slopes        [device] fp32 [h_q], or NULL
+ *   k_scale, v_scale  [device] fp32 [h_kv], both given exactly when the pool is e4m3
+ *   o             [device] dtype [max_tokens][h_q][d] out; must not overlap q
+ *   lse           [device] fp32 [max_tokens][h_q] out, or NULL
+ *   ws            [device] workspace of kvsel_chunk_attend_workspace_size() bytes; the size depends on the
+ *                 current device: query it where the call runs
+ *
+ * A length outside [0, max_blocks * P], offsets that fall or leave [0, max_tokens], or more new tokens than rows record
+ * KVSEL_ERR_INVALID_ARG (detail: the request), whose tokens are then left as they were; a page id outside
+ * [0, n_pages) records KVSEL_ERR_DEVICE (detail: the request) and its rows are left out.
+ *
+ * Arithmetic: products of 16-bit values (e4m3 values as fp16, exactly) accumulated in fp32 on the tensor cores, softmax
+ * statistics in fp32, each weight rounded once to the products' 16-bit type.  With an e4m3 pool the query row is held
+ * in fp16 scaled by a power of two of its own (2^-24 of the row's largest value).
+ */
+typedef struct {
+  int32_t batch;          /* requests: 1 .. KVSEL_PAGED_MAX_BATCH */
+  int32_t max_blocks;     /* columns of the block tables >= 1, (max_blocks + 1) * P < 2^31 */
+  int64_t max_tokens;     /* rows of q, o and lse: 0 .. 2^31 - 1, times h_q / h_kv below 2^31 */
+  int64_t q_stride;       /* elements between tokens' queries, a multiple of 8; 0: h_q * d */
+  float scale;            /* on the scores; 0: 1 / sqrt(d) */
+  float softcap;          /* c in [2^-126, 2^127], or 0: none */
+  int32_t window;         /* rows seen, >= 1, or 0: all */
+} kvsel_chunk_attend_desc;
+KVSEL_API kvsel_status kvsel_chunk_attend_workspace_size(const kvsel_cache_desc* cache,
+                                                         const kvsel_chunk_attend_desc* desc, size_t* bytes);
+KVSEL_API kvsel_status kvsel_chunk_attend(const kvsel_cache_desc* cache, const kvsel_chunk_attend_desc* desc,
+                                          const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, const int64_t* lens, const int64_t* indptr,
+                                          const float* slopes, const float* k_scale, const float* v_scale, void* o,
+                                          float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * kvsel_prefix_attend — kvsel_paged_attend for a batch whose requests share long prefixes, each read once.
+ *
+ * What it computes is kvsel_paged_attend's, of the same arguments.  Requests group_indptr[j] .. group_indptr[j + 1] - 1
+ * name the same pages for their first shared_lens[j] rows (beams of one prompt, requests behind one system prompt);
+ * of those rows the whole pages are read once for all of them, through the first one's table, and every
+ * request's other rows through its own.  A group of one request, or of no shared rows, is an ordinary request.
+ *
+ *   group_indptr  [device] int64 [n_groups + 1], rising, from 0 to batch
+ *   shared_lens   [device] int64 [n_groups]: at most the shortest length of the group
+ *   others        as kvsel_paged_attend's; ws of kvsel_prefix_attend_workspace_size() bytes
+ *
+ * Offsets that fall or do not run from 0 to batch record KVSEL_ERR_INVALID_ARG (detail: batch) and no rows count as shared; a
+ * shared length below 0 or above a member's length records it (detail: the group's first request) and the group's
+ * rows count as not shared: the output is right either way.  Other errors are kvsel_paged_attend's; those of
+ * a shared page name the group's first request.
+ *
+ * Arithmetic: kvsel_paged_attend's, the shared rows' and the own rows' parts joined in fp32.
+ */
+KVSEL_API kvsel_status kvsel_prefix_attend_workspace_size(const kvsel_cache_desc* cache,
+                                                          const kvsel_paged_attend_desc* desc, int32_t n_groups,
+                                                          size_t* bytes);
+KVSEL_API kvsel_status kvsel_prefix_attend(const kvsel_cache_desc* cache, const kvsel_paged_attend_desc* desc,
+                                           int32_t n_groups, const void* q, const void* k_cache, const void* v_cache,
+                                           const int32_t* block_tables, const int64_t* lens,
+                                           const int64_t* group_indptr, const int64_t* shared_lens,
+                                           const float* slopes, const float* k_scale, const float* v_scale, void* o,
+                                           float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * kvsel_beam_select — the best continuations of every set of beams.
  *
  * With x the logits of beam k of a set and s_k the sum of log probabilities it has so far,
