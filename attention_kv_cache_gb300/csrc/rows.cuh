@@ -24,8 +24,11 @@ struct RowsPlan {
   int64_t steps;                      // of a KV head
   int32_t n_items, n_parts;           // items; CTAs that have steps
 };
-struct RowsStart {
-  int32_t g, item, step, pad;         // where a CTA's steps begin
+struct RowsStart {                    // where a CTA's steps begin, and how many it has
+  int64_t steps;
+  int32_t g, at, step, n_items;       // KV head, item, step of it; items of the call
+  int32_t pad[2];
+  RowsItem item;
 };
 
 struct RowsArgs {
@@ -51,6 +54,7 @@ struct RowsArgs {
   int32_t h_q, h_kv, G, d, P, jobs, batch, max_blocks, n_pages, window, out_f16, prefix;
   uint32_t p_mul, p_shift;            // division of a row below 2^31 by P
   int32_t grid;                       // CTAs at most
+  int32_t box_rows;                   // rows of a box of the pools' tensor maps, 0: they have none
   int32_t max_items;
   int32_t head_rows;                  // query rows of a KV head (prefix)
   float unit, shift;                  // factor on O, and binary orders on sums, of the weights as the kernel holds them

@@ -1,6 +1,10 @@
 // Attention of many rows over a paged pool: the plan of a call's items, the merge of cut items, and the launches (the kernels
 // are in rows_attend.cuh).
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <cstring>
+#include <mutex>
 
 #include "rows_attend.cuh"
 
@@ -53,15 +57,24 @@ __device__ void finish_plan(const RowsArgs& a, int n_items, int64_t* warp_sum) {
   const int64_t W = steps * a.h_kv;
   const int N = (int)min((int64_t)a.grid, W);
   if (threadIdx.x == 0) *a.plan = RowsPlan{steps, n_items, N};
-  for (int i = threadIdx.x; i < N; i += kPlanThreads) {
-    const int64_t x = lane_begin64(i, W, N);
-    const int g = (int)(x / steps), y = (int)(x - g * steps);
-    int lo = 0, hi = n_items;                 // the last item that begins at or before y (items without steps come before it)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.items[mid].step0 <= y) lo = mid; else hi = mid;
+  for (int i = threadIdx.x; i < a.grid; i += kPlanThreads) {
+    RowsStart st = {};
+    if (i < N) {
+      const int64_t x = lane_begin64(i, W, N);
+      const int g = (int)(x / steps), y = (int)(x - g * steps);
+      int lo = 0, hi = n_items;               // the last item that begins at or before y (items without steps come before it)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.items[mid].step0 <= y) lo = mid; else hi = mid;
+      }
+      st.steps = lane_begin64(i + 1, W, N) - x;
+      st.g = g;
+      st.at = lo;
+      st.n_items = n_items;
+      st.item = a.items[lo];
+      st.step = y - st.item.step0;
     }
-    a.starts[i] = RowsStart{g, lo, y - a.items[lo].step0, 0};
+    a.starts[i] = st;
   }
 }
 
@@ -240,10 +253,10 @@ __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ R
   } else {
     const int cut = blockIdx.x + 1;
     if (cut >= N) return;
-    const RowsStart st = a.starts[cut];
+    const RowsStart& st = a.starts[cut];
     if (st.step == 0) return;
     g = st.g;
-    index = st.item;
+    index = st.at;
     if (lane_begin64(cut - 1, W, N) > g * plan.steps + a.items[index].step0) return;     // cut before, too
   }
   const RowsItem it = a.items[index];
@@ -315,6 +328,47 @@ RowsVariant variant(const RowsShape& p) {
   const bool split = p.prefix != 0;
   if (p.cache_dtype == KVSEL_DTYPE_E4M3) return rows_variant_e4m3(p.d, split);
   return p.dtype == KVSEL_DTYPE_F16 ? rows_variant_f16(p.d, split) : rows_variant_bf16(p.d, split);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// A map of a pool [page][head][row][d] in its own strides, in boxes of `rows` rows of one head: 128 bytes wide and swizzled for the
+// products, or bytes of whole rows.
+bool pool_map(const RowsShape& p, const void* pool, int rows, CUtensorMap* map) {
+  const auto fn = encoder();
+  if (fn == nullptr) return false;
+  const bool bytes = p.cache_dtype == KVSEL_DTYPE_E4M3;
+  const cuuint64_t size = bytes ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.P, (cuuint64_t)p.h_kv, (cuuint64_t)p.n_pages};
+  cuuint64_t strides[3] = {p.row_stride * size, p.head_stride * size, p.page_stride * size};
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] == 0) {
+      if (dims[i + 1] > 1) return false;          // (rows, heads or pages that are one and the same)
+      strides[i] = 16;
+    }
+  const cuuint32_t box[4] = {(cuuint32_t)(bytes ? p.d : 64), (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : p.cache_dtype == KVSEL_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(pool), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Rows of a box: the largest power of two up to 32 that divides a page, so that a box lies in one page and in one loader warp's
+// rows; pages without a factor of eight, and pools that no map describes, are copied by lanes.
+int boxes(const RowsShape& p, const void* k, const void* v, CUtensorMap* tk, CUtensorMap* tv) {
+  const int rows = std::min(32, p.P & -p.P);
+  memset(tk, 0, sizeof(*tk));
+  memset(tv, 0, sizeof(*tv));
+  return rows >= 8 && pool_map(p, k, rows, tk) && pool_map(p, v, rows, tv) ? rows : 0;
 }
 
 struct Layout {
@@ -409,7 +463,9 @@ kvsel_status launch_chunk_attend(const RowsShape& p, const RowsArgs& in, void* w
   Layout lay;
   if (!layout(p, 0, &lay)) return KVSEL_ERR_CUDA;
   const RowsVariant var = variant(p);
-  const RowsArgs a = rows_args(p, in, lay, ws);
+  RowsArgs a = rows_args(p, in, lay, ws);
+  CUtensorMap tk, tv;
+  a.box_rows = boxes(p, a.k, a.v, &tk, &tv);
   const size_t smem = sizeof(int32_t) * (2 * (size_t)a.jobs + 1);
   if (set_smem((const void*)chunk_plan, smem) != cudaSuccess || set_smem((const void*)var.kern, var.smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   kvsel_status st;
@@ -419,7 +475,7 @@ kvsel_status launch_chunk_attend(const RowsShape& p, const RowsArgs& in, void* w
   }
   {
     TraceScope ts("rows_attend", s);
-    if ((st = launch_after(var.kern, dim3(a.grid), kRowsThreads, var.smem, s, a)) != KVSEL_OK) return st;
+    if ((st = launch_after(var.kern, dim3(a.grid), kRowsThreads, var.smem, s, a, tk, tv)) != KVSEL_OK) return st;
   }
   TraceScope ts("rows_join", s);
   return launch_after(rows_join, dim3(std::max(1, a.grid - 1), p.d / kJoinValues), kItemRows, 0, s, a);
@@ -429,7 +485,9 @@ kvsel_status launch_prefix_attend(const RowsShape& p, const PagedShape& own, con
   Layout lay;
   if (!layout(p, front, &lay)) return KVSEL_ERR_CUDA;
   const RowsVariant var = variant(p);
-  const RowsArgs a = rows_args(p, in, lay, ws);
+  RowsArgs a = rows_args(p, in, lay, ws);
+  CUtensorMap tk, tv;
+  a.box_rows = boxes(p, a.k, a.v, &tk, &tv);
   const size_t smem = sizeof(int32_t) * (2 * (size_t)a.jobs + 1);
   if (set_smem((const void*)prefix_plan, smem) != cudaSuccess || set_smem((const void*)var.kern, var.smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   kvsel_status st;
@@ -439,7 +497,7 @@ kvsel_status launch_prefix_attend(const RowsShape& p, const PagedShape& own, con
   }
   {
     TraceScope ts("rows_attend", s);
-    if ((st = launch_after(var.kern, dim3(a.grid), kRowsThreads, var.smem, s, a)) != KVSEL_OK) return st;
+    if ((st = launch_after(var.kern, dim3(a.grid), kRowsThreads, var.smem, s, a, tk, tv)) != KVSEL_OK) return st;
   }
   st = launch_paged_attend(own, a.q, a.k, a.v, a.own_tables, a.own_lens, a.slopes, a.k_scale, a.v_scale, nullptr, const_cast<float*>(a.own_lse), ws, s,
                            const_cast<float*>(a.own_o));

@@ -2,14 +2,20 @@
 //
 // Both calls that have many rows for the same keys run this kernel: the new tokens of a request (kvsel_chunk_attend) and the
 // requests of a group over the prefix they share (kvsel_prefix_attend).  The query rows of a KV head are its G query heads of
-// every token (request), laid end to end; an item is up to 256 of them, two tiles of 128 that share every K and V tile, and
-// the keys that they see, in steps of 128.  All items' steps of all KV heads, laid end to end, are dealt evenly to one CTA per
-// SM; a piece is what a CTA has of an item.  Pieces that are not a whole item leave partial sums, which rows_join merges.
+// every token (request), laid end to end; an item is up to 256 of them and the keys that they see, in steps of 128.  All
+// items' steps of all KV heads, laid end to end, are dealt evenly to one CTA per SM; a piece is what a CTA has of an item.
+// Pieces that are not a whole item leave partial sums, which rows_join merges.
 //
-// Roles of the 16 warps: 0-3 and 4-7 softmax of tile A and B, a thread per query row; 8-11 load K and V; 12 issues the
+// Roles of the 16 warps: 0-3 and 4-7 softmax of tile A and B, a thread per row of the tile; 8-11 load K and V; 12 issues the
 // products.  S = Q K^T goes to TMEM; the softmax reads it, keeps an exponent offset that moves only when a row's largest
 // score passes it by 2^lag (so O is rescaled rarely) and writes the weights over S as 16-bit values, which O += P V takes from
-// TMEM with V as it lies.  P V of one tile and S of the other are issued in alternation, as the prefill kernel does.
+// TMEM with V as it lies.
+//
+// An item of more than 128 rows has them in both tiles, which share every step; P V of one and S of the other are issued in
+// alternation, as the prefill kernel does.  A smaller item has its rows in both: the tiles take steps in turn, so
+// that two chains S -> softmax -> P V -> S run at once (one alone takes 5000 cycles a step, which HBM brings in 2800).  Items of
+// up to 64 (32) rows fill the tile's 128 rows with two (four) copies, which take 64 (32) keys of a step each: the softmax of
+// a step is a thread's loop over its keys, 2000 cycles for 128.  What tiles and copies hold is merged when the piece ends.
 //
 // SPLIT (the shared prefix): weights are a high and a low 16-bit part, as in the decode kernel whose results it must match;
 // the steps wait for HBM there, so the third product is free up to 256 rows.  Without it (chunks, bound by the tensor
@@ -25,6 +31,8 @@
 // do see it by hand.
 #pragma once
 
+#include <type_traits>
+
 #include "paged_attend.cuh"
 #include "rows.cuh"
 
@@ -35,12 +43,23 @@ constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr uint32_t kHalf = 16384;                // bytes of 128 rows of 64 16-bit values
 template <int D>
 __host__ __device__ constexpr uint32_t rows_tile_bytes() { return D / 64 * kHalf; }
-// shared memory: Q_A | Q_B | K stages | V stages, then barriers and the steps' words
-template <int D>
-__host__ __device__ constexpr uint32_t rows_bar_off() { return 6 * rows_tile_bytes<D>(); }
-constexpr uint32_t kRowsBars = 16;
-template <int D>
-constexpr size_t rows_smem() { return rows_bar_off<D>() + kRowsBars * 8 + 64 + 2 * 4 * 16 + 1024; }
+// K and V tiles of the steps, in turn, as the products read them: as many as shared memory holds.  An e4m3 pool's bytes land
+// in a ring of their own, four tiles.
+template <int D, int KIND>
+__host__ __device__ constexpr int rows_slots() { return D == 64 ? 8 : KIND == kE4m3 ? 3 : 5; }
+constexpr int kRawTiles = 4;
+// shared memory: Q_A | Q_B (and the merge's buffers) | slots | bytes of an e4m3 pool | barriers and the steps' words
+template <int D, int KIND>
+__host__ __device__ constexpr uint32_t rows_raw_off() { return (2 + rows_slots<D, KIND>()) * rows_tile_bytes<D>(); }
+template <int D, int KIND>
+__host__ __device__ constexpr uint32_t rows_bar_off() { return rows_raw_off<D, KIND>() + (KIND == kE4m3 ? kRawTiles * kTileKeys * D : 0); }
+template <int D, int KIND>
+constexpr size_t rows_smem() { return rows_bar_off<D, KIND>() + 1024 + 1024; }
+// barriers: full and empty of the slots, then of the tiles s_full, p_full, pv_done and q_full, the merge's, of the loader
+// warps one each for rows that are looked at before they count, and one each per raw tile
+constexpr int kBarEmpty = 8, kBarTiles = 16, kBarMerge = 24, kBarDrain = 25, kBarLand = 26, kBarRaw = 30, kRowsBars = kBarRaw + 4 * kRawTiles;
+constexpr uint32_t kWordsOff = 512;              // behind the barriers: misc, then the words of 8 steps twice
+static_assert(kRowsBars * 8 <= kWordsOff, "barriers lie before the words");
 
 enum : uint32_t { kRowsLoader = 21, kRowsMma = 22, kRowsSoftmax = 23, kRowsDrain = 24 };
 
@@ -69,6 +88,13 @@ __device__ __forceinline__ void rows_fail(const RowsArgs& a, volatile uint32_t* 
   *flag = 1;
 }
 
+// A box of `rows` rows of one head of one page (the map says how many, and 128 bytes or all of a row) from element x of the rows.
+__device__ __forceinline__ void rows_box(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar)
+               : "memory");
+}
+
 // The pieces of a CTA, in order: every role walks them by itself.
 struct RowsPiece {
   const RowsItem* item;
@@ -77,31 +103,32 @@ struct RowsPiece {
   __device__ bool ends() const { return s1 == item->steps; }
 };
 struct RowsWalk {
-  int64_t x, x1;
+  int64_t left;
   int32_t g, at, s, n_items;
-  __device__ void begin(const RowsArgs& a, int cta, int64_t W, int N) {
-    n_items = a.plan->n_items;
-    x = lane_begin64(cta, W, N);
-    x1 = lane_begin64(cta + 1, W, N);
-    const RowsStart st = a.starts[cta];
+  const RowsItem* item;          // the first piece's is kept with the CTA's start
+  __device__ void begin(const RowsStart& st) {
+    left = st.steps;
+    n_items = st.n_items;
     g = st.g;
-    at = st.item;
+    at = st.at;
     s = st.step;
+    item = &st.item;
   }
   __device__ bool next(const RowsArgs& a, RowsPiece& p) {
-    if (x >= x1) return false;
-    for (;;) {
+    if (left <= 0) return false;
+    while (item == nullptr) {
       if (at == n_items) at = 0, ++g;
-      p.item = a.items + at;
-      if (p.item->steps > 0) break;            // (the x left says that there is one)
-      ++at;
+      if (a.items[at].steps > 0) item = a.items + at;       // (the steps left say that there is one)
+      else ++at;
     }
+    p.item = item;
     p.g = g;
     p.s0 = s;
-    p.s1 = (int)min((int64_t)p.item->steps, s + (x1 - x));
-    x += p.s1 - s;
+    p.s1 = (int)min((int64_t)item->steps, s + left);
+    left -= p.s1 - s;
     s = 0;
     ++at;
+    item = nullptr;
     return true;
   }
 };
@@ -154,14 +181,35 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float rows_max64(const float* v) {
-  float mp[8];
+template <int N>
+__device__ __forceinline__ float rows_max(const float* v) {
+  float m[N / 8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < N / 8; ++k) {
     const float* c = v + 8 * k;
-    mp[k] = fmaxf(max3(max3(c[0], c[1], c[2]), c[3], c[4]), max3(c[5], c[6], c[7]));
+    m[k] = fmaxf(max3(max3(c[0], c[1], c[2]), c[3], c[4]), max3(c[5], c[6], c[7]));
   }
-  return max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+#pragma unroll
+  for (int k = N / 16; k > 0; k /= 2)
+#pragma unroll
+    for (int i = 0; i < k; ++i) m[i] = fmaxf(m[i], m[i + k]);
+  return m[0];
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+               "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float* v) {
+  uint32_t r[16];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+                 "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 template <int KIND>
 __device__ __forceinline__ uint32_t pack16(float x, float y) {
@@ -169,24 +217,25 @@ __device__ __forceinline__ uint32_t pack16(float x, float y) {
   return pack_hi<KIND>(x, y, a, b);
 }
 
-// Weights of 64 scores, 2^(mul z - m) times the factor, as 16-bit pairs: hi (and lo with SPLIT); returns their sum.
+// Weights of N scores, 2^(mul z - m) times the factor, as 16-bit pairs: hi (and lo with SPLIT); returns their sum.
 // Without SPLIT the factor is in `nm` and the sum, and `hi` may be the scores' own registers (word c is written after v[2 c]
 // and v[2 c + 1] are read).
-template <int KIND, bool SPLIT>
+template <int KIND, bool SPLIT, int N>
 __device__ __forceinline__ float rows_weights(const float* v, float mul, float nm, uint32_t* hi, uint32_t* lo) {
   const float2 m2 = make_float2(mul, mul), n2 = make_float2(nm, nm);
   float2 sp[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) sp[k] = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
+  for (int c = 0; c < N / 2; ++c) {
     const float2 t = __ffma2_rn(make_float2(v[2 * c], v[2 * c + 1]), m2, n2);
     const float2 p = make_float2(ex2(t.x), ex2(t.y));
     sp[c & 3] = __fadd2_rn(sp[c & 3], p);
     if constexpr (SPLIT) {
       constexpr float unit = weight_unit<KIND>();
+      const float2 w = __fmul2_rn(p, make_float2(unit, unit));
       float r0, r1;
-      hi[c] = pack_hi<KIND>(p.x * unit, p.y * unit, r0, r1);
+      hi[c] = pack_hi<KIND>(w.x, w.y, r0, r1);
       lo[c] = pack16<KIND>(r0, r1);
     } else {
       hi[c] = pack16<KIND>(p.x, p.y);
@@ -196,52 +245,194 @@ __device__ __forceinline__ float rows_weights(const float* v, float mul, float n
   return s.x + s.y;
 }
 
+// A row's scores as they are compared, from the products: with a cap c z' = c tanh(z / c), a bias slope (t - p), in base 2.
+struct RowsScore {
+  float sc, icap, cap2, slope;        // sc: scale with log2 e, or with a cap scale / cap alone (icap is that then)
+  bool capped;
+};
+// z[0 .. N) of the keys whose distances to the row's own begin at d0; those whose bit of `see` is off at -inf.
+template <int N>
+__device__ __forceinline__ void rows_scores(float* z, const RowsScore& k, float d0, const uint32_t* see, bool general, bool whole) {
+  if (general) {
+    const float2 sl = make_float2(k.slope, k.slope);
+    if (k.capped) {
+      const float2 ic = make_float2(k.icap, k.icap), cp = make_float2(k.cap2, k.cap2);
+      float big = 0.f;
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const float2 x = __fmul2_rn(make_float2(z[c], z[c + 1]), ic);
+        z[c] = x.x;
+        z[c + 1] = x.y;
+        big = max3(big, fabsf(x.x), fabsf(x.y));
+      }
+      // (scores far below the cap are the rule: the series alone, as tanh_fast has it below 1/4)
+      if (__all_sync(0xffffffffu, big < 0.25f)) {
+        const float2 c3 = make_float2(-17.f / 315.f, -17.f / 315.f), c2 = make_float2(2.f / 15.f, 2.f / 15.f),
+                     c1 = make_float2(-1.f / 3.f, -1.f / 3.f), one = make_float2(1.f, 1.f);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+          const float2 x = make_float2(z[c], z[c + 1]), x2 = __fmul2_rn(x, x);
+          const float2 y = __fmul2_rn(__fmul2_rn(x, cp), __ffma2_rn(x2, __ffma2_rn(x2, __ffma2_rn(x2, c3, c2), c1), one));
+          z[c] = y.x;
+          z[c + 1] = y.y;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) z[c] = k.cap2 * tanh_fast(z[c]);
+      }
+    } else {
+      const float2 s2 = make_float2(k.sc, k.sc);
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const float2 y = __fmul2_rn(make_float2(z[c], z[c + 1]), s2);
+        z[c] = y.x;
+        z[c + 1] = y.y;
+      }
+    }
+    if (k.slope != 0.f) {
+      const float2 dd = make_float2(d0, d0 + 1.f);
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const float2 y = __ffma2_rn(sl, __fadd2_rn(dd, make_float2((float)c, (float)c)), make_float2(z[c], z[c + 1]));
+        z[c] = y.x;
+        z[c + 1] = y.y;
+      }
+    }
+  }
+  if (!whole) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) z[c] = (see[c / 32] >> (c & 31)) & 1u ? z[c] : -INFINITY;
+  }
+}
+
+// One step of a thread's row: weights of its 32 NB keys, from TMEM column `s` + 32 NB `copy` on, written over S (zeros in
+// the other copies' places); updates the offset m, mo, the sum l; returns the factor on what O holds.
+template <int KIND, bool SPLIT, int NB>
+__device__ __forceinline__ float rows_step(uint32_t s, int copy, const RowsScore& k, float d0, const uint32_t* see, bool general, bool whole,
+                                           float& m, float& mo, float& l) {
+  using namespace sm100;
+  constexpr float kShift = SPLIT ? 0.f : (KIND == kBf16 ? -8.f : 13.f), kLag = weight_lag<KIND>();
+  const float mul = general ? 1.f : k.sc;
+  float alpha = 1.f, sum;
+  auto offset = [&](float mt) {                         // where a score passes the lag, the offset moves to the largest
+    if (mt > m + kLag) {
+      if (m != -INFINITY) alpha = ex2(m - mt);          // (nothing to rescale before the first)
+      m = mo = mt;
+    }
+  };
+  if constexpr (NB == 4 && SPLIT) {
+    // the first half is read twice, so that a thread never holds both and their parts
+    uint32_t r[64], hi[32], lo[32];
+    float* z = reinterpret_cast<float*>(r);
+    tmem_ld64_async(s, r);
+    tmem_wait_ld64(r);
+    rows_scores<64>(z, k, d0, see, general, whole);
+    const float m0 = rows_max<64>(z);
+    tmem_ld64_async(s + 64, r);
+    tmem_wait_ld64(r);
+    rows_scores<64>(z, k, d0 + 64.f, see + 2, general, whole);
+    offset(fmaxf(m0, rows_max<64>(z)) * mul);           // (mul > 0: the largest stays the largest)
+    sum = rows_weights<KIND, true, 64>(z, mul, kShift - mo, hi, lo);
+    tmem_st32(s + 96, lo);
+    tmem_ld64_async(s, r);
+    tmem_wait_ld64(r);
+    tmem_st32(s + 32, hi);
+    rows_scores<64>(z, k, d0, see, general, whole);
+    sum += rows_weights<KIND, true, 64>(z, mul, kShift - mo, hi, lo);
+    tmem_st32(s + 64, lo);
+    tmem_st32(s, hi);
+  } else if constexpr (NB == 4) {
+    uint32_t rv[64], rw[64];
+    tmem_ld64_async(s + 64, rv);
+    tmem_ld64_async(s, rw);
+    tmem_wait_ld64(rv);                                 // one wait covers both loads
+    reg_tie64(rw);
+    float* v = reinterpret_cast<float*>(rv);
+    float* u = reinterpret_cast<float*>(rw);
+    rows_scores<64>(u, k, d0, see, general, whole);
+    rows_scores<64>(v, k, d0 + 64.f, see + 2, general, whole);
+    offset(fmaxf(rows_max<64>(u), rows_max<64>(v)) * mul);
+    sum = rows_weights<KIND, false, 64>(u, mul, kShift - mo, rw, nullptr);
+    tmem_st32(s, rw);
+    sum += rows_weights<KIND, false, 64>(v, mul, kShift - mo, rv, nullptr);
+    tmem_st32(s + 32, rv);
+  } else {
+    constexpr int N = 32 * NB;
+    float z[N];
+    uint32_t hi[N / 2], lo[N / 2], zero[N / 2];
+#pragma unroll
+    for (int c = 0; c < N / 2; ++c) zero[c] = 0u;
+    if constexpr (NB == 1) {
+      tmem_ld32(s + 32 * copy, z);
+    } else {
+      tmem_ld64(s + 64 * copy, z);
+    }
+    rows_scores<N>(z, k, d0 + (float)(N * copy), see, general, whole);
+    offset(rows_max<N>(z) * mul);
+    sum = rows_weights<KIND, SPLIT, N>(z, mul, kShift - mo, hi, lo);
+#pragma unroll
+    for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+      for (int j = 0; j < 4 / NB; ++j) {
+        const uint32_t at = s + 64 * part + 16 * NB * ((copy + j) & (4 / NB - 1));
+        const uint32_t* from = j != 0 ? zero : part ? lo : hi;
+        if constexpr (NB == 1) tmem_st16(at, from);
+        else tmem_st32(at, from);
+      }
+  }
+  l = l * alpha + sum;
+  return alpha;
+}
+
 template <int D, int KIND, bool SPLIT>
-__global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensorMap tk,
+                                                               const __grid_constant__ CUtensorMap tv) {
   using namespace sm100;
   constexpr uint32_t TB = rows_tile_bytes<D>();
-  constexpr int RB = row_bytes<D, KIND>(), CPR = RB / 16;
+  constexpr int RB = row_bytes<D, KIND>(), CPR = RB / 16, NS = rows_slots<D, KIND>();
   // TMEM: tile X in {0, 1}: S (the weights over it) at 256 X, O at 256 X + 128
   constexpr uint32_t kSCol = 0, kOCol = 128, kTileCols = 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t base = smem_addr(sbase), bars = base + rows_bar_off<D>();
-  const uint32_t kOff = 2 * TB, vOff = 4 * TB;
-  auto k_full = [&](int s) { return bars + 8u * s; };
-  auto k_empty = [&](int s) { return bars + 8u * (2 + s); };
-  auto v_full = [&](int s) { return bars + 8u * (4 + s); };
-  auto v_empty = [&](int s) { return bars + 8u * (6 + s); };
-  auto s_full = [&](int x) { return bars + 8u * (8 + x); };
-  auto p_full = [&](int x) { return bars + 8u * (10 + x); };
-  auto pv_done = [&](int x) { return bars + 8u * (12 + x); };
-  auto q_full = [&](int x) { return bars + 8u * (14 + x); };
-  uint32_t* misc = reinterpret_cast<uint32_t*>(sbase + rows_bar_off<D>() + kRowsBars * 8);
+  const uint32_t base = smem_addr(sbase), bars = base + rows_bar_off<D, KIND>(), slots = base + 2 * TB;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  // tile q (K of step q / 2, V after it) of the CTA: its slot's barriers and the parity of its use
+  auto full = [&](uint32_t q) { return bar(q % NS); };
+  auto empty = [&](uint32_t q) { return bar(kBarEmpty + q % NS); };
+  auto use = [&](uint32_t q) { return (q / NS) & 1; };
+  auto s_full = [&](int x) { return bar(kBarTiles + x); };
+  auto p_full = [&](int x) { return bar(kBarTiles + 2 + x); };
+  auto pv_done = [&](int x) { return bar(kBarTiles + 4 + x); };
+  auto q_full = [&](int x) { return bar(kBarTiles + 6 + x); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sbase + rows_bar_off<D, KIND>() + kWordsOff);
   uint32_t* tslot = misc;
   volatile uint32_t* flag = misc + 1;
   volatile uint32_t* o_begun = misc + 2;           // [2]: O of the piece holds values before its first product
-  const uint32_t drain = smem_addr(misc + 4);      // (8-byte aligned)
-  uint32_t* seen_w = misc + 16;                    // [4][4]: rows of a step that were loaded, by steps of the CTA modulo 4
-  uint32_t* bad_w = misc + 32;                     // [4][4]: rows whose V is not finite, where that matters
+  // [8][4] each, by steps of the CTA modulo 8: rows that were loaded and are seen by some row; rows whose V is not finite, where
+  // that matters
+  uint32_t *seen_w = misc + 16, *bad_w = misc + 48;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   wait_for_earlier_kernels();
   let_later_kernels_start();
-  const int64_t W = a.plan->steps * a.h_kv;
-  const int N = (int)min((int64_t)a.grid, W), cta = blockIdx.x;
-  if (cta >= N) return;
+  const int cta = blockIdx.x;
+  const RowsStart& start = a.starts[cta];
+  if (start.steps <= 0) return;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(k_full(s), 4);                     // one arrival per loader warp
-      mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 4);
-      mbar_init(v_empty(s), 1);
-      mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 4);                     // one arrival per softmax warp of the tile
-      mbar_init(pv_done(s), 1);
-      mbar_init(q_full(s), 4);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(i), 4);                        // one arrival per loader warp
+      mbar_init(bar(kBarEmpty + i), 1);
     }
-    mbar_init(drain, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full(x), 1);
+      mbar_init(p_full(x), 4);                     // one arrival per softmax warp of the tile
+      mbar_init(pv_done(x), 1);
+      mbar_init(q_full(x), 4);
+    }
+    mbar_init(bar(kBarMerge), 8);
+    mbar_init(bar(kBarDrain), 1);
+    for (int i = kBarLand; i < kRowsBars; ++i) mbar_init(bar(i), 1);
     *flag = 0;
     o_begun[0] = o_begun[1] = 0;
     fence_barrier_init();
@@ -260,28 +451,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
 
   if (warp >= 8 && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegLoad));
-    walk.begin(a, cta, W, N);
+    walk.begin(start);
     // ---------------------------------------------------------------- loaders: rows 32 w .. 32 w + 31 of every step
     const int w = warp - 8;
-    // a step to load: this lane's row of it
+    constexpr int KPI = 32 / CPR;                  // rows that 32 lanes take 16 bytes of
+    const int c = lane % CPR;
+    const int R = a.box_rows;                      // rows of a box, 0: the pool's pages do not fall into boxes
+    // a step to load: this lane's row of it; the page's entry is read ahead, nothing waits for it here
     struct Row {
-      int32_t id, within, g, table, t0;
-      bool need, check, more;
+      int32_t id, within, g, table;
+      uint32_t flags;                              // there is a step; this row is needed; its box is; some row needs looking at
     };
+    enum : uint32_t { kMore = 1, kNeed = 2, kBox = 4, kPartial = 8 };
     bool have = walk.next(a, p);
     int s = have ? p.s0 : 0;
     auto look = [&]() -> Row {
-      Row r{0, 0, 0, 0, 0, false, false, false};
+      Row r{0, 0, 0, 0, 0};
       if (!have) return r;
       const RowsItem& it = *p.item;
-      r.more = true;
-      r.t0 = it.k0 + kTileKeys * s;
-      const int t = r.t0 + 32 * w + lane;
-      r.need = t >= it.lo && t < it.hi;
+      const int t0 = it.k0 + kTileKeys * s, t = t0 + 32 * w + lane, tb = R != 0 ? t & ~(R - 1) : t;
+      r.flags = kMore | (t >= it.lo && t < it.hi ? kNeed : 0u) | (tb < it.hi && tb + max(R, 1) > it.lo ? kBox : 0u) |
+                (t0 < it.lo || t0 + kTileKeys > it.hi || rows_partial(it.lo, it.hi, it.full_lo, it.full_hi, t0) ? kPartial : 0u);
       r.g = p.g;
       r.table = it.table;
-      r.check = rows_partial(it.lo, it.hi, it.full_lo, it.full_hi, r.t0);
-      if (r.need) {
+      if (r.flags & kBox) {
         const int blk = (int)((__umulhi(a.p_mul, (uint32_t)t) + (uint32_t)t) >> a.p_shift);
         r.within = t - blk * a.P;
         r.id = a.tables[(int64_t)it.table * a.max_blocks + blk];
@@ -292,192 +485,295 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
       }
       return r;
     };
+    // the row's entry names a page of the pool
+    auto known = [&](const Row& r) {
+      const bool in = r.id >= 0 && r.id < a.n_pages;
+      if ((r.flags & kNeed) && !in) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)r.table);
+      return in;
+    };
+    auto await = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, rows_wait(b, parity, flag)); };
+    auto slot_chunk = [&](uint32_t q, int x, int cc) {         // of row x of this warp's, 16-byte chunk cc of 16-bit values
+      return 2 * TB + (q % NS) * TB + (cc >> 3) * kHalf + (32 * w + x) * 128 + (((cc & 7) ^ (x & 7)) << 4);
+    };
+    // the boxes of a tile's rows (those of `boxes`, by first row), 128 bytes of them at a time into a slot, or whole into `dst`
+    auto load_boxes = [&](const Row& r, uint32_t boxes, const CUtensorMap* map, uint32_t dst, uint32_t b) {
+      constexpr int HALVES = KIND == kE4m3 ? 1 : D / 64;
+      const uint32_t bytes = __popc(boxes) * R * RB;
+      if (lane == 0) {
+        if (bytes != 0) mbar_expect_tx(b, bytes);
+        else mbar_arrive(b);
+      }
+      __syncwarp();
+      if ((boxes >> lane) & 1u)
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+          rows_box(dst + h * kHalf + lane * (KIND == kE4m3 ? RB : 128), map, 64 * h, r.within, r.g, r.id, b);
+    };
+    // 16-bit rows in a slot: those not in `rows` become zeros, and values that are not finite do in the others; which rows had such
+    auto clean = [&](uint32_t q, uint32_t rows) -> uint32_t {
+      uint32_t bad = 0;
+#pragma unroll 1
+      for (int i = 0; i < 32 / KPI; ++i) {
+        const int x = i * KPI + lane / CPR;
+        uint4* at = reinterpret_cast<uint4*>(sbase + slot_chunk(q, x, c));
+        uint4 y = *at;
+        uint32_t* h = reinterpret_cast<uint32_t*>(&y);
+        constexpr uint32_t ex = KIND == kBf16 ? 0x7f80u : 0x7c00u;
+        bool hit = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((h[e] & ex) == ex) h[e] &= 0xffff0000u, hit = true;
+          if ((h[e] & (ex << 16)) == (ex << 16)) h[e] &= 0xffffu, hit = true;
+        }
+        if (!((rows >> x) & 1u)) *at = make_uint4(0, 0, 0, 0);
+        else if (hit) *at = y, bad |= 1u << x;
+      }
+      return __reduce_or_sync(0xffffffffu, bad);
+    };
+    auto told = [&](uint32_t q) {                  // this warp's rows of tile q are there
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(q));
+    };
     bool ok = true;
-    Row next = look();
-    if constexpr (KIND != kE4m3) {
-      uint32_t issued = 0, told = 0, check = 0;      // tiles (K and V of every step in turn); bit i & 7: V to be checked
-      // the oldest tile not told of is there: fence, arrive
-      auto tell = [&]() {
-        switch (issued - told) {                     // (cp.async groups may end in order only)
+    uint32_t boxed = 0, n_land = 0;                // tiles whose boxes were asked for, and those that were looked at first
+    constexpr int AHEAD = 2;                       // steps whose pages are looked up ahead
+    Row rows[AHEAD + 1];
+#pragma unroll
+    for (int i = 0; i <= AHEAD; ++i) rows[i] = look();
+    auto shift = [&]() {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) rows[i] = rows[i + 1];
+      rows[AHEAD] = look();
+    };
+    if (KIND != kE4m3 && R != 0) {
+      for (uint32_t step = 0; (rows[0].flags & kMore) && ok; ++step) {
+        const Row& r = rows[0];
+        const bool in = known(r), partial = r.flags & kPartial;
+        const uint32_t fine = __ballot_sync(0xffffffffu, in && (r.flags & kNeed));
+        const uint32_t boxes = __ballot_sync(0xffffffffu, in && (r.flags & kBox) && (lane & (R - 1)) == 0);
+        ok = await(empty(2 * step), use(2 * step) ^ 1);
+        if (!ok) break;
+        if (lane == 0) seen_w[(step & 7) * 4 + w] = fine;
+        load_boxes(r, boxes, &tk, slots + (2 * step) % NS * TB + 32 * w * 128, full(2 * step));
+        const uint32_t q = 2 * step + 1;
+        boxed = q;
+        ok = await(empty(q), use(q) ^ 1);
+        if (!ok) break;
+        const uint32_t dst = slots + q % NS * TB + 32 * w * 128;
+        boxed = q + 1;
+        if (partial) {
+          load_boxes(r, boxes, &tv, dst, bar(kBarLand + w));
+          ok = await(bar(kBarLand + w), n_land++ & 1);
+          if (!ok) break;
+          const uint32_t bad = clean(q, fine);
+          if (lane == 0) bad_w[(step & 7) * 4 + w] = bad;
+          told(q);
+        } else {
+          if (fine != 0xffffffffu) {               // (pages outside the pool)
+            clean(q, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          load_boxes(r, boxes, &tv, dst, full(q));
+        }
+        shift();
+      }
+    } else if (KIND != kE4m3) {
+      // cp.async, whole rows at a time, rows without a source as zeros
+      uint32_t issued = 0, done = 0, check = 0;    // tiles; bit i & 7: V to be looked at
+      auto tell = [&]() {                          // the oldest tile not told of is there (copies end in order only)
+        switch (issued - done) {
           case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
           case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
           case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
           default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
         }
-        const uint32_t step = told >> 1, stage = step & 1;
-        if ((told & 1) && ((check >> (told & 7)) & 1)) {
-          // what this lane copied is searched for values that are not finite, 0 in their place
-          constexpr int KPI = 32 / CPR;
-          const int c = lane % CPR;
-          uint32_t bad = 0;
-#pragma unroll 1
-          for (int i = 0; i < 32 / KPI; ++i) {
-            const int x = i * KPI + lane / CPR;
-            uint4* at = reinterpret_cast<uint4*>(sbase + vOff + stage * TB + (c >> 3) * kHalf + (32 * w + x) * 128 + (((c & 7) ^ (x & 7)) << 4));
-            uint4 y = *at;
-            uint32_t* h = reinterpret_cast<uint32_t*>(&y);
-            constexpr uint32_t ex = KIND == kBf16 ? 0x7f80u : 0x7c00u;
-            bool hit = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((h[e] & ex) == ex) h[e] &= 0xffff0000u, hit = true;
-              if ((h[e] & (ex << 16)) == (ex << 16)) h[e] &= 0xffffu, hit = true;
-            }
-            if (hit) *at = y, bad |= 1u << x;
-          }
-          bad = __reduce_or_sync(0xffffffffu, bad);
-          if (lane == 0) bad_w[(step & 3) * 4 + w] = bad;
+        if ((done & 1) && ((check >> (done & 7)) & 1)) {
+          const uint32_t bad = clean(done, 0xffffffffu);
+          if (lane == 0) bad_w[((done >> 1) & 7) * 4 + w] = bad;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive((told & 1) ? v_full(stage) : k_full(stage));
-        ++told;
+        told(done);
+        ++done;
       };
-      while (next.more && ok) {
-        const Row r = next;
-        const bool fine = r.need && r.id >= 0 && r.id < a.n_pages;
-        if (r.need && !fine) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)r.table);
+      while ((rows[0].flags & kMore) && ok) {
+        const Row& r = rows[0];
+        const bool fine = known(r) && (r.flags & kNeed);
         const int64_t off = (fine ? (int64_t)r.id * a.page_stride + (int64_t)r.within * a.row_stride : 0) * 2;
-        const uint32_t rows = __ballot_sync(0xffffffffu, fine);
-        next = look();
+        const uint32_t there = __ballot_sync(0xffffffffu, fine);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t step = issued >> 1, stage = step & 1, parity = ((step >> 1) & 1) ^ 1;
-          const uint32_t empty = kv ? v_empty(stage) : k_empty(stage);
-          while (!__all_sync(0xffffffffu, rows_test(empty, parity))) {
-            if (issued != told) tell();
-            else {
-              ok = __all_sync(0xffffffffu, rows_wait(empty, parity, flag));
-              if (!ok) break;
-            }
+          while (issued - done == 4 || !__all_sync(0xffffffffu, rows_test(empty(issued), use(issued) ^ 1))) {
+            if (issued != done) tell();
+            else if (!(ok = await(empty(issued), use(issued) ^ 1))) break;
           }
           if (!ok) break;
-          if (kv == 0 && lane == 0) {
-            seen_w[(step & 3) * 4 + w] = rows;
-            bad_w[(step & 3) * 4 + w] = 0;
-          }
+          if (kv == 0 && lane == 0) seen_w[((issued >> 1) & 7) * 4 + w] = there;
           const uint8_t* from = static_cast<const uint8_t*>(kv ? a.v : a.k) + (int64_t)r.g * a.head_stride * 2;
-          const uint32_t dst = base + (kv ? vOff : kOff) + stage * TB;
-          constexpr int KPI = 32 / CPR;
-          const int c = lane % CPR;
 #pragma unroll
           for (int i = 0; i < 32 / KPI; ++i) {
             const int x = i * KPI + lane / CPR;
             const int64_t ox = __shfl_sync(0xffffffffu, off, x) + c * 16;
-            cp_async16(dst + (c >> 3) * kHalf + (32 * w + x) * 128 + (((c & 7) ^ (x & 7)) << 4), from + ox, (rows >> x) & 1u);
+            cp_async16(base + slot_chunk(issued, x, c), from + ox, (there >> x) & 1u);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
-          if (kv && r.check) check |= 1u << (issued & 7);
-          else check &= ~(1u << (issued & 7));
+          check &= ~(1u << (issued & 7));
+          if (kv && (r.flags & kPartial)) check |= 1u << (issued & 7);
           ++issued;
         }
+        shift();
       }
-      while (ok && told != issued) tell();
+      while (ok && done != issued) tell();
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
-      // rows through registers, a tile ahead: 16 e4m3 values become two chunks of 8 fp16 values
-      constexpr int KPI = 32 / CPR, NI = 32 / KPI;
-      uint4 kr[NI], vr[NI];
-      const int c = lane % CPR;
-      struct Fetch {
-        int64_t off;
-        uint32_t rows;
-        int g;
-      };
-      auto resolve = [&](const Row& r) -> Fetch {
-        const bool fine = r.need && r.id >= 0 && r.id < a.n_pages;
-        if (r.need && !fine) set_device_error(a.err, KVSEL_ERR_DEVICE, (uint32_t)r.table);
-        return {fine ? (int64_t)r.id * a.page_stride + (int64_t)r.within * a.row_stride : 0, __ballot_sync(0xffffffffu, fine), r.g};
-      };
-      auto fetch = [&](const Fetch& f, const void* pool, uint4* to) {
-        const uint8_t* from = static_cast<const uint8_t*>(pool) + (int64_t)f.g * a.head_stride + c * 16;
+      // 16 e4m3 values become two chunks of 8 fp16 values; values that are no numbers become zeros where they are looked for
+      auto widen = [&](uint4 y, uint32_t q, int x, bool look_at) -> uint32_t {
+        uint32_t* h = reinterpret_cast<uint32_t*>(&y);
+        uint32_t bad = 0, o[8];
+        if (look_at) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int x = i * KPI + lane / CPR;
-          const int64_t ox = __shfl_sync(0xffffffffu, f.off, x);
-          to[i] = (f.rows >> x) & 1u ? *reinterpret_cast<const uint4*>(from + ox) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      uint32_t step = 0;
-      auto store = [&](uint4* y, uint32_t dst, bool check) -> uint32_t {
-        uint32_t bad = 0;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int x = i * KPI + lane / CPR;
-          uint32_t* h = reinterpret_cast<uint32_t*>(&y[i]);
-          if (check) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t nan = __vcmpeq4(h[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              if (nan) h[e] &= ~nan, bad |= 1u << x;
-            }
-          }
-          uint32_t o[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) e4m3x4_to_f16(h[e], o[2 * e], o[2 * e + 1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int cc = 2 * c + e;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (cc >> 3) * kHalf + (32 * w + x) * 128 + (((cc & 7) ^ (x & 7)) << 4)),
-                         "r"(o[4 * e]), "r"(o[4 * e + 1]), "r"(o[4 * e + 2]), "r"(o[4 * e + 3]) : "memory");
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t nan = __vcmpeq4(h[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            if (nan) h[e] &= ~nan, bad |= 1u << x;
           }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) e4m3x4_to_f16(h[e], o[2 * e], o[2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + slot_chunk(q, x, 2 * c + e)), "r"(o[4 * e]), "r"(o[4 * e + 1]),
+                       "r"(o[4 * e + 2]), "r"(o[4 * e + 3]) : "memory");
         return bad;
       };
-      Row r = next;
-      Fetch f{0, 0, 0};
-      if (r.more) {
-        f = resolve(r);
-        fetch(f, a.k, kr);
-      }
-      while (r.more && ok) {
-        fetch(f, a.v, vr);
-        next = look();
-        const uint32_t stage = step & 1, parity = ((step >> 1) & 1) ^ 1;
-        ok = __all_sync(0xffffffffu, rows_wait(k_empty(stage), parity, flag));
-        if (!ok) break;
-        if (lane == 0) seen_w[(step & 3) * 4 + w] = f.rows;
-        store(kr, base + kOff + stage * TB, false);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full(stage));
-        const bool check = r.check;
-        r = next;
-        if (r.more) {
-          f = resolve(r);
-          fetch(f, a.k, kr);
+      constexpr int NI = 32 / KPI;
+      if (R != 0) {
+        // boxes of bytes, four tiles ahead, into this warp's part of a ring
+        const uint32_t raw = rows_raw_off<D, KIND>() + 32 * w * RB;
+        auto raw_bar = [&](uint32_t q) { return bar(kBarRaw + 4 * (q % kRawTiles) + w); };
+        auto request = [&](const Row& r, uint32_t q) {         // K (even q) or V of the step
+          if (!(r.flags & kMore)) return;
+          const uint32_t boxes = __ballot_sync(0xffffffffu, known(r) && (r.flags & kBox) && (lane & (R - 1)) == 0);
+          load_boxes(r, boxes, (q & 1) ? &tv : &tk, base + raw + (q % kRawTiles) * kTileKeys * RB, raw_bar(q));
+          boxed = q + 1;
+        };
+        static_assert(kRawTiles == 2 * AHEAD, "the tiles ahead are those of the steps looked up");
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          request(rows[i], 2 * i);
+          request(rows[i], 2 * i + 1);
         }
-        ok = __all_sync(0xffffffffu, rows_wait(v_empty(stage), parity, flag));
-        if (!ok) break;
-        const uint32_t bad = __reduce_or_sync(0xffffffffu, store(vr, base + vOff + stage * TB, check));
-        if (lane == 0) bad_w[(step & 3) * 4 + w] = bad;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full(stage));
-        ++step;
+        for (uint32_t step = 0; (rows[0].flags & kMore) && ok; ++step) {
+          const Row& r = rows[0];
+          const uint32_t fine = __ballot_sync(0xffffffffu, known(r) && (r.flags & kNeed));
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t q = 2 * step + kv;
+            ok = ok && await(raw_bar(q), (q / kRawTiles) & 1) && await(empty(q), use(q) ^ 1);
+            if (!ok) break;
+            if (kv == 0 && lane == 0) seen_w[(step & 7) * 4 + w] = fine;
+            uint32_t bad = 0;
+            const uint8_t* from = sbase + raw + (q % kRawTiles) * kTileKeys * RB;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              const int x = i * KPI + lane / CPR;
+              const uint4 y = *reinterpret_cast<const uint4*>(from + x * RB + c * 16);
+              bad |= widen((fine >> x) & 1u ? y : make_uint4(0, 0, 0, 0), q, x, kv && (r.flags & kPartial));
+            }
+            if (kv && (r.flags & kPartial)) {
+              bad = __reduce_or_sync(0xffffffffu, bad);
+              if (lane == 0) bad_w[(step & 7) * 4 + w] = bad;
+            }
+            told(q);                               // (and the warp is done with the raw tile)
+            request(rows[AHEAD], q + kRawTiles);
+          }
+          shift();
+        }
+      } else {
+        // rows through registers, a tile ahead
+        uint4 y[2][NI];
+        struct Fetch {
+          int64_t off;
+          uint32_t rows;
+        };
+        auto resolve = [&](const Row& r) -> Fetch {
+          const bool fine = known(r) && (r.flags & kNeed);
+          return {fine ? (int64_t)r.id * a.page_stride + (int64_t)r.within * a.row_stride : 0, __ballot_sync(0xffffffffu, fine)};
+        };
+        auto fetch = [&](const Fetch& f, int g, const void* pool, uint4* to) {
+          const uint8_t* from = static_cast<const uint8_t*>(pool) + (int64_t)g * a.head_stride + c * 16;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int x = i * KPI + lane / CPR;
+            const int64_t ox = __shfl_sync(0xffffffffu, f.off, x);
+            to[i] = (f.rows >> x) & 1u ? *reinterpret_cast<const uint4*>(from + ox) : make_uint4(0, 0, 0, 0);
+          }
+        };
+        Fetch f{0, 0};
+        if (rows[0].flags & kMore) {
+          f = resolve(rows[0]);
+          fetch(f, rows[0].g, a.k, y[0]);
+        }
+        for (uint32_t step = 0; (rows[0].flags & kMore) && ok; ++step) {
+          const bool partial = rows[0].flags & kPartial;
+          fetch(f, rows[0].g, a.v, y[1]);
+          const uint32_t there = f.rows;
+          shift();
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t q = 2 * step + kv;
+            ok = ok && await(empty(q), use(q) ^ 1);
+            if (!ok) break;
+            if (kv == 0 && lane == 0) seen_w[(step & 7) * 4 + w] = there;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) bad |= widen(y[kv][i], q, i * KPI + lane / CPR, kv && partial);
+            if (kv && partial) {
+              bad = __reduce_or_sync(0xffffffffu, bad);
+              if (lane == 0) bad_w[(step & 7) * 4 + w] = bad;
+            }
+            told(q);
+            if (kv == 0 && (rows[0].flags & kMore)) {
+              f = resolve(rows[0]);
+              fetch(f, rows[0].g, a.k, y[0]);
+            }
+          }
+        }
       }
     }
     if (!ok && lane == 0) rows_fail(a, flag, kRowsLoader);
+    // Boxes in flight land before the CTA ends.  (Without a failure every tile's barrier was waited for by those who read it.)
+    if (!ok && R != 0) {
+      constexpr uint32_t kPolls = 1u << 14;
+      if constexpr (KIND == kE4m3) {
+        for (uint32_t q = boxed < kRawTiles ? 0 : boxed - kRawTiles; q < boxed; ++q) (void)mbar_wait_n(bar(kBarRaw + 4 * (q % kRawTiles) + w), (q / kRawTiles) & 1, kPolls);
+      } else {
+        for (uint32_t q = boxed < NS ? 0 : boxed - NS; q < boxed; ++q) (void)mbar_wait_n(full(q), use(q), kPolls);
+        if (n_land > 0) (void)mbar_wait_n(bar(kBarLand + w), (n_land - 1) & 1, kPolls);
+      }
+    }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegMma));
     // ---------------------------------------------------------------- products
     if (warp == 12 && lane == 0) {
-      walk.begin(a, cta, W, N);
+      walk.begin(start);
       constexpr uint32_t idesc_s = rows_idesc<KIND>(128, 128), idesc_o = rows_idesc<KIND>(128, D) | kUmmaBMajorMN;
       constexpr int KS = D / 16, KP = kTileKeys / 16 * (SPLIT ? 2 : 1);
       bool ok = true, any = false;
-      // a step: its number among the CTA's, whether tile B has rows, first of its piece
+      // a step: its number among the CTA's, its tiles (both, or the one whose turn it is), whether it is their first of the piece
       struct Step {
-        int i;
-        bool two, first, more;
+        uint32_t i;
+        int tiles;
+        bool first, more;
       };
       bool have = walk.next(a, p);
-      int s = have ? p.s0 : 0, count = 0;
+      int s = have ? p.s0 : 0;
+      uint32_t count = 0;
       auto advance = [&]() -> Step {
-        Step r{count, false, false, have};
+        Step r{count, 0, false, have};
         if (!have) return r;
-        r.two = p.item->rows > kTileRows;
-        r.first = s == p.s0;
+        const bool two = p.item->rows > kTileRows;
+        r.tiles = two ? 3 : 1 << (count & 1);
+        r.first = s < p.s0 + (two ? 1 : 2);
         ++count;
         if (++s == p.s1) {
           have = walk.next(a, p);
@@ -486,107 +782,138 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
         return r;
       };
       uint32_t nq[2] = {0, 0}, npv[2] = {0, 0}, np[2] = {0, 0};      // phases waited for, by tile
+      int s_left = 0, pv_left = 0;                                   // tiles of the step whose S (P V) is not issued
       // S of a step may start once K has landed, the tile's queries are there, and its last P V (which reads the same TMEM
       // columns) is done; P V once V has landed and the weights are written
-      auto s_ready = [&](int x, const Step& t) {
-        if (!rows_wait(k_full(t.i & 1), (t.i >> 1) & 1, flag)) return false;
-        if (t.first) {
-          if (!rows_wait(q_full(x), nq[x] & 1, flag)) return false;
-          ++nq[x];
-        }
-        return npv[x] == 0 || rows_wait(pv_done(x), (npv[x] - 1) & 1, flag);
+      auto s_wait = [&](int x, const Step& t) {
+        return rows_wait(full(2 * t.i), use(2 * t.i), flag) && (!t.first || rows_wait(q_full(x), nq[x] & 1, flag)) &&
+               (npv[x] == 0 || rows_wait(pv_done(x), (npv[x] - 1) & 1, flag));
       };
-      auto pv_ready = [&](int x, const Step& t) {
-        if (!rows_wait(v_full(t.i & 1), (t.i >> 1) & 1, flag) || !rows_wait(p_full(x), np[x] & 1, flag)) return false;
-        ++np[x];
-        return true;
+      auto s_test = [&](int x, const Step& t) {
+        return rows_test(full(2 * t.i), use(2 * t.i)) && (!t.first || rows_test(q_full(x), nq[x] & 1)) &&
+               (npv[x] == 0 || rows_test(pv_done(x), (npv[x] - 1) & 1));
       };
+      auto pv_wait = [&](int x, const Step& t) {
+        return rows_wait(full(2 * t.i + 1), use(2 * t.i + 1), flag) && rows_wait(p_full(x), np[x] & 1, flag);
+      };
+      auto pv_test = [&](int x, const Step& t) { return rows_test(p_full(x), np[x] & 1) && rows_test(full(2 * t.i + 1), use(2 * t.i + 1)); };
       auto s_step = [&](int x, const Step& t, int kk) {
-        const uint32_t sq = base + x * TB, sk = base + kOff + (t.i & 1) * TB, off = (kk >> 2) * kHalf + (kk & 3) * 32;
+        const uint32_t sq = base + x * TB, sk = slots + (2 * t.i) % NS * TB, off = (kk >> 2) * kHalf + (kk & 3) * 32;
         umma_bf16(tmem + x * kTileCols + kSCol, umma_desc_sw128(sq + off), umma_desc_sw128(sk + off), idesc_s, kk > 0);
       };
       auto pv_step = [&](int x, const Step& t, int kk, bool keep) {
-        const uint32_t sv = base + vOff + (t.i & 1) * TB;
+        const uint32_t sv = slots + (2 * t.i + 1) % NS * TB;
         umma_bf16_ta(tmem + x * kTileCols + kOCol, tmem + x * kTileCols + kSCol + kk * 8,
                      umma_desc_sw128_mn(sv + (kk & 7) * 2048, kHalf), idesc_o, (keep || kk > 0) ? 1u : 0u);
       };
       // a commit covers every product before it
       auto s_done = [&](int x, const Step& t) {
         umma_commit(s_full(x));
-        if (x == 1 || !t.two) umma_commit(k_empty(t.i & 1));
+        if (--s_left == 0) umma_commit(empty(2 * t.i));
+        nq[x] += t.first;
         any = true;
       };
       auto pv_end = [&](int x, const Step& t) {
         umma_commit(pv_done(x));
-        if (x == 1 || !t.two) umma_commit(v_empty(t.i & 1));
+        if (--pv_left == 0) umma_commit(empty(2 * t.i + 1));
         ++npv[x];
+        ++np[x];
       };
-      auto s_alone = [&](int x, const Step& t) {
-        if (!s_ready(x, t)) return false;
+      auto s_all = [&](int x, const Step& t) {
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) s_step(x, t, kk);
         s_done(x, t);
-        return true;
+      };
+      auto pv_all = [&](int x, const Step& t) {
+        tc_fence_after();
+        const bool keep = !t.first || o_begun[x] != 0;
+#pragma unroll
+        for (int kk = 0; kk < KP; ++kk) pv_step(x, t, kk, keep);
+        pv_end(x, t);
       };
       Step cur = advance();
-      ok = cur.more && s_alone(0, cur) && (!cur.two || s_alone(1, cur));
+      s_left = cur.tiles == 3 ? 2 : 1;
+      for (int x = 0; x < 2 && ok; ++x)
+        if ((cur.tiles >> x) & 1) {
+          ok = s_wait(x, cur);
+          if (ok) s_all(x, cur);
+        }
       while (cur.more && ok) {
         const Step nxt = advance();
-        if (!(ok = pv_ready(0, cur))) break;
-        tc_fence_after();
-        const bool keep0 = !cur.first || o_begun[0] != 0;
+        int todo = nxt.more ? nxt.tiles : 0;
+        s_left = __popc(todo);
+        pv_left = __popc(cur.tiles);
+        if (cur.tiles == 3) {
+          if (!(ok = pv_wait(0, cur))) break;
+          pv_all(0, cur);
+          if (!(ok = pv_wait(1, cur))) break;
+          if (todo & 1) {
+            if (!(ok = s_wait(0, nxt))) break;
+            tc_fence_after();
+            const bool keep = !cur.first || o_begun[1] != 0;
 #pragma unroll
-        for (int kk = 0; kk < KP; ++kk) pv_step(0, cur, kk, keep0);
-        pv_end(0, cur);
-        const bool pvb = cur.two, sa = nxt.more;
-        if (pvb && !(ok = pv_ready(1, cur))) break;
-        if (sa && !(ok = s_ready(0, nxt))) break;
-        tc_fence_after();
-        if (pvb && sa) {
-          const bool keep1 = !cur.first || o_begun[1] != 0;
-#pragma unroll
-          for (int kk = 0; kk < (KP > KS ? KP : KS); ++kk) {
-            if (kk < KP) pv_step(1, cur, kk, keep1);
-            if (kk < KS) s_step(0, nxt, kk);
+            for (int kk = 0; kk < (KP > KS ? KP : KS); ++kk) {
+              if (kk < KP) pv_step(1, cur, kk, keep);
+              if (kk < KS) s_step(0, nxt, kk);
+            }
+            pv_end(1, cur);
+            s_done(0, nxt);
+            todo &= ~1;
+          } else {
+            pv_all(1, cur);
           }
-        } else if (pvb) {
-          const bool keep1 = !cur.first || o_begun[1] != 0;
-#pragma unroll
-          for (int kk = 0; kk < KP; ++kk) pv_step(1, cur, kk, keep1);
-        } else if (sa) {
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) s_step(0, nxt, kk);
+        } else {
+          // one tile's P V, and S of the next step on the other: whichever is ready first
+          const int x = (int)(cur.i & 1);
+          bool other = (todo >> (x ^ 1)) & 1, pv = true;
+          for (uint32_t i = 0; (pv || other) && ok; ++i) {
+            if (other && s_test(x ^ 1, nxt)) {
+              s_all(x ^ 1, nxt);
+              todo &= 1 << x;
+              other = false;
+            }
+            if (pv && pv_test(x, cur)) {
+              pv_all(x, cur);
+              pv = false;
+            }
+            ok = i < kSpinLimit && ((i & 255) != 255 || *flag == 0);
+          }
+          if (!ok) break;
         }
-        if (pvb) pv_end(1, cur);
-        if (sa) s_done(0, nxt);
-        if (sa && nxt.two) ok = s_alone(1, nxt);
+        for (int x = 0; x < 2 && ok; ++x)
+          if ((todo >> x) & 1) {
+            ok = s_wait(x, nxt);
+            if (ok) s_all(x, nxt);
+          }
         cur = nxt;
       }
       if (!ok) rows_fail(a, flag, kRowsMma);
       if (any) {
-        umma_commit(drain);
-        if (!mbar_wait(drain, 0)) set_device_error(a.err, KVSEL_ERR_TIMEOUT, kRowsDrain);
+        umma_commit(bar(kBarDrain));
+        if (!mbar_wait(bar(kBarDrain), 0)) set_device_error(a.err, KVSEL_ERR_TIMEOUT, kRowsDrain);
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegRows));
-    walk.begin(a, cta, W, N);
+    walk.begin(start);
     // ---------------------------------------------------------------- softmax, a thread per query row
     const int x = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + x * kTileCols;
-    const float kShift = SPLIT ? 0.f : (KIND == kBf16 ? -8.f : 13.f);
-    constexpr float kLag = weight_lag<KIND>();
-    auto live_piece = [&](RowsPiece& to) {          // the next piece in which this tile has rows
-      while (walk.next(a, to))
-        if (x == 0 || to.item->rows > kTileRows) return true;
-      return false;
+    constexpr float kShift = SPLIT ? 0.f : (KIND == kBf16 ? -8.f : 13.f);
+    uint32_t n = 0, n_merged = 0;                   // steps of this tile, meetings of the softmax warps so far
+    bool ok = true;
+    // a piece's rows: blocks of 32 in a tile (its other rows are copies), and whether this tile has a step of it
+    auto blocks = [](int rows) { return rows > 64 ? 4 : rows > 32 ? 2 : 1; };
+    auto has_steps = [&](const RowsPiece& t, int i0) {
+      return t.item->rows > kTileRows || t.s1 - t.s0 > 1 || (i0 & 1) == x;
     };
     // this thread's query row of a piece: into shared memory, swizzled; returns the factor taken out of it
     auto load_q = [&](const RowsPiece& t) -> float {
-      const int i = x * kTileRows + row, r = t.item->row0 + i;
-      const bool live = i < t.item->rows;
+      const int rows = t.item->rows;
+      const int i = rows > kTileRows ? x * kTileRows + row : row & (32 * blocks(rows) - 1), r = t.item->row0 + i;
+      const bool live = i < rows;
       uint4 y[D / 8];
       const int tok = r / a.G, h = r - tok * a.G;
       const uint16_t* from = static_cast<const uint16_t*>(a.q) + (live ? ((int64_t)t.item->token0 + tok) * a.q_stride + (int64_t)(t.g * a.G + h) * D : 0);
@@ -619,127 +946,96 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
       if (lane == 0) mbar_arrive(q_full(x));
       return by;
     };
-    const int64_t x_begin = walk.x;                 // steps are numbered as the loaders number them
+    // the eight softmax warps meet; false where one does not come
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarMerge));
+      return __all_sync(0xffffffffu, rows_wait(bar(kBarMerge), n_merged++ & 1, flag));
+    };
     RowsPiece cur;
-    bool more = live_piece(cur);
-    float by = more ? load_q(cur) : 1.f;
-    uint32_t n = 0;                                 // steps of this tile so far
-    bool ok = true;
-    int64_t x_end = walk.x;                         // step number behind the current piece
+    bool more = walk.next(a, cur);
+    int i0 = 0;                                     // the piece's first step among the CTA's
+    float by = more && has_steps(cur, i0) ? load_q(cur) : 1.f;
     while (more && ok) {
       const RowsItem& it = *cur.item;
+      const int rows = it.rows, nb = blocks(rows);
+      const bool two = rows > kTileRows;
+      const int i = two ? x * kTileRows + row : row & (32 * nb - 1), copy = two ? 0 : quarter / nb;
+      const int r = it.row0 + i, tok = r / a.G, h = cur.g * a.G + (r - tok * a.G);
       const int k0 = it.k0, k_lo = it.lo, k_hi = it.hi, full_lo = it.full_lo, full_hi = it.full_hi;
-      const int i = x * kTileRows + row, r = it.row0 + i, tok = r / a.G, h = cur.g * a.G + (r - tok * a.G);
-      const bool live = i < it.rows;
+      const bool live = i < rows;
       const int pos = !live ? -1 : a.prefix ? (int)a.lens[it.token0 + tok] - 1 : it.base + tok;
       const int low = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
-      const float ksc = a.scale * (a.k_scale != nullptr ? a.k_scale[cur.g] : 1.f);
-      const float sc = ksc * by * (a.softcap != 0.f ? 1.f : kLog2e);
-      const float slope = a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
-      const float cap2 = a.softcap * kLog2e, icap = a.softcap != 0.f ? 1.f / a.softcap : 0.f;
-      const bool general = a.softcap != 0.f || a.slopes != nullptr || !(ksc > 0.f);
+      const float ksc = a.scale * (a.k_scale != nullptr ? a.k_scale[cur.g] : 1.f) * by;
+      RowsScore score;
+      score.capped = a.softcap != 0.f;
+      score.sc = ksc * kLog2e;
+      score.icap = score.capped ? ksc / a.softcap : 0.f;
+      score.cap2 = a.softcap * kLog2e;
+      score.slope = a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
+      const bool general = score.capped || a.slopes != nullptr || !(a.k_scale == nullptr || a.k_scale[cur.g] > 0.f);
       const bool idle = __all_sync(0xffffffffu, !live);         // a warp of padding alone
       float m = -INFINITY, mo = 0.f, l = 0.f;
-      bool begun = false;
+      bool begun = false, had = false;
       if (lane == 0 && quarter == 0) o_begun[x] = 0;            // (before the piece's first weights are told of)
-      int step = (int)(x_end - x_begin) - (cur.s1 - cur.s0);    // its number among the CTA's steps
-      for (int s = cur.s0; s < cur.s1; ++s, ++step, ++n) {
+      uint32_t step = i0;
+      for (int s = cur.s0; s < cur.s1; ++s, ++step) {
+        if (!two && (int)(step & 1) != x) continue;
         ok = __all_sync(0xffffffffu, rows_wait(s_full(x), n & 1, flag));
         if (!ok) break;
+        ++n;
         tc_fence_after();
         const int t0 = k0 + kTileKeys * s;
-        const uint4 there = *reinterpret_cast<const uint4*>(&seen_w[(step & 3) * 4]);
+        const uint4 there = *reinterpret_cast<const uint4*>(&seen_w[(step & 7) * 4]);
         const bool whole = t0 >= full_lo && t0 + kTileKeys <= full_hi && (there.x & there.y & there.z & there.w) == 0xffffffffu;
         if (rows_partial(k_lo, k_hi, full_lo, full_hi, t0)) {
-          ok = __all_sync(0xffffffffu, rows_wait(v_full(step & 1), (step >> 1) & 1, flag));
+          ok = __all_sync(0xffffffffu, rows_wait(full(2 * step + 1), use(2 * step + 1), flag));
           if (!ok) break;
-          const uint4 bad = *reinterpret_cast<const uint4*>(&bad_w[(step & 3) * 4]);
+          uint4 bad = *reinterpret_cast<const uint4*>(&bad_w[(step & 7) * 4]);
           if ((bad.x | bad.y | bad.z | bad.w) != 0) {
-            const bool fresh = s == cur.s0;
+            if (nb < 4) {                                       // a copy adds those of its own keys
+              if (copy * nb > 0 || copy * nb + nb <= 0) bad.x = 0;
+              if (copy * nb > 1 || copy * nb + nb <= 1) bad.y = 0;
+              if (copy * nb > 2 || copy * nb + nb <= 2) bad.z = 0;
+              if (copy * nb > 3 || copy * nb + nb <= 3) bad.w = 0;
+            }
             add_bad_rows<D, KIND>(a, static_cast<const uint8_t*>(a.v) + (int64_t)cur.g * a.head_stride * elem_bytes<KIND>(), it.table, t0, pos,
-                                  bad, tm + kOCol, fresh);
-            if (fresh) begun = true;
-            if (fresh && lane == 0 && quarter == 0) o_begun[x] = 1;
+                                  bad, tm + kOCol, !had);
+            if (!had) begun = true;
+            if (!had && lane == 0 && quarter == 0) o_begun[x] = 1;
           }
         }
         if (!idle) {
-          // keys of the step that the row sees, by 32
+          // keys of the thread's part of the step that the row sees, by 32
           uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
           if (!whole) {
             const int from = low - t0, to = pos + 1 - t0;
             const uint32_t word[4] = {there.x, there.y, there.z, there.w};
+            uint32_t all[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int lo = min(32, max(0, from - 32 * k)), hi = min(32, max(0, to - 32 * k));
               const uint32_t below_hi = hi >= 32 ? 0xffffffffu : (1u << hi) - 1u, below_lo = lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
-              see[k] = live ? word[k] & below_hi & ~below_lo : 0u;
+              all[k] = live ? word[k] & below_hi & ~below_lo : 0u;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) see[k] = all[k];
+            if (nb == 2 && copy == 1) see[0] = all[2], see[1] = all[3];
+            if (nb == 1) see[0] = copy == 0 ? all[0] : copy == 1 ? all[1] : copy == 2 ? all[2] : all[3];
           }
-          const float mul = general ? 1.f : sc;
-          // 64 scores of the step (its half H) as they are compared: capped and biased, those not seen at -inf
-          auto scores = [&](float* z, int half) {
-            if (general) {
-              const float d0 = (float)(t0 + 64 * half - pos);
-#pragma unroll
-              for (int c = 0; c < 64; ++c) {
-                float y = z[c] * sc;
-                if (a.softcap != 0.f) y = cap2 * tanh_fast(y * icap);
-                z[c] = fmaf(slope, d0 + (float)c, y);
-              }
-            }
-            if (!whole) {
-              const uint32_t w0 = half ? see[2] : see[0], w1 = half ? see[3] : see[1];
-#pragma unroll
-              for (int c = 0; c < 64; ++c) z[c] = ((c < 32 ? w0 : w1) >> (c & 31)) & 1u ? z[c] : -INFINITY;
-            }
-          };
-          float alpha = 1.f, sum;
-          auto offset = [&](float mt) {                         // where a score passes the lag, the offset moves to the largest
-            if (mt > m + kLag) {
-              if (m != -INFINITY) alpha = ex2(m - mt);          // (nothing to rescale before the first)
-              m = mo = mt;
-            }
-          };
-          if constexpr (SPLIT) {
-            // the first half is read twice, so that a thread never holds both and their parts
-            uint32_t r[64], hi[32], lo[32];
-            float* z = reinterpret_cast<float*>(r);
-            tmem_ld64_async(tm + kSCol, r);
-            tmem_wait_ld64(r);
-            scores(z, 0);
-            const float m0 = rows_max64(z);
-            tmem_ld64_async(tm + kSCol + 64, r);
-            tmem_wait_ld64(r);
-            scores(z, 1);
-            offset(fmaxf(m0, rows_max64(z)) * mul);             // (mul > 0: the largest stays the largest)
-            sum = rows_weights<KIND, true>(z, mul, kShift - mo, hi, lo);
-            tmem_st32(tm + kSCol + 96, lo);
-            tmem_ld64_async(tm + kSCol, r);
-            tmem_wait_ld64(r);
-            tmem_st32(tm + kSCol + 32, hi);
-            scores(z, 0);
-            sum += rows_weights<KIND, true>(z, mul, kShift - mo, hi, lo);
-            tmem_st32(tm + kSCol + 64, lo);
-            tmem_st32(tm + kSCol, hi);
+          const float d0 = (float)(t0 - pos);
+          float alpha;
+          const bool fast = whole && !general;
+          if (nb == 4) {
+            if (fast) alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, 0, score, d0, see, false, true, m, mo, l);
+            else alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, 0, score, d0, see, general, whole, m, mo, l);
+          } else if (nb == 2) {
+            alpha = rows_step<KIND, SPLIT, 2>(tm + kSCol, copy, score, d0, see, general, whole, m, mo, l);
           } else {
-            uint32_t rv[64], rw[64];
-            tmem_ld64_async(tm + kSCol + 64, rv);
-            tmem_ld64_async(tm + kSCol, rw);
-            tmem_wait_ld64(rv);                                 // one wait covers both loads
-            reg_tie64(rw);
-            float* v = reinterpret_cast<float*>(rv);
-            float* u = reinterpret_cast<float*>(rw);
-            scores(u, 0);
-            scores(v, 1);
-            offset(fmaxf(rows_max64(u), rows_max64(v)) * mul);
-            sum = rows_weights<KIND, false>(u, mul, kShift - mo, rw, nullptr);
-            tmem_st32(tm + kSCol, rw);
-            sum += rows_weights<KIND, false>(v, mul, kShift - mo, rv, nullptr);
-            tmem_st32(tm + kSCol + 32, rv);
+            alpha = rows_step<KIND, SPLIT, 1>(tm + kSCol, copy, score, d0, see, general, whole, m, mo, l);
           }
-          l = l * alpha + sum;
-          // O of the step before is final (this step's S was issued behind its P V)
-          if ((s > cur.s0 || begun) && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O of the tile's step before is final (this step's S was issued behind its P V)
+          if ((had || begun) && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
               float f[32];
@@ -752,60 +1048,137 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
           }
           tmem_wait_st();
         }
+        had = true;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(x));
       }
       if (!ok) break;
-      // the next piece's queries (this piece's last S is done with them), then this one's result
       RowsPiece nxt;
-      const bool has_next = live_piece(nxt);
+      const bool has_next = walk.next(a, nxt);
+      const int i_next = i0 + cur.s1 - cur.s0;
       float by_next = 1.f;
-      const int64_t nx_end = walk.x;
-      if (has_next) by_next = load_q(nxt);
-      ok = __all_sync(0xffffffffu, rows_wait(pv_done(x), (n - 1) & 1, flag));
-      if (!ok) break;
-      tc_fence_after();
-      if (!idle) {
-        const bool final = !a.prefix && cur.starts() && cur.ends();
-        const float vsc = a.v_scale != nullptr ? a.v_scale[cur.g] : 1.f;
-        const float f = !final ? 1.f : l == 0.f ? 0.f : (SPLIT ? vsc / weight_unit<KIND>() : vsc) / l;
-        const int64_t out = ((int64_t)it.token0 + tok) * a.h_q + h;
-        const int64_t prow = rows_part(a, cta, cur.starts(), cur.g, it);
+      // the next piece's queries (this tile's last S is done with its own), then this piece's result; a merge needs the room first
+      if (two && has_next && has_steps(nxt, i_next)) by_next = load_q(nxt);
+      if (had) {
+        ok = __all_sync(0xffffffffu, rows_wait(pv_done(x), (n - 1) & 1, flag));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool final = !a.prefix && cur.starts() && cur.ends();
+      const float vsc = a.v_scale != nullptr ? a.v_scale[cur.g] : 1.f;
+      const int64_t out = ((int64_t)it.token0 + tok) * a.h_q + h;
+      const int64_t prow = rows_part(a, cta, cur.starts(), cur.g, it);
+      if (two) {
+        if (!idle) {
+          const float f = !final ? 1.f : l == 0.f ? 0.f : (SPLIT ? vsc / weight_unit<KIND>() : vsc) / l;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float y[32];
-          tmem_ld32(tm + kOCol + c, y);
-          if (!live) continue;
-          if (final) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + c);
+          for (int c = 0; c < D; c += 32) {
+            float y[32];
+            __syncwarp();
+            tmem_ld32(tm + kOCol + c, y);
+            if (!live) continue;
+            if (final) {
+              uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + c);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t b[4];
+              for (int e = 0; e < 4; ++e) {
+                uint32_t b[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float y0 = y[8 * e + 2 * k] * f, y1 = y[8 * e + 2 * k + 1] * f;
-                b[k] = a.out_f16 ? pack16<kF16>(y0, y1) : pack16<kBf16>(y0, y1);
+                for (int k = 0; k < 4; ++k) {
+                  const float y0 = y[8 * e + 2 * k] * f, y1 = y[8 * e + 2 * k + 1] * f;
+                  b[k] = a.out_f16 ? pack16<kF16>(y0, y1) : pack16<kBf16>(y0, y1);
+                }
+                to[e] = make_uint4(b[0], b[1], b[2], b[3]);
               }
-              to[e] = make_uint4(b[0], b[1], b[2], b[3]);
-            }
-          } else {
-            // four values of a row next to those of the next row
-            float4* to = reinterpret_cast<float4*>(a.part + prow * D) + (int64_t)(c / 4) * it.rows + i;
+            } else {
+              // four values of a row next to those of the next row
+              float4* to = reinterpret_cast<float4*>(a.part + prow * D) + (int64_t)(c / 4) * rows + i;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) to[(int64_t)e * it.rows] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              for (int e = 0; e < 8; ++e) to[(int64_t)e * rows] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            }
           }
         }
-        if (live) {
-          if (!final) a.part_ml[prow + i] = make_float2(m, l);
-          else if (a.lse != nullptr) a.lse[out] = (m + log2f(l) - kShift) * 0.6931471805599453f;
-        }
+      } else {
+        // What the tiles and copies hold of a row, in the queries' room once both tiles' products are done with them.  Warp w has
+        // block w mod nb; offsets and sums meet first, then D / 4 columns at a time in one of two buffers, where every
+        // warp sums its share of its block's columns, each part times 2^(m - M).
+        if (!(ok = meet())) break;
+        constexpr int COLS = D / 4;
+        float* buf = reinterpret_cast<float*>(sbase);
+        float2* ml = reinterpret_cast<float2*>(buf + 8 * COLS * 32);
+        ml[warp * 32 + lane] = make_float2(m, l);
+        auto merge = [&](auto blocks_c) {
+          constexpr int NB = decltype(blocks_c)::value, PARTS = 8 / NB, OWN = COLS * NB / 8;    // parts of a row, columns of a warp
+          const int block = warp % NB, c0 = warp / NB * OWN;
+          float f[PARTS], M = -INFINITY, L = 0.f;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float* b = buf + (q & 1) * 8 * COLS * 32;
+            __syncwarp();
+            if (had && !idle) {
+              float y[COLS];
+              if constexpr (COLS == 32) tmem_ld32(tm + kOCol + q * COLS, y);
+              else tmem_ld16(tm + kOCol + q * COLS, y);
+#pragma unroll
+              for (int e = 0; e < COLS; ++e) b[(warp * COLS + e) * 32 + lane] = y[e];
+            } else {
+#pragma unroll
+              for (int e = 0; e < COLS; ++e) b[(warp * COLS + e) * 32 + lane] = 0.f;
+            }
+            if (!(ok = meet())) return;
+            if (q == 0) {
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) M = fmaxf(M, ml[(block + NB * k) * 32 + lane].x);
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) {
+                const float2 y = ml[(block + NB * k) * 32 + lane];
+                f[k] = y.x == M ? 1.f : exp2f(y.x - M);
+                L += y.y * f[k];
+              }
+              if (!(ok = meet())) return;           // (the second buffer is read)
+              m = M;
+              l = L;
+              const float g = !final ? 1.f : L == 0.f ? 0.f : (SPLIT ? vsc / weight_unit<KIND>() : vsc) / L;
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) f[k] *= g;
+            }
+            float y[OWN];
+#pragma unroll
+            for (int e = 0; e < OWN; ++e) {
+              y[e] = 0.f;
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) y[e] = fmaf(b[((block + NB * k) * COLS + c0 + e) * 32 + lane], f[k], y[e]);
+            }
+            if (!live) continue;
+            const int col = q * COLS + c0;
+            if (final) {
+              uint32_t* to = static_cast<uint32_t*>(a.o) + (out * D + col) / 2;
+#pragma unroll
+              for (int e = 0; e < OWN; e += 2) to[e / 2] = a.out_f16 ? pack16<kF16>(y[e], y[e + 1]) : pack16<kBf16>(y[e], y[e + 1]);
+            } else {
+              float* to = a.part + prow * D;
+#pragma unroll
+              for (int e = 0; e < OWN; e += 2)
+                *reinterpret_cast<float2*>(to + ((int64_t)((col + e) / 4) * rows + i) * 4 + ((col + e) & 2)) = make_float2(y[e], y[e + 1]);
+            }
+          }
+          ok = meet();                              // the buffers are read
+        };
+        if (nb == 4) merge(std::integral_constant<int, 4>{});
+        else if (nb == 2) merge(std::integral_constant<int, 2>{});
+        else merge(std::integral_constant<int, 1>{});
+        if (!ok) break;
+        if (has_next && has_steps(nxt, i_next)) by_next = load_q(nxt);
+      }
+      if (live && (two || warp / nb == 0)) {
+        if (!final) a.part_ml[prow + i] = make_float2(m, l);
+        else if (a.lse != nullptr) a.lse[out] = (m + log2f(l) - kShift) * 0.6931471805599453f;
       }
       tc_fence_before();
       cur = nxt;
       more = has_next;
       by = by_next;
-      x_end = nx_end;
+      i0 = i_next;
     }
     if (!ok && lane == 0) rows_fail(a, flag, kRowsSoftmax);
   }
@@ -817,14 +1190,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
   }
 }
 
-using RowsKernel = void (*)(const RowsArgs);
+using RowsKernel = void (*)(const RowsArgs, const CUtensorMap, const CUtensorMap);
 struct RowsVariant {
   RowsKernel kern;
   size_t smem;
 };
 template <int D, int KIND>
 RowsVariant rows_variant(bool split) {
-  return {split ? rows_attend<D, KIND, true> : rows_attend<D, KIND, false>, rows_smem<D>()};
+  return {split ? rows_attend<D, KIND, true> : rows_attend<D, KIND, false>, rows_smem<D, KIND>()};
 }
 // The kernels of a pool type, each in a file of its own (rows_attend_*.cu).
 RowsVariant rows_variant_bf16(int d, bool split);
