@@ -31,8 +31,6 @@
 // do see it by hand.
 #pragma once
 
-#include <type_traits>
-
 #include "paged_attend.cuh"
 #include "rows.cuh"
 
@@ -139,10 +137,11 @@ __device__ __forceinline__ bool rows_partial(int lo, int hi, int full_lo, int fu
 }
 // Adds to this thread's O (TMEM at `o`) the values of V rows that are not finite and that the thread's row sees.
 template <int D, int KIND>
-__device__ __noinline__ void add_bad_rows(const RowsArgs& a, const uint8_t* vbase, int table, int t0, int pos, uint4 bad, uint32_t o,
+__device__ __forceinline__ void add_bad_rows(const RowsArgs& a, const uint8_t* vbase, int table, int t0, int pos, uint4 bad, uint32_t o,
                                           bool fresh) {
   const uint32_t word[4] = {bad.x, bad.y, bad.z, bad.w};
   const int low = a.window > 0 ? pos + 1 - a.window : 0;
+#pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += 32) {
     float v[32];
     if (fresh) {
@@ -247,19 +246,22 @@ __device__ __forceinline__ float rows_weights(const float* v, float mul, float n
 
 // A row's scores as they are compared, from the products: with a cap c z' = c tanh(z / c), a bias slope (t - p), in base 2.
 struct RowsScore {
-  float sc, icap, cap2, slope;        // sc: scale with log2 e, or with a cap scale / cap alone (icap is that then)
-  bool capped;
+  float sc, icap, cap2, slope;        // sc: scale with log2 e; icap: scale / cap
+  bool capped, general;               // general: more than a positive factor
 };
-// z[0 .. N) of the keys whose distances to the row's own begin at d0; those whose bit of `see` is off at -inf.
-template <int N>
-__device__ __forceinline__ void rows_scores(float* z, const RowsScore& k, float d0, const uint32_t* see, bool general, bool whole) {
-  if (general) {
-    const float2 sl = make_float2(k.slope, k.slope);
+// The products of a thread's keys that are more than a factor away from their scores, or some of which the row does not see:
+// rewritten in TMEM, 32 at a time, the ones not seen as -inf.  d0: distance of the first key to the row's own.
+__device__ __forceinline__ void rows_scores(uint32_t s, int blocks, const RowsScore k, float d0, uint4 see) {
+  uint32_t word[4] = {see.x, see.y, see.z, see.w};
+#pragma unroll 1
+  for (int j = 0; j < blocks; ++j) {
+    float z[32];
+    sm100::tmem_ld32(s + 32 * j, z);
     if (k.capped) {
       const float2 ic = make_float2(k.icap, k.icap), cp = make_float2(k.cap2, k.cap2);
       float big = 0.f;
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
+      for (int c = 0; c < 32; c += 2) {
         const float2 x = __fmul2_rn(make_float2(z[c], z[c + 1]), ic);
         z[c] = x.x;
         z[c + 1] = x.y;
@@ -270,7 +272,7 @@ __device__ __forceinline__ void rows_scores(float* z, const RowsScore& k, float 
         const float2 c3 = make_float2(-17.f / 315.f, -17.f / 315.f), c2 = make_float2(2.f / 15.f, 2.f / 15.f),
                      c1 = make_float2(-1.f / 3.f, -1.f / 3.f), one = make_float2(1.f, 1.f);
 #pragma unroll
-        for (int c = 0; c < N; c += 2) {
+        for (int c = 0; c < 32; c += 2) {
           const float2 x = make_float2(z[c], z[c + 1]), x2 = __fmul2_rn(x, x);
           const float2 y = __fmul2_rn(__fmul2_rn(x, cp), __ffma2_rn(x2, __ffma2_rn(x2, __ffma2_rn(x2, c3, c2), c1), one));
           z[c] = y.x;
@@ -278,41 +280,34 @@ __device__ __forceinline__ void rows_scores(float* z, const RowsScore& k, float 
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < N; ++c) z[c] = k.cap2 * tanh_fast(z[c]);
+        for (int c = 0; c < 32; ++c) z[c] = k.cap2 * tanh_fast(z[c]);
       }
-    } else {
-      const float2 s2 = make_float2(k.sc, k.sc);
+    }
+    if (k.general) {
+      const float2 s2 = make_float2(k.capped ? 1.f : k.sc, k.capped ? 1.f : k.sc), sl = make_float2(k.slope, k.slope);
+      const float2 dd = make_float2(d0 + 32.f * j, d0 + 32.f * j + 1.f);
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const float2 y = __fmul2_rn(make_float2(z[c], z[c + 1]), s2);
+      for (int c = 0; c < 32; c += 2) {
+        const float2 y = __ffma2_rn(sl, __fadd2_rn(dd, make_float2((float)c, (float)c)), __fmul2_rn(make_float2(z[c], z[c + 1]), s2));
         z[c] = y.x;
         z[c + 1] = y.y;
       }
     }
-    if (k.slope != 0.f) {
-      const float2 dd = make_float2(d0, d0 + 1.f);
+    const uint32_t w = j == 0 ? word[0] : j == 1 ? word[1] : j == 2 ? word[2] : word[3];
+    uint32_t r[32];
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const float2 y = __ffma2_rn(sl, __fadd2_rn(dd, make_float2((float)c, (float)c)), make_float2(z[c], z[c + 1]));
-        z[c] = y.x;
-        z[c + 1] = y.y;
-      }
-    }
+    for (int c = 0; c < 32; ++c) r[c] = (w >> c) & 1u ? __float_as_uint(z[c]) : 0xff800000u;
+    sm100::tmem_st32(s + 32 * j, r);
   }
-  if (!whole) {
-#pragma unroll
-    for (int c = 0; c < N; ++c) z[c] = (see[c / 32] >> (c & 31)) & 1u ? z[c] : -INFINITY;
-  }
+  sm100::tmem_wait_st();
 }
 
-// One step of a thread's row: weights of its 32 NB keys, from TMEM column `s` + 32 NB `copy` on, written over S (zeros in
-// the other copies' places); updates the offset m, mo, the sum l; returns the factor on what O holds.
-template <int KIND, bool SPLIT, int NB>
-__device__ __forceinline__ float rows_step(uint32_t s, int copy, const RowsScore& k, float d0, const uint32_t* see, bool general, bool whole,
-                                           float& m, float& mo, float& l) {
+// One step of a thread's row: weights of its keys, written over S: all 128 of the step (COPIES 1), or the 32 of copy `copy` with
+// zeros in the other copies' places; updates the offset m, mo, the sum l; returns the factor on what O holds.
+template <int KIND, bool SPLIT, int COPIES>
+__device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, float& m, float& mo, float& l) {
   using namespace sm100;
   constexpr float kShift = SPLIT ? 0.f : (KIND == kBf16 ? -8.f : 13.f), kLag = weight_lag<KIND>();
-  const float mul = general ? 1.f : k.sc;
   float alpha = 1.f, sum;
   auto offset = [&](float mt) {                         // where a score passes the lag, the offset moves to the largest
     if (mt > m + kLag) {
@@ -320,28 +315,25 @@ __device__ __forceinline__ float rows_step(uint32_t s, int copy, const RowsScore
       m = mo = mt;
     }
   };
-  if constexpr (NB == 4 && SPLIT) {
+  if constexpr (COPIES == 1 && SPLIT) {
     // the first half is read twice, so that a thread never holds both and their parts
     uint32_t r[64], hi[32], lo[32];
     float* z = reinterpret_cast<float*>(r);
     tmem_ld64_async(s, r);
     tmem_wait_ld64(r);
-    rows_scores<64>(z, k, d0, see, general, whole);
     const float m0 = rows_max<64>(z);
     tmem_ld64_async(s + 64, r);
     tmem_wait_ld64(r);
-    rows_scores<64>(z, k, d0 + 64.f, see + 2, general, whole);
     offset(fmaxf(m0, rows_max<64>(z)) * mul);           // (mul > 0: the largest stays the largest)
     sum = rows_weights<KIND, true, 64>(z, mul, kShift - mo, hi, lo);
     tmem_st32(s + 96, lo);
     tmem_ld64_async(s, r);
     tmem_wait_ld64(r);
     tmem_st32(s + 32, hi);
-    rows_scores<64>(z, k, d0, see, general, whole);
     sum += rows_weights<KIND, true, 64>(z, mul, kShift - mo, hi, lo);
     tmem_st32(s + 64, lo);
     tmem_st32(s, hi);
-  } else if constexpr (NB == 4) {
+  } else if constexpr (COPIES == 1) {
     uint32_t rv[64], rw[64];
     tmem_ld64_async(s + 64, rv);
     tmem_ld64_async(s, rw);
@@ -349,36 +341,23 @@ __device__ __forceinline__ float rows_step(uint32_t s, int copy, const RowsScore
     reg_tie64(rw);
     float* v = reinterpret_cast<float*>(rv);
     float* u = reinterpret_cast<float*>(rw);
-    rows_scores<64>(u, k, d0, see, general, whole);
-    rows_scores<64>(v, k, d0 + 64.f, see + 2, general, whole);
     offset(fmaxf(rows_max<64>(u), rows_max<64>(v)) * mul);
     sum = rows_weights<KIND, false, 64>(u, mul, kShift - mo, rw, nullptr);
     tmem_st32(s, rw);
     sum += rows_weights<KIND, false, 64>(v, mul, kShift - mo, rv, nullptr);
     tmem_st32(s + 32, rv);
   } else {
-    constexpr int N = 32 * NB;
-    float z[N];
-    uint32_t hi[N / 2], lo[N / 2], zero[N / 2];
+    float z[32];
+    uint32_t hi[16], lo[16], zero[16];
 #pragma unroll
-    for (int c = 0; c < N / 2; ++c) zero[c] = 0u;
-    if constexpr (NB == 1) {
-      tmem_ld32(s + 32 * copy, z);
-    } else {
-      tmem_ld64(s + 64 * copy, z);
-    }
-    rows_scores<N>(z, k, d0 + (float)(N * copy), see, general, whole);
-    offset(rows_max<N>(z) * mul);
-    sum = rows_weights<KIND, SPLIT, N>(z, mul, kShift - mo, hi, lo);
+    for (int c = 0; c < 16; ++c) zero[c] = 0u;
+    tmem_ld32(s + 32 * copy, z);
+    offset(rows_max<32>(z) * mul);
+    sum = rows_weights<KIND, SPLIT, 32>(z, mul, kShift - mo, hi, lo);
 #pragma unroll
     for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
-      for (int j = 0; j < 4 / NB; ++j) {
-        const uint32_t at = s + 64 * part + 16 * NB * ((copy + j) & (4 / NB - 1));
-        const uint32_t* from = j != 0 ? zero : part ? lo : hi;
-        if constexpr (NB == 1) tmem_st16(at, from);
-        else tmem_st32(at, from);
-      }
+      for (int j = 0; j < 4; ++j) tmem_st16(s + 64 * part + 16 * ((copy + j) & 3), j != 0 ? zero : part ? lo : hi);
   }
   l = l * alpha + sum;
   return alpha;
@@ -758,21 +737,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
       walk.begin(start);
       constexpr uint32_t idesc_s = rows_idesc<KIND>(128, 128), idesc_o = rows_idesc<KIND>(128, D) | kUmmaBMajorMN;
       constexpr int KS = D / 16, KP = kTileKeys / 16 * (SPLIT ? 2 : 1);
-      bool ok = true, any = false;
-      // a step: its number among the CTA's, its tiles (both, or the one whose turn it is), whether it is their first of the piece
+      const uint64_t vdesc = umma_desc_sw128_mn(slots, kHalf), kdesc = umma_desc_sw128(slots), qdesc = umma_desc_sw128(base);
+      // a step: its number among the CTA's, its tiles (both, or the one whose turn it is), whether it is their first of the
+      // piece, and the slots of its K and V
       struct Step {
-        uint32_t i;
-        int tiles;
-        bool first, more;
+        uint32_t i, tiles, k_slot, v_slot;
+        bool first;
       };
       bool have = walk.next(a, p);
       int s = have ? p.s0 : 0;
       uint32_t count = 0;
       auto advance = [&]() -> Step {
-        Step r{count, 0, false, have};
+        Step r{count, 0u, 2 * count % NS, (2 * count + 1) % NS, false};
         if (!have) return r;
         const bool two = p.item->rows > kTileRows;
-        r.tiles = two ? 3 : 1 << (count & 1);
+        r.tiles = two ? 3u : 1u << (count & 1);
         r.first = s < p.s0 + (two ? 1 : 2);
         ++count;
         if (++s == p.s1) {
@@ -781,112 +760,72 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
         }
         return r;
       };
-      uint32_t nq[2] = {0, 0}, npv[2] = {0, 0}, np[2] = {0, 0};      // phases waited for, by tile
-      int s_left = 0, pv_left = 0;                                   // tiles of the step whose S (P V) is not issued
+      // by tile: parity of the next queries and weights, of the last P V, and whether that is not known to be done
+      uint32_t at_q = 0, at_p = 0, last_pv = 3, await_pv = 0;
+      // `cur` has tiles whose P V is left, `nxt` tiles whose S is
+      Step cur{0, 0, 0, 0, false}, nxt = advance();
+      uint32_t pv_left = 0, s_left = nxt.tiles, spins = 0;
+      bool k_there = false, v_there = false, ok = true, any = false;
       // S of a step may start once K has landed, the tile's queries are there, and its last P V (which reads the same TMEM
-      // columns) is done; P V once V has landed and the weights are written
-      auto s_wait = [&](int x, const Step& t) {
-        return rows_wait(full(2 * t.i), use(2 * t.i), flag) && (!t.first || rows_wait(q_full(x), nq[x] & 1, flag)) &&
-               (npv[x] == 0 || rows_wait(pv_done(x), (npv[x] - 1) & 1, flag));
+      // columns) is done; P V once V has landed and the weights are written.  S first: the softmax waits for it.
+      auto s_ready = [&](uint32_t x) {
+        if (((await_pv >> x) & 1) && !rows_test(pv_done(x), (last_pv >> x) & 1)) return false;
+        await_pv &= ~(1u << x);
+        if (!k_there && !(k_there = rows_test(full(2 * nxt.i), use(2 * nxt.i)))) return false;
+        return !nxt.first || rows_test(q_full(x), (at_q >> x) & 1);
       };
-      auto s_test = [&](int x, const Step& t) {
-        return rows_test(full(2 * t.i), use(2 * t.i)) && (!t.first || rows_test(q_full(x), nq[x] & 1)) &&
-               (npv[x] == 0 || rows_test(pv_done(x), (npv[x] - 1) & 1));
+      auto pv_ready = [&](uint32_t x) {
+        if (!rows_test(p_full(x), (at_p >> x) & 1)) return false;
+        return v_there || (v_there = rows_test(full(2 * cur.i + 1), use(2 * cur.i + 1)));
       };
-      auto pv_wait = [&](int x, const Step& t) {
-        return rows_wait(full(2 * t.i + 1), use(2 * t.i + 1), flag) && rows_wait(p_full(x), np[x] & 1, flag);
-      };
-      auto pv_test = [&](int x, const Step& t) { return rows_test(p_full(x), np[x] & 1) && rows_test(full(2 * t.i + 1), use(2 * t.i + 1)); };
-      auto s_step = [&](int x, const Step& t, int kk) {
-        const uint32_t sq = base + x * TB, sk = slots + (2 * t.i) % NS * TB, off = (kk >> 2) * kHalf + (kk & 3) * 32;
-        umma_bf16(tmem + x * kTileCols + kSCol, umma_desc_sw128(sq + off), umma_desc_sw128(sk + off), idesc_s, kk > 0);
-      };
-      auto pv_step = [&](int x, const Step& t, int kk, bool keep) {
-        const uint32_t sv = slots + (2 * t.i + 1) % NS * TB;
-        umma_bf16_ta(tmem + x * kTileCols + kOCol, tmem + x * kTileCols + kSCol + kk * 8,
-                     umma_desc_sw128_mn(sv + (kk & 7) * 2048, kHalf), idesc_o, (keep || kk > 0) ? 1u : 0u);
-      };
-      // a commit covers every product before it
-      auto s_done = [&](int x, const Step& t) {
-        umma_commit(s_full(x));
-        if (--s_left == 0) umma_commit(empty(2 * t.i));
-        nq[x] += t.first;
-        any = true;
-      };
-      auto pv_end = [&](int x, const Step& t) {
-        umma_commit(pv_done(x));
-        if (--pv_left == 0) umma_commit(empty(2 * t.i + 1));
-        ++npv[x];
-        ++np[x];
-      };
-      auto s_all = [&](int x, const Step& t) {
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) s_step(x, t, kk);
-        s_done(x, t);
-      };
-      auto pv_all = [&](int x, const Step& t) {
-        tc_fence_after();
-        const bool keep = !t.first || o_begun[x] != 0;
-#pragma unroll
-        for (int kk = 0; kk < KP; ++kk) pv_step(x, t, kk, keep);
-        pv_end(x, t);
-      };
-      Step cur = advance();
-      s_left = cur.tiles == 3 ? 2 : 1;
-      for (int x = 0; x < 2 && ok; ++x)
-        if ((cur.tiles >> x) & 1) {
-          ok = s_wait(x, cur);
-          if (ok) s_all(x, cur);
-        }
-      while (cur.more && ok) {
-        const Step nxt = advance();
-        int todo = nxt.more ? nxt.tiles : 0;
-        s_left = __popc(todo);
-        pv_left = __popc(cur.tiles);
-        if (cur.tiles == 3) {
-          if (!(ok = pv_wait(0, cur))) break;
-          pv_all(0, cur);
-          if (!(ok = pv_wait(1, cur))) break;
-          if (todo & 1) {
-            if (!(ok = s_wait(0, nxt))) break;
-            tc_fence_after();
-            const bool keep = !cur.first || o_begun[1] != 0;
-#pragma unroll
-            for (int kk = 0; kk < (KP > KS ? KP : KS); ++kk) {
-              if (kk < KP) pv_step(1, cur, kk, keep);
-              if (kk < KS) s_step(0, nxt, kk);
-            }
-            pv_end(1, cur);
-            s_done(0, nxt);
-            todo &= ~1;
-          } else {
-            pv_all(1, cur);
+      while ((pv_left | s_left) != 0) {
+        const uint32_t free = s_left & ~pv_left;
+        uint32_t px = 2, sx = 2;
+        if ((free & 1) && s_ready(0)) sx = 0;
+        else if ((free & 2) && s_ready(1)) sx = 1;
+        else if ((pv_left & 1) && pv_ready(0)) px = 0;
+        else if ((pv_left & 2) && pv_ready(1)) px = 1;
+        else {
+          if (++spins >= kSpinLimit || ((spins & 255) == 0 && *flag != 0)) {
+            ok = false;
+            break;
           }
+          continue;
+        }
+        spins = 0;
+        tc_fence_after();
+        // (a commit covers every product before it)
+        if (sx != 2) {
+          const uint64_t qd = qdesc + sx * (TB >> 4), kd = kdesc + nxt.k_slot * (TB >> 4);
+          const uint32_t to = tmem + sx * kTileCols + kSCol;
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk)
+            umma_bf16(to, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+          umma_commit(s_full(sx));
+          s_left &= ~(1u << sx);
+          if (s_left == 0) umma_commit(empty(2 * nxt.i));
+          if (nxt.first) at_q ^= 1u << sx;
+          any = true;
         } else {
-          // one tile's P V, and S of the next step on the other: whichever is ready first
-          const int x = (int)(cur.i & 1);
-          bool other = (todo >> (x ^ 1)) & 1, pv = true;
-          for (uint32_t i = 0; (pv || other) && ok; ++i) {
-            if (other && s_test(x ^ 1, nxt)) {
-              s_all(x ^ 1, nxt);
-              todo &= 1 << x;
-              other = false;
-            }
-            if (pv && pv_test(x, cur)) {
-              pv_all(x, cur);
-              pv = false;
-            }
-            ok = i < kSpinLimit && ((i & 255) != 255 || *flag == 0);
-          }
-          if (!ok) break;
+          const bool keep = !cur.first || o_begun[px] != 0;
+          const uint64_t vd = vdesc + cur.v_slot * (TB >> 4);
+          const uint32_t to = tmem + px * kTileCols + kOCol, from = tmem + px * kTileCols + kSCol;
+#pragma unroll
+          for (int kk = 0; kk < KP; ++kk) umma_bf16_ta(to, from + kk * 8, vd + ((kk & 7) * 2048 >> 4), idesc_o, (keep || kk > 0) ? 1u : 0u);
+          umma_commit(pv_done(px));
+          pv_left &= ~(1u << px);
+          if (pv_left == 0) umma_commit(empty(2 * cur.i + 1));
+          at_p ^= 1u << px;
+          last_pv ^= 1u << px;
+          await_pv |= 1u << px;
         }
-        for (int x = 0; x < 2 && ok; ++x)
-          if ((todo >> x) & 1) {
-            ok = s_wait(x, nxt);
-            if (ok) s_all(x, nxt);
-          }
-        cur = nxt;
+        if ((pv_left | s_left) == 0) {
+          cur = nxt;
+          nxt = advance();
+          pv_left = cur.tiles;
+          s_left = nxt.tiles;
+          k_there = v_there = false;
+        }
       }
       if (!ok) rows_fail(a, flag, kRowsMma);
       if (any) {
@@ -904,15 +843,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
     constexpr float kShift = SPLIT ? 0.f : (KIND == kBf16 ? -8.f : 13.f);
     uint32_t n = 0, n_merged = 0;                   // steps of this tile, meetings of the softmax warps so far
     bool ok = true;
-    // a piece's rows: blocks of 32 in a tile (its other rows are copies), and whether this tile has a step of it
-    auto blocks = [](int rows) { return rows > 64 ? 4 : rows > 32 ? 2 : 1; };
+    // small: a piece's rows are one block of 32 in a tile, with four copies; whether the tile has a step of a piece
     auto has_steps = [&](const RowsPiece& t, int i0) {
       return t.item->rows > kTileRows || t.s1 - t.s0 > 1 || (i0 & 1) == x;
     };
     // this thread's query row of a piece: into shared memory, swizzled; returns the factor taken out of it
     auto load_q = [&](const RowsPiece& t) -> float {
       const int rows = t.item->rows;
-      const int i = rows > kTileRows ? x * kTileRows + row : row & (32 * blocks(rows) - 1), r = t.item->row0 + i;
+      const int i = rows > kTileRows ? x * kTileRows + row : rows <= 32 ? lane : row, r = t.item->row0 + i;
       const bool live = i < rows;
       uint4 y[D / 8];
       const int tok = r / a.G, h = r - tok * a.G;
@@ -952,234 +890,206 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
       if (lane == 0) mbar_arrive(bar(kBarMerge));
       return __all_sync(0xffffffffu, rows_wait(bar(kBarMerge), n_merged++ & 1, flag));
     };
-    RowsPiece cur;
-    bool more = walk.next(a, cur);
+    RowsPiece cur{nullptr, 0, 0, 0};                // (none before the first)
     int i0 = 0;                                     // the piece's first step among the CTA's
-    float by = more && has_steps(cur, i0) ? load_q(cur) : 1.f;
-    while (more && ok) {
-      const RowsItem& it = *cur.item;
-      const int rows = it.rows, nb = blocks(rows);
-      const bool two = rows > kTileRows;
-      const int i = two ? x * kTileRows + row : row & (32 * nb - 1), copy = two ? 0 : quarter / nb;
+    float by = 1.f;
+    do {
+      const bool now = cur.item != nullptr;
+      const RowsItem& it = now ? *cur.item : start.item;
+      const int rows = now ? it.rows : 0;
+      const bool two = rows > kTileRows, small = rows <= 32;
+      const int i = two ? x * kTileRows + row : small ? lane : row, copy = small ? quarter : 0;
       const int r = it.row0 + i, tok = r / a.G, h = cur.g * a.G + (r - tok * a.G);
-      const int k0 = it.k0, k_lo = it.lo, k_hi = it.hi, full_lo = it.full_lo, full_hi = it.full_hi;
       const bool live = i < rows;
-      const int pos = !live ? -1 : a.prefix ? (int)a.lens[it.token0 + tok] - 1 : it.base + tok;
-      const int low = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
-      const float ksc = a.scale * (a.k_scale != nullptr ? a.k_scale[cur.g] : 1.f) * by;
-      RowsScore score;
-      score.capped = a.softcap != 0.f;
-      score.sc = ksc * kLog2e;
-      score.icap = score.capped ? ksc / a.softcap : 0.f;
-      score.cap2 = a.softcap * kLog2e;
-      score.slope = a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
-      const bool general = score.capped || a.slopes != nullptr || !(a.k_scale == nullptr || a.k_scale[cur.g] > 0.f);
       const bool idle = __all_sync(0xffffffffu, !live);         // a warp of padding alone
       float m = -INFINITY, mo = 0.f, l = 0.f;
-      bool begun = false, had = false;
-      if (lane == 0 && quarter == 0) o_begun[x] = 0;            // (before the piece's first weights are told of)
-      uint32_t step = i0;
-      for (int s = cur.s0; s < cur.s1; ++s, ++step) {
-        if (!two && (int)(step & 1) != x) continue;
-        ok = __all_sync(0xffffffffu, rows_wait(s_full(x), n & 1, flag));
-        if (!ok) break;
-        ++n;
-        tc_fence_after();
-        const int t0 = k0 + kTileKeys * s;
-        const uint4 there = *reinterpret_cast<const uint4*>(&seen_w[(step & 7) * 4]);
-        const bool whole = t0 >= full_lo && t0 + kTileKeys <= full_hi && (there.x & there.y & there.z & there.w) == 0xffffffffu;
-        if (rows_partial(k_lo, k_hi, full_lo, full_hi, t0)) {
-          ok = __all_sync(0xffffffffu, rows_wait(full(2 * step + 1), use(2 * step + 1), flag));
+      bool had = false;
+      if (now) {
+        const int k0 = it.k0, k_lo = it.lo, k_hi = it.hi, full_lo = it.full_lo, full_hi = it.full_hi;
+        const int pos = !live ? -1 : a.prefix ? (int)a.lens[it.token0 + tok] - 1 : it.base + tok;
+        const int low = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+        const float head_scale = a.k_scale != nullptr ? a.k_scale[cur.g] : 1.f, ksc = a.scale * head_scale * by;
+        RowsScore score;
+        score.capped = a.softcap != 0.f;
+        score.sc = ksc * kLog2e;
+        score.icap = score.capped ? ksc / a.softcap : 0.f;
+        score.cap2 = a.softcap * kLog2e;
+        score.slope = a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
+        score.general = score.capped || a.slopes != nullptr || !(head_scale > 0.f);
+        const float mul = score.general ? 1.f : score.sc;
+        bool begun = false;
+        if (lane == 0 && quarter == 0) o_begun[x] = 0;          // (before the piece's first weights are told of)
+        uint32_t step = i0;
+#pragma unroll 1
+        for (int s = cur.s0; s < cur.s1; ++s, ++step) {
+          if (!two && (int)(step & 1) != x) continue;
+          ok = __all_sync(0xffffffffu, rows_wait(s_full(x), n & 1, flag));
           if (!ok) break;
-          uint4 bad = *reinterpret_cast<const uint4*>(&bad_w[(step & 7) * 4]);
-          if ((bad.x | bad.y | bad.z | bad.w) != 0) {
-            if (nb < 4) {                                       // a copy adds those of its own keys
-              if (copy * nb > 0 || copy * nb + nb <= 0) bad.x = 0;
-              if (copy * nb > 1 || copy * nb + nb <= 1) bad.y = 0;
-              if (copy * nb > 2 || copy * nb + nb <= 2) bad.z = 0;
-              if (copy * nb > 3 || copy * nb + nb <= 3) bad.w = 0;
+          ++n;
+          tc_fence_after();
+          const int t0 = k0 + kTileKeys * s;
+          const uint4 there = *reinterpret_cast<const uint4*>(&seen_w[(step & 7) * 4]);
+          const bool whole = t0 >= full_lo && t0 + kTileKeys <= full_hi && (there.x & there.y & there.z & there.w) == 0xffffffffu;
+          if (rows_partial(k_lo, k_hi, full_lo, full_hi, t0)) {
+            ok = __all_sync(0xffffffffu, rows_wait(full(2 * step + 1), use(2 * step + 1), flag));
+            if (!ok) break;
+            uint4 bad = *reinterpret_cast<const uint4*>(&bad_w[(step & 7) * 4]);
+            if ((bad.x | bad.y | bad.z | bad.w) != 0) {
+              if (small) bad = make_uint4(copy == 0 ? bad.x : 0, copy == 1 ? bad.y : 0, copy == 2 ? bad.z : 0, copy == 3 ? bad.w : 0);
+              add_bad_rows<D, KIND>(a, static_cast<const uint8_t*>(a.v) + (int64_t)cur.g * a.head_stride * elem_bytes<KIND>(), it.table, t0, pos,
+                                    bad, tm + kOCol, !had);
+              if (!had) begun = true;
+              if (!had && lane == 0 && quarter == 0) o_begun[x] = 1;
             }
-            add_bad_rows<D, KIND>(a, static_cast<const uint8_t*>(a.v) + (int64_t)cur.g * a.head_stride * elem_bytes<KIND>(), it.table, t0, pos,
-                                  bad, tm + kOCol, !had);
-            if (!had) begun = true;
-            if (!had && lane == 0 && quarter == 0) o_begun[x] = 1;
           }
+          if (!idle) {
+            if (!whole || score.general) {
+              const int from = low - t0, to = pos + 1 - t0;     // keys of the step that the row sees: [from, to)
+              uint32_t word[4] = {there.x, there.y, there.z, there.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int lo = min(32, max(0, from - 32 * k)), hi = min(32, max(0, to - 32 * k));
+                const uint32_t below_hi = hi >= 32 ? 0xffffffffu : (1u << hi) - 1u, below_lo = lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
+                word[k] = live ? word[k] & below_hi & ~below_lo : 0u;
+              }
+              if (small) word[0] = copy == 0 ? word[0] : copy == 1 ? word[1] : copy == 2 ? word[2] : word[3];
+              rows_scores(tm + kSCol + 32 * copy, small ? 1 : 4, score, (float)(t0 + 32 * copy - pos), make_uint4(word[0], word[1], word[2], word[3]));
+            }
+            float alpha;
+            if (small) alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, copy, mul, m, mo, l);
+            else alpha = rows_step<KIND, SPLIT, 1>(tm + kSCol, 0, mul, m, mo, l);
+            // O of the tile's step before is final (this step's S was issued behind its P V)
+            if ((had || begun) && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float f[32];
+                uint32_t y[32];
+                tmem_ld32(tm + kOCol + c, f);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(f[e] * alpha);
+                tmem_st32(tm + kOCol + c, y);
+              }
+            }
+            tmem_wait_st();
+          }
+          had = true;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(x));
         }
-        if (!idle) {
-          // keys of the thread's part of the step that the row sees, by 32
-          uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-          if (!whole) {
-            const int from = low - t0, to = pos + 1 - t0;
-            const uint32_t word[4] = {there.x, there.y, there.z, there.w};
-            uint32_t all[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int lo = min(32, max(0, from - 32 * k)), hi = min(32, max(0, to - 32 * k));
-              const uint32_t below_hi = hi >= 32 ? 0xffffffffu : (1u << hi) - 1u, below_lo = lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
-              all[k] = live ? word[k] & below_hi & ~below_lo : 0u;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) see[k] = all[k];
-            if (nb == 2 && copy == 1) see[0] = all[2], see[1] = all[3];
-            if (nb == 1) see[0] = copy == 0 ? all[0] : copy == 1 ? all[1] : copy == 2 ? all[2] : all[3];
-          }
-          const float d0 = (float)(t0 - pos);
-          float alpha;
-          const bool fast = whole && !general;
-          if (nb == 4) {
-            if (fast) alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, 0, score, d0, see, false, true, m, mo, l);
-            else alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, 0, score, d0, see, general, whole, m, mo, l);
-          } else if (nb == 2) {
-            alpha = rows_step<KIND, SPLIT, 2>(tm + kSCol, copy, score, d0, see, general, whole, m, mo, l);
-          } else {
-            alpha = rows_step<KIND, SPLIT, 1>(tm + kSCol, copy, score, d0, see, general, whole, m, mo, l);
-          }
-          // O of the tile's step before is final (this step's S was issued behind its P V)
-          if ((had || begun) && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              float f[32];
-              uint32_t y[32];
-              tmem_ld32(tm + kOCol + c, f);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(f[e] * alpha);
-              tmem_st32(tm + kOCol + c, y);
-            }
-          }
-          tmem_wait_st();
+        if (ok && had) {
+          // the piece's last P V; its queries are read by then
+          ok = __all_sync(0xffffffffu, rows_wait(pv_done(x), (n - 1) & 1, flag));
+          tc_fence_after();
         }
-        had = true;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(x));
-      }
-      if (!ok) break;
-      RowsPiece nxt;
-      const bool has_next = walk.next(a, nxt);
-      const int i_next = i0 + cur.s1 - cur.s0;
-      float by_next = 1.f;
-      // the next piece's queries (this tile's last S is done with its own), then this piece's result; a merge needs the room first
-      if (two && has_next && has_steps(nxt, i_next)) by_next = load_q(nxt);
-      if (had) {
-        ok = __all_sync(0xffffffffu, rows_wait(pv_done(x), (n - 1) & 1, flag));
         if (!ok) break;
-        tc_fence_after();
       }
-      const bool final = !a.prefix && cur.starts() && cur.ends();
+      const bool final = now && !a.prefix && cur.starts() && cur.ends();
       const float vsc = a.v_scale != nullptr ? a.v_scale[cur.g] : 1.f;
       const int64_t out = ((int64_t)it.token0 + tok) * a.h_q + h;
       const int64_t prow = rows_part(a, cta, cur.starts(), cur.g, it);
-      if (two) {
-        if (!idle) {
-          const float f = !final ? 1.f : l == 0.f ? 0.f : (SPLIT ? vsc / weight_unit<KIND>() : vsc) / l;
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            float y[32];
-            __syncwarp();
-            tmem_ld32(tm + kOCol + c, y);
-            if (!live) continue;
-            if (final) {
-              uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + c);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t b[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float y0 = y[8 * e + 2 * k] * f, y1 = y[8 * e + 2 * k + 1] * f;
-                  b[k] = a.out_f16 ? pack16<kF16>(y0, y1) : pack16<kBf16>(y0, y1);
-                }
-                to[e] = make_uint4(b[0], b[1], b[2], b[3]);
-              }
-            } else {
-              // four values of a row next to those of the next row
-              float4* to = reinterpret_cast<float4*>(a.part + prow * D) + (int64_t)(c / 4) * rows + i;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) to[(int64_t)e * rows] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-            }
-          }
-        }
-      } else {
-        // What the tiles and copies hold of a row, in the queries' room once both tiles' products are done with them.  Warp w has
-        // block w mod nb; offsets and sums meet first, then D / 4 columns at a time in one of two buffers, where every
-        // warp sums its share of its block's columns, each part times 2^(m - M).
+      const bool f16 = KIND == kE4m3 ? a.out_f16 != 0 : KIND == kF16;
+      auto pack = [&](float u, float v) { return f16 ? pack16<kF16>(u, v) : pack16<kBf16>(u, v); };
+      // factor on O: to the output, or none to the partial sums
+      auto factor = [&](float sum) { return !final ? 1.f : sum == 0.f ? 0.f : (SPLIT ? vsc / weight_unit<KIND>() : vsc) / sum; };
+      if (now && !two) {
+        // What the tiles and copies hold of a row, in the queries' room once both tiles' products are done with them: offsets and
+        // sums meet first, then D / 4 columns at a time in one of two buffers, where every warp sums its share of its rows'
+        // columns, each part times 2^(m - M).  With copies all warps hold parts of the same 32 rows, else two.
         if (!(ok = meet())) break;
         constexpr int COLS = D / 4;
         float* buf = reinterpret_cast<float*>(sbase);
         float2* ml = reinterpret_cast<float2*>(buf + 8 * COLS * 32);
         ml[warp * 32 + lane] = make_float2(m, l);
-        auto merge = [&](auto blocks_c) {
-          constexpr int NB = decltype(blocks_c)::value, PARTS = 8 / NB, OWN = COLS * NB / 8;    // parts of a row, columns of a warp
-          const int block = warp % NB, c0 = warp / NB * OWN;
-          float f[PARTS], M = -INFINITY, L = 0.f;
+        const int parts = small ? 8 : 2, first = small ? 0 : quarter, step = small ? 1 : 4;     // parts of a row: warps first + k step
+        const int own = COLS / parts, c0 = (small ? warp : x) * own;                            // columns of a warp
+        float f[8];
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float* b = buf + (q & 1) * 8 * COLS * 32;
-            __syncwarp();
-            if (had && !idle) {
-              float y[COLS];
-              if constexpr (COLS == 32) tmem_ld32(tm + kOCol + q * COLS, y);
-              else tmem_ld16(tm + kOCol + q * COLS, y);
+        for (int q = 0; q < 4 && ok; ++q) {
+          float* b = buf + (q & 1) * 8 * COLS * 32;
+          float y[COLS];
+          __syncwarp();
+          if (had && !idle) {
+            if constexpr (COLS == 32) tmem_ld32(tm + kOCol + q * COLS, y);
+            else tmem_ld16(tm + kOCol + q * COLS, y);
+          } else {
 #pragma unroll
-              for (int e = 0; e < COLS; ++e) b[(warp * COLS + e) * 32 + lane] = y[e];
-            } else {
-#pragma unroll
-              for (int e = 0; e < COLS; ++e) b[(warp * COLS + e) * 32 + lane] = 0.f;
-            }
-            if (!(ok = meet())) return;
-            if (q == 0) {
-#pragma unroll
-              for (int k = 0; k < PARTS; ++k) M = fmaxf(M, ml[(block + NB * k) * 32 + lane].x);
-#pragma unroll
-              for (int k = 0; k < PARTS; ++k) {
-                const float2 y = ml[(block + NB * k) * 32 + lane];
-                f[k] = y.x == M ? 1.f : exp2f(y.x - M);
-                L += y.y * f[k];
-              }
-              if (!(ok = meet())) return;           // (the second buffer is read)
-              m = M;
-              l = L;
-              const float g = !final ? 1.f : L == 0.f ? 0.f : (SPLIT ? vsc / weight_unit<KIND>() : vsc) / L;
-#pragma unroll
-              for (int k = 0; k < PARTS; ++k) f[k] *= g;
-            }
-            float y[OWN];
-#pragma unroll
-            for (int e = 0; e < OWN; ++e) {
-              y[e] = 0.f;
-#pragma unroll
-              for (int k = 0; k < PARTS; ++k) y[e] = fmaf(b[((block + NB * k) * COLS + c0 + e) * 32 + lane], f[k], y[e]);
-            }
-            if (!live) continue;
-            const int col = q * COLS + c0;
-            if (final) {
-              uint32_t* to = static_cast<uint32_t*>(a.o) + (out * D + col) / 2;
-#pragma unroll
-              for (int e = 0; e < OWN; e += 2) to[e / 2] = a.out_f16 ? pack16<kF16>(y[e], y[e + 1]) : pack16<kBf16>(y[e], y[e + 1]);
-            } else {
-              float* to = a.part + prow * D;
-#pragma unroll
-              for (int e = 0; e < OWN; e += 2)
-                *reinterpret_cast<float2*>(to + ((int64_t)((col + e) / 4) * rows + i) * 4 + ((col + e) & 2)) = make_float2(y[e], y[e + 1]);
-            }
+            for (int e = 0; e < COLS; ++e) y[e] = 0.f;
           }
-          ok = meet();                              // the buffers are read
-        };
-        if (nb == 4) merge(std::integral_constant<int, 4>{});
-        else if (nb == 2) merge(std::integral_constant<int, 2>{});
-        else merge(std::integral_constant<int, 1>{});
+#pragma unroll
+          for (int e = 0; e < COLS; ++e) b[(warp * COLS + e) * 32 + lane] = y[e];
+          if (!(ok = meet())) break;
+          if (q == 0) {
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) M = fmaxf(M, k < parts ? ml[(first + step * k) * 32 + lane].x : -INFINITY);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 z = k < parts ? ml[(first + step * k) * 32 + lane] : make_float2(-INFINITY, 0.f);
+              f[k] = z.x == M ? 1.f : exp2f(z.x - M);
+              if (k < parts) L += z.y * f[k];
+            }
+            if (!(ok = meet())) break;              // (the second buffer is read)
+            m = M;
+            l = L;
+            const float g = factor(L);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= g;
+          }
+#pragma unroll 1
+          for (int e = c0; e < c0 + own; e += 2) {
+            float u = 0.f, v = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < parts) {
+                u = fmaf(b[((first + step * k) * COLS + e) * 32 + lane], f[k], u);
+                v = fmaf(b[((first + step * k) * COLS + e + 1) * 32 + lane], f[k], v);
+              }
+            const int col = q * COLS + e;
+            if (live && final) static_cast<uint32_t*>(a.o)[(out * D + col) / 2] = pack(u, v);
+            else if (live) *reinterpret_cast<float2*>(a.part + prow * D + ((int64_t)(col / 4) * rows + i) * 4 + (col & 2)) = make_float2(u, v);
+          }
+        }
+        if (ok) ok = meet();                        // the buffers are read
         if (!ok) break;
-        if (has_next && has_steps(nxt, i_next)) by_next = load_q(nxt);
       }
-      if (live && (two || warp / nb == 0)) {
+      // the next piece's queries, then what is left of this one's result
+      RowsPiece nxt{nullptr, 0, 0, 0};
+      (void)walk.next(a, nxt);
+      const int i_next = i0 + cur.s1 - cur.s0;
+      float by_next = 1.f;
+      if (nxt.item != nullptr && has_steps(nxt, i_next)) by_next = load_q(nxt);
+      if (now && two && !idle) {
+        const float f = factor(l);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float y[32];
+          __syncwarp();
+          tmem_ld32(tm + kOCol + c, y);
+          if (!live) continue;
+          if (final) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              to[e] = make_uint4(pack(y[8 * e] * f, y[8 * e + 1] * f), pack(y[8 * e + 2] * f, y[8 * e + 3] * f), pack(y[8 * e + 4] * f, y[8 * e + 5] * f),
+                                 pack(y[8 * e + 6] * f, y[8 * e + 7] * f));
+          } else {
+            // four values of a row next to those of the next row
+            float4* to = reinterpret_cast<float4*>(a.part + prow * D) + (int64_t)(c / 4) * rows + i;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) to[(int64_t)e * rows] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          }
+        }
+      }
+      if (live && (two || (small ? warp == 0 : x == 0))) {
         if (!final) a.part_ml[prow + i] = make_float2(m, l);
         else if (a.lse != nullptr) a.lse[out] = (m + log2f(l) - kShift) * 0.6931471805599453f;
       }
       tc_fence_before();
       cur = nxt;
-      more = has_next;
       by = by_next;
       i0 = i_next;
-    }
+    } while (cur.item != nullptr);
     if (!ok && lane == 0) rows_fail(a, flag, kRowsSoftmax);
   }
   tc_fence_before();
