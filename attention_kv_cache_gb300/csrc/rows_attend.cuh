@@ -6,8 +6,8 @@
 // items' steps of all KV heads, laid end to end, are dealt evenly to one CTA per SM; a piece is what a CTA has of an item.
 // Pieces that are not a whole item leave partial sums, which rows_join merges.
 //
-// Roles of the 16 warps: 0-3 and 4-7 softmax of tile A and B, a thread per row of the tile; 8-11 load K and V; 12 issues the
-// products.  S = Q K^T goes to TMEM; the softmax reads it, keeps an exponent offset that moves only when a row's largest
+// Roles of the 16 warps: 0-3 and 4-7 softmax of tile A and B, a thread per row of the tile; 8-11 load K and V; 12 issues
+// the products S, 13 P V.  S = Q K^T goes to TMEM; the softmax reads it, keeps an exponent offset that moves only when a row's largest
 // score passes it by 2^lag (so O is rescaled rarely) and writes the weights over S as 16-bit values, which O += P V takes from
 // TMEM with V as it lies.
 //
@@ -55,7 +55,7 @@ template <int D, int KIND>
 constexpr size_t rows_smem() { return rows_bar_off<D, KIND>() + 1024 + 1024; }
 // barriers: full and empty of the slots, then of the tiles s_full, p_full, pv_done and q_full, the merge's, of the loader
 // warps one each for rows that are looked at before they count, and one each per raw tile
-constexpr int kBarEmpty = 8, kBarTiles = 16, kBarMerge = 24, kBarDrain = 25, kBarLand = 26, kBarRaw = 30, kRowsBars = kBarRaw + 4 * kRawTiles;
+constexpr int kBarEmpty = 8, kBarTiles = 16, kBarMerge = 24, kBarDrain = 25, kBarLand = 27, kBarRaw = 31, kRowsBars = kBarRaw + 4 * kRawTiles;
 constexpr uint32_t kWordsOff = 512;              // behind the barriers: misc, then the words of 8 steps twice
 static_assert(kRowsBars * 8 <= kWordsOff, "barriers lie before the words");
 
@@ -410,8 +410,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
       mbar_init(q_full(x), 4);
     }
     mbar_init(bar(kBarMerge), 8);
-    mbar_init(bar(kBarDrain), 1);
-    for (int i = kBarLand; i < kRowsBars; ++i) mbar_init(bar(i), 1);
+    for (int i = kBarDrain; i < kRowsBars; ++i) mbar_init(bar(i), 1);
     *flag = 0;
     o_begun[0] = o_begun[1] = 0;
     fence_barrier_init();
@@ -732,105 +731,71 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
     }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegMma));
-    // ---------------------------------------------------------------- products
-    if (warp == 12 && lane == 0) {
+    // ---------------------------------------------------------------- products, a thread for S and one for P V: each of
+    // them spends as long on waits and commits as the tensor cores on its products
+    if (warp <= 13 && lane == 0) {
       walk.begin(start);
+      const bool pv = warp == 13;
       constexpr uint32_t idesc_s = rows_idesc<KIND>(128, 128), idesc_o = rows_idesc<KIND>(128, D) | kUmmaBMajorMN;
       constexpr int KS = D / 16, KP = kTileKeys / 16 * (SPLIT ? 2 : 1);
       const uint64_t vdesc = umma_desc_sw128_mn(slots, kHalf), kdesc = umma_desc_sw128(slots), qdesc = umma_desc_sw128(base);
-      // a step: its number among the CTA's, its tiles (both, or the one whose turn it is), whether it is their first of the
-      // piece, and the slots of its K and V
-      struct Step {
-        uint32_t i, tiles, k_slot, v_slot;
-        bool first;
-      };
-      bool have = walk.next(a, p);
-      int s = have ? p.s0 : 0;
-      uint32_t count = 0;
-      auto advance = [&]() -> Step {
-        Step r{count, 0u, 2 * count % NS, (2 * count + 1) % NS, false};
-        if (!have) return r;
+      uint32_t q = pv ? 1 : 0, slot = q, turn = 0;  // the step's K (V) tile, its slot, the tile whose turn it is
+      uint32_t phase = 0;                           // of the slot
+      uint32_t at = 0, last_pv = 3, was_pv = 0;     // by tile: parity of the next queries (weights), of the last P V; whether there was one
+      bool ok = true, any = false;
+      while (ok && walk.next(a, p)) {
         const bool two = p.item->rows > kTileRows;
-        r.tiles = two ? 3u : 1u << (count & 1);
-        r.first = s < p.s0 + (two ? 1 : 2);
-        ++count;
-        if (++s == p.s1) {
-          have = walk.next(a, p);
-          s = p.s0;
-        }
-        return r;
-      };
-      // by tile: parity of the next queries and weights, of the last P V, and whether that is not known to be done
-      uint32_t at_q = 0, at_p = 0, last_pv = 3, await_pv = 0;
-      // `cur` has tiles whose P V is left, `nxt` tiles whose S is
-      Step cur{0, 0, 0, 0, false}, nxt = advance();
-      uint32_t pv_left = 0, s_left = nxt.tiles, spins = 0;
-      bool k_there = false, v_there = false, ok = true, any = false;
-      // S of a step may start once K has landed, the tile's queries are there, and its last P V (which reads the same TMEM
-      // columns) is done; P V once V has landed and the weights are written.  S first: the softmax waits for it.
-      auto s_ready = [&](uint32_t x) {
-        if (((await_pv >> x) & 1) && !rows_test(pv_done(x), (last_pv >> x) & 1)) return false;
-        await_pv &= ~(1u << x);
-        if (!k_there && !(k_there = rows_test(full(2 * nxt.i), use(2 * nxt.i)))) return false;
-        return !nxt.first || rows_test(q_full(x), (at_q >> x) & 1);
-      };
-      auto pv_ready = [&](uint32_t x) {
-        if (!rows_test(p_full(x), (at_p >> x) & 1)) return false;
-        return v_there || (v_there = rows_test(full(2 * cur.i + 1), use(2 * cur.i + 1)));
-      };
-      while ((pv_left | s_left) != 0) {
-        const uint32_t free = s_left & ~pv_left;
-        uint32_t px = 2, sx = 2;
-        if ((free & 1) && s_ready(0)) sx = 0;
-        else if ((free & 2) && s_ready(1)) sx = 1;
-        else if ((pv_left & 1) && pv_ready(0)) px = 0;
-        else if ((pv_left & 2) && pv_ready(1)) px = 1;
-        else {
-          if (++spins >= kSpinLimit || ((spins & 255) == 0 && *flag != 0)) {
-            ok = false;
-            break;
+        const int s0 = p.s0, s1 = p.s1;
+        for (int s = s0; s < s1 && ok; ++s) {
+          const bool first = s < s0 + (two ? 1 : 2);
+          const uint32_t x0 = two ? 0 : turn, x1 = two ? 1 : turn;
+          ok = rows_wait(bar(slot), phase, flag);   // the tile has landed
+          for (uint32_t x = x0; x <= x1 && ok; ++x) {
+            if (pv) {
+              // P V once the weights are written
+              if (!(ok = rows_wait(p_full(x), (at >> x) & 1, flag))) break;
+              at ^= 1u << x;
+              tc_fence_after();
+              const bool keep = !first || o_begun[x] != 0;
+              const uint64_t vd = vdesc + slot * (TB >> 4);
+              const uint32_t to = tmem + x * kTileCols + kOCol, from = tmem + x * kTileCols + kSCol;
+#pragma unroll
+              for (int kk = 0; kk < KP; ++kk) umma_bf16_ta(to, from + kk * 8, vd + ((kk & 7) * 2048 >> 4), idesc_o, (keep || kk > 0) ? 1u : 0u);
+              umma_commit(pv_done(x));
+            } else {
+              // S once the tile's queries are there and its last P V (which reads the same TMEM columns) is done
+              if (first) {
+                if (!(ok = rows_wait(q_full(x), (at >> x) & 1, flag))) break;
+                at ^= 1u << x;
+              }
+              if ((was_pv >> x) & 1) {
+                if (!(ok = rows_wait(pv_done(x), (last_pv >> x) & 1, flag))) break;
+              }
+              was_pv |= 1u << x;
+              last_pv ^= 1u << x;                   // (0 for the first: what the tile's second S waits for)
+              tc_fence_after();
+              const uint64_t qd = qdesc + x * (TB >> 4), kd = kdesc + slot * (TB >> 4);
+              const uint32_t to = tmem + x * kTileCols + kSCol;
+#pragma unroll
+              for (int kk = 0; kk < KS; ++kk)
+                umma_bf16(to, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
+              umma_commit(s_full(x));
+            }
+            any = true;
           }
-          continue;
-        }
-        spins = 0;
-        tc_fence_after();
-        // (a commit covers every product before it)
-        if (sx != 2) {
-          const uint64_t qd = qdesc + sx * (TB >> 4), kd = kdesc + nxt.k_slot * (TB >> 4);
-          const uint32_t to = tmem + sx * kTileCols + kSCol;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk)
-            umma_bf16(to, qd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), kd + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0);
-          umma_commit(s_full(sx));
-          s_left &= ~(1u << sx);
-          if (s_left == 0) umma_commit(empty(2 * nxt.i));
-          if (nxt.first) at_q ^= 1u << sx;
-          any = true;
-        } else {
-          const bool keep = !cur.first || o_begun[px] != 0;
-          const uint64_t vd = vdesc + cur.v_slot * (TB >> 4);
-          const uint32_t to = tmem + px * kTileCols + kOCol, from = tmem + px * kTileCols + kSCol;
-#pragma unroll
-          for (int kk = 0; kk < KP; ++kk) umma_bf16_ta(to, from + kk * 8, vd + ((kk & 7) * 2048 >> 4), idesc_o, (keep || kk > 0) ? 1u : 0u);
-          umma_commit(pv_done(px));
-          pv_left &= ~(1u << px);
-          if (pv_left == 0) umma_commit(empty(2 * cur.i + 1));
-          at_p ^= 1u << px;
-          last_pv ^= 1u << px;
-          await_pv |= 1u << px;
-        }
-        if ((pv_left | s_left) == 0) {
-          cur = nxt;
-          nxt = advance();
-          pv_left = cur.tiles;
-          s_left = nxt.tiles;
-          k_there = v_there = false;
+          if (!ok) break;
+          umma_commit(bar(kBarEmpty + slot));       // (a commit covers every product of its thread before it)
+          turn ^= 1;
+          q += 2;
+          slot += 2;
+          if (slot >= NS) slot -= NS;
+          phase = (q / NS) & 1;
         }
       }
       if (!ok) rows_fail(a, flag, kRowsMma);
       if (any) {
-        umma_commit(bar(kBarDrain));
-        if (!mbar_wait(bar(kBarDrain), 0)) set_device_error(a.err, KVSEL_ERR_TIMEOUT, kRowsDrain);
+        umma_commit(bar(kBarDrain + (pv ? 1 : 0)));
+        if (!mbar_wait(bar(kBarDrain + (pv ? 1 : 0)), 0)) set_device_error(a.err, KVSEL_ERR_TIMEOUT, kRowsDrain);
       }
     }
   } else {
