@@ -5,13 +5,14 @@
 
 namespace kvsel {
 
-constexpr int kSliceKeys = 8192;      // tokens of one row that a CTA selects from
+constexpr int kSliceKeys = 8192;      // tokens of one row that a CTA takes at a time
 constexpr int kMaxBeams = 64, kMaxBeamOut = 64;
-constexpr int64_t kMaxLists = 8192;   // slices of a set's rows
+constexpr int64_t kMaxLists = 8192;   // slices of a set's rows, and segments at most
 
 // ---- beam_select.cu ----------------------------------------------------------------------
 struct SelectArgs {
-  int32_t batch, beams, n_out, vocab, slices, pad_token;
+  int32_t batch, beams, n_out, vocab, pad_token;
+  int32_t segments, seg_slices;         // of a row, and slices of a segment
   int64_t row_stride;
   const void* logits;
   const float* scores;
@@ -19,10 +20,10 @@ struct SelectArgs {
   float* scores_out;
   int32_t *parents, *tokens;
   float* lse;
-  float2* best;         // [row][slice][n_out]: a slice's best tokens, (logit, token as bits) in order; token -1: none
-  double2* sums;        // [row][slice]: largest logit, sum of exp(x - largest)
+  float2* best;         // [row][segment][n_out]: a segment's best tokens, (logit, token as bits) in order; token -1: none
+  double2* sums;        // [row][segment]: largest logit, sum of exp(x - largest)
 };
-size_t beam_select_ws(int64_t rows, int32_t slices, int32_t n_out, size_t* best_off, size_t* sums_off);
+size_t beam_select_ws(int64_t rows, int32_t segments, int32_t n_out, size_t* best_off, size_t* sums_off);
 kvsel_status launch_beam_select(const SelectArgs& a, int32_t dtype, cudaStream_t s);
 
 // ---- beam_reorder.cu ---------------------------------------------------------------------

@@ -152,7 +152,7 @@ __device__ bool groups_ok(const RowsArgs& a) {
   return __syncthreads_and(ok) != 0;
 }
 
-// Of every group (a CTA each, from the second on): its requests' tables behind the shared pages, and their rows left.
+// Of the requests (dealt to the CTAs from the second on): their tables behind the shared pages, and their rows left.
 // The first CTA makes the items: the rows of every group's requests, 256 at a time, over the shared rows.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constant__ RowsArgs a) {
   extern __shared__ int32_t first[];          // [groups + 1] items before each group, then [groups] its shared rows
@@ -162,16 +162,21 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
   let_later_kernels_start();
   const bool ok = groups_ok(a);
   if (blockIdx.x > 0) {
-    for (int j = blockIdx.x - 1; j < (ok ? a.jobs : 1); j += gridDim.x - 1) {
-      const int64_t r0 = ok ? a.first[j] : 0, r1 = ok ? a.first[j + 1] : a.batch;
-      const int skip = ok ? shared_pages(a, r0, r1, a.shared[j]) : 0;
-      for (int64_t r = r0; r < r1; ++r) {
-        const int64_t len = a.lens[r], left = len - (int64_t)skip * a.P;
-        if (threadIdx.x == 0) a.own_lens[r] = left;
-        const int n = left > 0 && len <= (int64_t)a.max_blocks * a.P ? (int)((left + a.P - 1) / a.P) : 0;
-        for (int c = threadIdx.x; c < n; c += kPlanThreads)
-          a.own_tables[r * a.max_blocks + c] = a.tables[r * a.max_blocks + skip + c];
+    for (int r = blockIdx.x - 1; r < a.batch; r += gridDim.x - 1) {
+      int skip = 0;
+      if (ok) {
+        int lo = 0, hi = a.jobs;              // the group with first[lo] <= r < first[lo + 1]: the last that begins there or before
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (a.first[mid] <= r) lo = mid; else hi = mid;
+        }
+        skip = shared_pages(a, a.first[lo], a.first[lo + 1], a.shared[lo]);
       }
+      const int64_t len = a.lens[r], left = len - (int64_t)skip * a.P;
+      if (threadIdx.x == 0) a.own_lens[r] = left;
+      const int n = left > 0 && len <= (int64_t)a.max_blocks * a.P ? (int)((left + a.P - 1) / a.P) : 0;
+      for (int c = threadIdx.x; c < n; c += kPlanThreads)
+        a.own_tables[(int64_t)r * a.max_blocks + c] = a.tables[(int64_t)r * a.max_blocks + skip + c];
     }
     return;
   }
@@ -236,9 +241,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
 
 // o of an item's rows from its pieces, sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, and with a prefix from what the decode
 // kernel made of the requests' own rows (normalised: a sum of one at the offset lse).
-// A CTA takes 32 values of each row of an item, a thread per row; neighbouring rows' values lie next to one another.
+// A CTA takes 8 values of each row of an item, a thread per row, so that neighbouring rows' values lie next to one another; of
+// few rows the threads share out the pieces.  Four pieces' loads are in flight at once: latency is what this costs.
 // Chunk: blockIdx.x is a cut between two CTAs' shares, and the first cut of an item speaks for it.  Prefix: a (KV head, item).
-constexpr int kJoinValues = 32;
+constexpr int kJoinValues = 8, kJoinLoads = 4;
 __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ RowsArgs a) {
   wait_for_earlier_kernels();
   let_later_kernels_start();
@@ -265,62 +271,78 @@ __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ R
     first = lane_of64(x, W, N);
     last = lane_of64(x + it.steps - 1, W, N);
   }
-  const int i = threadIdx.x, c0 = blockIdx.y * kJoinValues;
-  if (i >= it.rows) return;
+  const int rows_p = it.rows > 128 ? 256 : it.rows > 64 ? 128 : it.rows > 32 ? 64 : 32;
+  const int i = threadIdx.x & (rows_p - 1), share = threadIdx.x / rows_p, shares = kItemRows / rows_p, c0 = blockIdx.y * kJoinValues;
+  const bool live = i < it.rows;
   const int r = it.row0 + i, tok = r / a.G, h = g * a.G + (r - tok * a.G);
   const int64_t out = ((int64_t)it.token0 + tok) * a.h_q + h;
+  float own_lse = -INFINITY;
+  float4 own_y[kJoinValues / 4] = {};
+  if (a.prefix && live && share == 0) {
+    own_lse = a.own_lse[out];
+#pragma unroll
+    for (int e = 0; e < kJoinValues / 4; ++e) own_y[e] = reinterpret_cast<const float4*>(a.own_o + out * a.d + c0)[e];
+  }
   float M = -INFINITY, den = 0.f, num[kJoinValues];
 #pragma unroll
   for (int e = 0; e < kJoinValues; ++e) num[e] = 0.f;
-  const float vsc = (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / a.unit;
-  for (int c = first; c <= last; ++c) {
-    const int64_t row = rows_part(a, c, c == first, g, it);
-    const float2 ml = a.part_ml[row + i];
-    const float4* from = reinterpret_cast<const float4*>(a.part + row * a.d) + (int64_t)(c0 / 4) * it.rows + i;
-    float4 y[kJoinValues / 4];
-#pragma unroll
-    for (int e = 0; e < kJoinValues / 4; ++e) y[e] = from[(int64_t)e * it.rows];
-    const float top = fmaxf(M, ml.x);                     // (a piece whose scores were all NaN, or none, has offset -inf)
-    const float wo = M == top ? 1.f : exp2f(M - top), wn = ml.x == top ? 1.f : exp2f(ml.x - top);
+  // (offset, sum, values) taken in; a piece whose scores were all NaN, or none, has offset -inf
+  auto take = [&](float m, float l, const float* y) {
+    const float top = fmaxf(M, m);
+    const float wo = M == top ? 1.f : exp2f(M - top), wn = m == top ? 1.f : exp2f(m - top);
     M = top;
-    den = den * wo + ml.y * wn;
+    den = den * wo + l * wn;
 #pragma unroll
-    for (int e = 0; e < kJoinValues; ++e) num[e] = num[e] * wo + reinterpret_cast<const float*>(y)[e] * wn;
-  }
-  float own = 0.f, inv;
-  const float4* own_row = nullptr;
-  if (a.prefix) {
-    const float own_lse = a.own_lse[out];
-    own_row = reinterpret_cast<const float4*>(a.own_o + out * a.d + c0);
-    if (own_lse == -INFINITY) {
-      own_row = nullptr;
-    } else {
-      const float z = own_lse * kLog2e, top = fmaxf(M, z);
-      const float wo = M == top ? 1.f : exp2f(M - top);
-      own = z == top ? 1.f : exp2f(z - top);
-      if (z != z) own = z;
-      M = top;
-      den = den * wo + own;
+    for (int e = 0; e < kJoinValues; ++e) num[e] = num[e] * wo + y[e] * wn;
+  };
+  for (int c = first + share; c <= last && live; c += kJoinLoads * shares) {
+    float2 ml[kJoinLoads];
+    float4 y[kJoinLoads][kJoinValues / 4];
 #pragma unroll
-      for (int e = 0; e < kJoinValues; ++e) num[e] *= wo;
-    }
+    for (int k = 0; k < kJoinLoads; ++k)
+      if (c + k * shares <= last) {
+        const int64_t row = rows_part(a, c + k * shares, c + k * shares == first, g, it);
+        const float4* from = reinterpret_cast<const float4*>(a.part + row * a.d) + (int64_t)(c0 / 4) * it.rows + i;
+        ml[k] = a.part_ml[row + i];
+#pragma unroll
+        for (int e = 0; e < kJoinValues / 4; ++e) y[k][e] = from[(int64_t)e * it.rows];
+      }
+#pragma unroll
+    for (int k = 0; k < kJoinLoads; ++k)
+      if (c + k * shares <= last) take(ml[k].x, ml[k].y, reinterpret_cast<const float*>(y[k]));
   }
-  inv = den == 0.f ? 0.f : 1.f / den;
+  __shared__ float red[kItemRows][kJoinValues + 3];
+  if (shares > 1) {
+    float* to = red[threadIdx.x];
+    to[0] = M;
+    to[1] = den;
+#pragma unroll
+    for (int e = 0; e < kJoinValues; ++e) to[2 + e] = num[e];
+    __syncthreads();
+    if (share != 0 || !live) return;
+    for (int k = 1; k < shares; ++k) take(red[k * rows_p + i][0], red[k * rows_p + i][1], red[k * rows_p + i] + 2);
+  }
+  if (!live) return;
+  const float vsc = (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / a.unit;
+  float own = 0.f;
+  if (own_lse != -INFINITY) {
+    const float z = own_lse * kLog2e, top = fmaxf(M, z);
+    const float wo = M == top ? 1.f : exp2f(M - top);
+    own = z == top ? 1.f : exp2f(z - top);    // (of a NaN, NaN)
+    M = top;
+    den = den * wo + own;
+#pragma unroll
+    for (int e = 0; e < kJoinValues; ++e) num[e] *= wo;
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const float* u = reinterpret_cast<const float*>(own_y);
+  float f[kJoinValues];
+#pragma unroll
+  for (int e = 0; e < kJoinValues; ++e) f[e] = (num[e] * vsc + (own != 0.f ? own * u[e] : 0.f)) * inv;
   uint32_t b[kJoinValues / 2];
 #pragma unroll
-  for (int e = 0; e < kJoinValues / 4; ++e) {
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (own_row != nullptr) y = own_row[e];
-    const float* u = reinterpret_cast<const float*>(&y);
-    float f[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = (num[4 * e + k] * vsc + (own_row != nullptr ? own * u[k] : 0.f)) * inv;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) b[2 * e + k] = a.out_f16 ? pack16<kF16>(f[2 * k], f[2 * k + 1]) : pack16<kBf16>(f[2 * k], f[2 * k + 1]);
-  }
-  uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * a.d + c0);
-#pragma unroll
-  for (int e = 0; e < kJoinValues / 8; ++e) to[e] = make_uint4(b[4 * e], b[4 * e + 1], b[4 * e + 2], b[4 * e + 3]);
+  for (int e = 0; e < kJoinValues / 2; ++e) b[e] = a.out_f16 ? pack16<kF16>(f[2 * e], f[2 * e + 1]) : pack16<kBf16>(f[2 * e], f[2 * e + 1]);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * a.d + c0) = make_uint4(b[0], b[1], b[2], b[3]);
   if (a.lse != nullptr && c0 == 0) a.lse[out] = (M + log2f(den) - a.shift) * 0.6931471805599453f;
 }
 
@@ -493,7 +515,7 @@ kvsel_status launch_prefix_attend(const RowsShape& p, const PagedShape& own, con
   kvsel_status st;
   {
     TraceScope ts("prefix_plan", s);
-    if ((st = launch_after(prefix_plan, dim3(1 + std::min(a.jobs, 2 * a.grid)), kPlanThreads, smem, s, a)) != KVSEL_OK) return st;
+    if ((st = launch_after(prefix_plan, dim3(1 + std::min(a.batch, 2 * a.grid)), kPlanThreads, smem, s, a)) != KVSEL_OK) return st;
   }
   {
     TraceScope ts("rows_attend", s);

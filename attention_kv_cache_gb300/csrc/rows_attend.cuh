@@ -31,6 +31,8 @@
 // do see it by hand.
 #pragma once
 
+#include <type_traits>
+
 #include "paged_attend.cuh"
 #include "rows.cuh"
 
@@ -392,12 +394,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
   uint32_t *seen_w = misc + 16, *bad_w = misc + 48;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  wait_for_earlier_kernels();
-  let_later_kernels_start();
+  // (what needs nothing of the earlier kernels, while they run)
   const int cta = blockIdx.x;
-  const RowsStart& start = a.starts[cta];
-  if (start.steps <= 0) return;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(i), 4);                        // one arrival per loader warp
@@ -420,6 +418,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
+  wait_for_earlier_kernels();
+  let_later_kernels_start();
+  const RowsStart& start = a.starts[cta];         // (a CTA without steps walks none)
 
   // registers: 512 x 128 at the launch; the rows' threads hold 128 scores
   constexpr int kRegRows = KIND == kE4m3 ? 168 : 184, kRegLoad = KIND == kE4m3 ? 112 : 80, kRegMma = 64;
@@ -966,56 +967,63 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
         float* buf = reinterpret_cast<float*>(sbase);
         float2* ml = reinterpret_cast<float2*>(buf + 8 * COLS * 32);
         ml[warp * 32 + lane] = make_float2(m, l);
-        const int parts = small ? 8 : 2, first = small ? 0 : quarter, step = small ? 1 : 4;     // parts of a row: warps first + k step
-        const int own = COLS / parts, c0 = (small ? warp : x) * own;                            // columns of a warp
-        float f[8];
+        auto merge = [&](auto parts_c) {
+          constexpr int PARTS = decltype(parts_c)::value, OWN = COLS / PARTS;      // parts of a row, columns of a warp
+          const int first = PARTS == 8 ? 0 : quarter, c0 = (PARTS == 8 ? warp : x) * OWN;        // warps first + k * (8 / PARTS)
+          float f[PARTS];
 #pragma unroll 1
-        for (int q = 0; q < 4 && ok; ++q) {
-          float* b = buf + (q & 1) * 8 * COLS * 32;
-          float y[COLS];
-          __syncwarp();
-          if (had && !idle) {
-            if constexpr (COLS == 32) tmem_ld32(tm + kOCol + q * COLS, y);
-            else tmem_ld16(tm + kOCol + q * COLS, y);
-          } else {
+          for (int q = 0; q < 4; ++q) {
+            float* b = buf + (q & 1) * 8 * COLS * 32;
+            float y[COLS];
+            __syncwarp();
+            if (had && !idle) {
+              if constexpr (COLS == 32) tmem_ld32(tm + kOCol + q * COLS, y);
+              else tmem_ld16(tm + kOCol + q * COLS, y);
+            } else {
 #pragma unroll
-            for (int e = 0; e < COLS; ++e) y[e] = 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < COLS; ++e) b[(warp * COLS + e) * 32 + lane] = y[e];
-          if (!(ok = meet())) break;
-          if (q == 0) {
-            float M = -INFINITY, L = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) M = fmaxf(M, k < parts ? ml[(first + step * k) * 32 + lane].x : -INFINITY);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 z = k < parts ? ml[(first + step * k) * 32 + lane] : make_float2(-INFINITY, 0.f);
-              f[k] = z.x == M ? 1.f : exp2f(z.x - M);
-              if (k < parts) L += z.y * f[k];
+              for (int e = 0; e < COLS; ++e) y[e] = 0.f;
             }
-            if (!(ok = meet())) break;              // (the second buffer is read)
-            m = M;
-            l = L;
-            const float g = factor(L);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] *= g;
-          }
-#pragma unroll 1
-          for (int e = c0; e < c0 + own; e += 2) {
-            float u = 0.f, v = 0.f;
+            for (int e = 0; e < COLS; ++e) b[(warp * COLS + e) * 32 + lane] = y[e];
+            if (!(ok = meet())) return;
+            if (q == 0) {
+              float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k < parts) {
-                u = fmaf(b[((first + step * k) * COLS + e) * 32 + lane], f[k], u);
-                v = fmaf(b[((first + step * k) * COLS + e + 1) * 32 + lane], f[k], v);
+              for (int k = 0; k < PARTS; ++k) M = fmaxf(M, ml[(first + 8 / PARTS * k) * 32 + lane].x);
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) {
+                const float2 z = ml[(first + 8 / PARTS * k) * 32 + lane];
+                f[k] = z.x == M ? 1.f : exp2f(z.x - M);
+                L += z.y * f[k];
               }
-            const int col = q * COLS + e;
-            if (live && final) static_cast<uint32_t*>(a.o)[(out * D + col) / 2] = pack(u, v);
-            else if (live) *reinterpret_cast<float2*>(a.part + prow * D + ((int64_t)(col / 4) * rows + i) * 4 + (col & 2)) = make_float2(u, v);
+              if (!(ok = meet())) return;           // (the second buffer is read)
+              m = M;
+              l = L;
+              const float g = factor(L);
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) f[k] *= g;
+            }
+            float r[OWN];
+#pragma unroll
+            for (int e = 0; e < OWN; ++e) {
+              r[e] = 0.f;
+#pragma unroll
+              for (int k = 0; k < PARTS; ++k) r[e] = fmaf(b[((first + 8 / PARTS * k) * COLS + c0 + e) * 32 + lane], f[k], r[e]);
+            }
+            const int col = q * COLS + c0;
+            if (live && final) {
+#pragma unroll
+              for (int e = 0; e < OWN; e += 2) static_cast<uint32_t*>(a.o)[(out * D + col + e) / 2] = pack(r[e], r[e + 1]);
+            } else if (live) {
+#pragma unroll
+              for (int e = 0; e < OWN; e += 2)
+                *reinterpret_cast<float2*>(a.part + prow * D + ((int64_t)((col + e) / 4) * rows + i) * 4 + ((col + e) & 2)) = make_float2(r[e], r[e + 1]);
+            }
           }
-        }
-        if (ok) ok = meet();                        // the buffers are read
+          ok = meet();                              // the buffers are read
+        };
+        if (small) merge(std::integral_constant<int, 8>{});
+        else merge(std::integral_constant<int, 2>{});
         if (!ok) break;
       }
       // the next piece's queries, then what is left of this one's result
