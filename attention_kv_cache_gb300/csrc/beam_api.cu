@@ -22,7 +22,7 @@ kvsel_status check_select(const kvsel_beam_select_desc* p, SelectArgs* out) {
   a.vocab = p->vocab;
   // Segments: slices of their own while there are few rows; of many rows so that the CTAs are some 4096 (each begins a bound and
   // leaves a list: 64 sets of 16 beams over 128256 tokens take 245 us in slices of their own, SELECT_US in four segments).
-  const int64_t rows = (int64_t)p->batch * p->beams, most = std::max<int64_t>(1, 4096 / rows);
+  const int64_t rows = (int64_t)p->batch * p->beams, most = std::max<int64_t>(1, kSelectCtas / rows);
   a.seg_slices = (int32_t)ceil_div(slices, std::min(slices, most));
   a.segments = (int32_t)ceil_div(slices, a.seg_slices);
   a.pad_token = p->pad_token;

@@ -53,34 +53,129 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-// Largest of a thread's values, NaN passed over; -0 as 0.
+// A thread's kEach tokens of a slice, as they lie: kEach * sizeof(T) / 4 words.  Vector v of 16 bytes holds the tokens from
+// place V * (v * kThreads + tid) of the slice on, whatever the row's alignment: rows that lie equal are summed alike.
 template <typename T>
-__device__ __forceinline__ float thread_max(const T* v) {
-  if constexpr (sizeof(T) == 4) {
-    float m = v[0];
+struct Tokens {
+  static constexpr int V = 16 / (int)sizeof(T), WORDS = kEach * (int)sizeof(T) / 4;
+  uint32_t w[WORDS];
+  static __device__ __forceinline__ int place(int tid, int i) { return (i / V * kThreads + tid) * V + i % V; }
+
+  // x: the slice's first token; tokens from n on are -inf.
+  __device__ __forceinline__ void load(const T* x, int n, int tid) {
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15);
+    if (n == kSliceKeys) {
+      if (off == 0) {
 #pragma unroll
-    for (int i = 1; i < kEach; ++i) m = fmaxf(m, v[i]);
-    return (m == m ? m : -INFINITY) + 0.f;
-  } else {
-    using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-    const P* p = reinterpret_cast<const P*>(v);
-    P m = p[0];
+        for (int v = 0; v < WORDS / 4; ++v)
+          *reinterpret_cast<uint4*>(w + 4 * v) = __ldcs(reinterpret_cast<const uint4*>(x) + v * kThreads + tid);
+      } else {
+        // Two aligned vectors and a shift by the row's offset.  (The words before the first token, and behind the last, are of
+        // vectors that hold tokens.)
+        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) - off);
 #pragma unroll
-    for (int i = 1; i < kEach / 2; ++i) m = __hmax2(m, p[i]);
-    const float r = fmaxf(to_float(T(m.x)), to_float(T(m.y)));
+        for (int v = 0; v < WORDS / 4; ++v) {
+          const uint4 a = __ldg(from + v * kThreads + tid), b = __ldg(from + v * kThreads + tid + 1);
+          uint32_t y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          if (off & 8) {
+#pragma unroll
+            for (int k = 0; k < 6; ++k) y[k] = y[k + 2];
+          }
+          if (off & 4) {
+#pragma unroll
+            for (int k = 0; k < 5; ++k) y[k] = y[k + 1];
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[4 * v + k] = sizeof(T) == 2 ? __funnelshift_r(y[k], y[k + 1], (off & 2) * 8) : y[k];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          const int p = place(tid, i);
+          w[i] = p < n ? __float_as_uint(x[p]) : 0xff800000u;
+        } else {
+          const int p = place(tid, 2 * i);
+          T u = p < n ? x[p] : T(-INFINITY), v = p + 1 < n ? x[p + 1] : T(-INFINITY);
+          w[i] = (uint32_t)*reinterpret_cast<uint16_t*>(&u) | (uint32_t)*reinterpret_cast<uint16_t*>(&v) << 16;
+        }
+      }
+    }
+  }
+  // tokens 2 i and 2 i + 1
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  // The largest, NaN passed over; -0 as 0.
+  __device__ __forceinline__ float largest() const {
+    float r;
+    if constexpr (sizeof(T) == 4) {
+      r = __uint_as_float(w[0]);
+#pragma unroll
+      for (int i = 1; i < WORDS; ++i) r = fmaxf(r, __uint_as_float(w[i]));
+    } else {
+      using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      P m = *reinterpret_cast<const P*>(&w[0]);
+#pragma unroll
+      for (int i = 1; i < WORDS; ++i) m = __hmax2(m, *reinterpret_cast<const P*>(&w[i]));
+      r = fmaxf(to_float(T(m.x)), to_float(T(m.y)));
+    }
     return (r == r ? r : -INFINITY) + 0.f;
   }
-}
+  // sum of exp(x - top), a NaN as none
+  __device__ __forceinline__ float exp_sum(float top) const {
+    const float2 t2 = make_float2(-top, -top), l2 = make_float2(kLog2e, kLog2e);
+    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < kEach / 2; ++i) {
+      const float2 z = __fmul2_rn(__fadd2_rn(pair(i), t2), l2);
+      part[i & 1] = __fadd2_rn(part[i & 1], make_float2(ex2f(z.x), ex2f(z.y)));
+    }
+    const float2 s = __fadd2_rn(part[0], part[1]);
+    float sum = s.x + s.y;
+    if (sum != sum) {                         // (a NaN among them: once more without it)
+      sum = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i) {
+          const float y = k ? pair(i).y : pair(i).x;
+          sum += y == y ? ex2f((y - top) * kLog2e) : 0.f;
+        }
+    }
+    return sum;
+  }
+  // The tokens above `least` (one of the logits, or -inf), or equal to it and not -inf where `equal` ones count: bit i for
+  // token i, or in pairs bit i for token 2 i and bit 16 + i for token 2 i + 1.
+  static __device__ __forceinline__ int token_of(int bit) { return sizeof(T) == 4 ? bit : 2 * (bit & 15) + (bit >> 4); }
+  __device__ __forceinline__ uint32_t above(float least, bool equal) const {
+    uint32_t r = 0;
+    const bool ge = equal && least != -INFINITY;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const float y = __uint_as_float(w[i]);
+        r |= ((ge ? y >= least : y > least) ? 1u : 0u) << i;
+      }
+    } else {
+      using P = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      const P b = P(T(least), T(least));
+      if (ge) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r |= __hge2_mask(*reinterpret_cast<const P*>(&w[i]), b) & (0x00010001u << i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r |= __hgt2_mask(*reinterpret_cast<const P*>(&w[i]), b) & (0x00010001u << i);
+      }
+    }
+    return r;
+  }
+};
 
-// Element i of a thread's kEach is token `first + place(tid, i)` of its slice; places rise with i.  Vectors of 16 bytes where
-// all rows are aligned to them, else single elements, neighbours on neighbouring threads.
-template <typename T, bool VEC>
-__device__ __forceinline__ int place(int tid, int i) {
-  constexpr int V = 16 / (int)sizeof(T);
-  return VEC ? (i / V * kThreads + tid) * V + i % V : i * kThreads + tid;
-}
-
-template <typename T, bool VEC, int KEYS>
+template <typename T, int KEYS>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(const __grid_constant__ SelectArgs a) {
   __shared__ uint32_t group_key[32 * KEYS];
   __shared__ float warp_max[kThreads / 32];
@@ -95,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
   wait_for_earlier_kernels();
   let_later_kernels_start();                  // (the merge: it waits for this grid's end)
   const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-  constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
   const int n = a.n_out;
   if (tid == 0) n_cand = 0;
   auto key_of = [&](float y, int p) { return (uint64_t)ordered(no_nan(y)) << 32 | (0xffffffffu - (uint32_t)p); };
@@ -108,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
     for (int c = tid; c < c_all; c += kThreads) {
       const uint64_t k = cand[c];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < c_all; ++j) rank += cand[j] > k;
       if (rank < n) kept[rank] = k;
     }
@@ -121,21 +216,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
     __syncthreads();
   };
   float mine_m = -INFINITY, mine_s = 0.f;     // this thread's largest logit and sum of exponentials
+#pragma unroll 1
   for (int first = s0; first < s1; first += kSliceKeys) {
     const int n_here = min(kSliceKeys, s1 - first);
-    alignas(16) T val[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; i += V) {
-      const int p = place<T, VEC>(tid, i);
-      if (p + V <= n_here) {
-        if constexpr (VEC) *reinterpret_cast<uint4*>(&val[i]) = __ldcs(reinterpret_cast<const uint4*>(x + first + p));
-        else val[i] = x[first + p];
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) val[i + e] = p + e < n_here ? x[first + p + e] : T(-INFINITY);
-      }
-    }
-    const float mine = thread_max(val);       // (passes over NaN)
+    Tokens<T> val;
+    val.load(x + first, n_here, tid);
+    const float mine = val.largest();
     if (first == s0) {
       // group maxima: 8 KEYS lanes of a warp's 32 leave a key each; the n-th largest is the first bound
       float grp = mine;
@@ -151,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
         uint32_t key[KEYS], found = 0;
 #pragma unroll
         for (int k = 0; k < KEYS; ++k) key[k] = group_key[lane + 32 * k];
-        // (16-bit logits differ in the top 16 bits, bf16, or the top 19)
+        // (16-bit logits differ in the top 16 bits, bf16, or the top 19; the others are all ones in a negative one's key)
         constexpr int last = sizeof(T) == 4 ? 0 : std::is_same<T, __half>::value ? 13 : 16;
         for (int bit = 31; bit >= last; --bit) {
           const uint32_t probe = found | (1u << bit);
@@ -160,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
           for (int k = 0; k < KEYS; ++k) c += __popc(__ballot_sync(0xffffffffu, key[k] >= probe));
           if (c >= n) found = probe;
         }
+        if ((found >> 31) == 0) found |= (1u << last) - 1u;
         if (lane == 0) edge = found;
       }
     }
@@ -167,13 +254,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
     const float top = fmaxf(mine_m, mine);
     if (isfinite(top)) {
       if (top > mine_m) mine_s *= ex2f((mine_m - top) * kLog2e);
-      float part[2] = {0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const float y = to_float(val[i]);
-        part[i & 1] += y == y ? ex2f((y - top) * kLog2e) : 0.f;
-      }
-      mine_s += part[0] + part[1];
+      mine_s += val.exp_sum(top);
     }
     mine_m = top;
     if (first == s0) __syncthreads();
@@ -181,17 +262,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
     // behind n); never -inf
     const int before = n_cand;
     const float least = first == s0 ? unordered(edge) : bound;
-    const bool strict = first != s0;
     __syncthreads();                          // (`before` is read)
     if (mine >= least && mine != -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const float y = to_float(val[i]);
-        const int p = place<T, VEC>(tid, i);
-        if ((strict ? y > least : y >= least) && y != -INFINITY && p < n_here) {
-          const int c = atomicAdd(&n_cand, 1);
-          if (c < kCandidates) cand[c] = key_of(y, first + p);
-        }
+      uint32_t hits = val.above(least, first == s0);
+      while (hits != 0) {
+        const int p = first + Tokens<T>::place(tid, Tokens<T>::token_of(__ffs((int)hits) - 1));
+        hits &= hits - 1;
+        const int c = atomicAdd(&n_cand, 1);
+        if (c < kCandidates) cand[c] = key_of(to_float(x[p]), p);           // (in L1 or L2 still)
       }
     }
     __syncthreads();
@@ -320,21 +398,22 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   }
   if (tid == 0) n_cand = n_lists = 0;
   __syncthreads();
-  for (int l = tid; l < lists; l += kMergeThreads) {
-    const int k = l / a.segments;
+  // The n-th largest of the lists' first entries (of as many as make 2 n, where there are few lists), by its upper half, which is
+  // enough unless more lists than there is room for reach it; then by all of it, and of the lists equal to it those
+  // before the place `upto`.
+  const int n = a.n_out, depth = lists > n ? 1 : min(n, (2 * n + lists - 1) / lists), values = lists * depth;
+  for (int v = tid; v < values; v += kMergeThreads) {
+    const int l = v / depth, k = l / a.segments;
     double z;
-    head[l] = entry(a, beam[k], row0 + k, l - k * a.segments, 0, z) >= 0 ? ordered(z) : 0ull;   // (a real key is not 0)
+    head[v] = entry(a, beam[k], row0 + k, l - k * a.segments, v - l * depth, z) >= 0 ? ordered(z) : 0ull;   // (a real key is not 0)
   }
   __syncthreads();
-  // The n-th largest head: by its upper half, which is enough unless more than there is room for are equal to it there; then by
-  // all of it, and of the lists equal to it those before the place `upto`.
-  const int n = a.n_out;
   auto count = [&](auto test) {
     int c = 0;
-    if (lists <= kMergeThreads) return (int)__syncthreads_count(tid < lists && test(head[tid], tid));
+    if (values <= kMergeThreads) return (int)__syncthreads_count(tid < values && test(head[tid], tid));
     if (tid == 0) total = 0;
     __syncthreads();
-    for (int l = tid; l < lists; l += kMergeThreads) c += test(head[l], l) ? 1 : 0;
+    for (int v = tid; v < values; v += kMergeThreads) c += test(head[v], v) ? 1 : 0;
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0 && c != 0) atomicAdd(&total, c);
     __syncthreads();
@@ -344,11 +423,11 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   };
   uint64_t found = 0;
   int upto = lists;
-  if (lists > n) {
-    for (int bit = 63; bit >= 32; --bit) {
-      const uint64_t probe = found | (uint64_t(1) << bit);
-      if (count([&](uint64_t h, int) { return h >= probe; }) >= n) found = probe;
-    }
+  for (int bit = 63; bit >= 32; --bit) {
+    const uint64_t probe = found | (uint64_t(1) << bit);
+    if (count([&](uint64_t h, int) { return h >= probe; }) >= n) found = probe;
+  }
+  if (lists > kMaxBeamOut) {                                   // (depth 1: a value is a list)
     if (count([&](uint64_t h, int) { return h != 0 && h >= found; }) > kMaxBeamOut) {
       for (int bit = 31; bit >= 0; --bit) {
         const uint64_t probe = found | (uint64_t(1) << bit);
@@ -362,8 +441,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
       }
     }
   }
-  for (int l = tid; l < lists; l += kMergeThreads)
-    if (head[l] > found || (head[l] == found && head[l] != 0 && l < upto)) chosen[atomicAdd(&n_lists, 1)] = (int16_t)l;
+  for (int l = tid; l < lists; l += kMergeThreads) {
+    const uint64_t h = head[l * depth];
+    if (h > found || (h == found && h != 0 && l < upto)) chosen[atomicAdd(&n_lists, 1)] = (int16_t)l;
+  }
   __syncthreads();
   // what those lists hold at or above it, a warp each
   for (int i = warp; i < n_lists; i += kMergeThreads / 32) {
@@ -401,13 +482,13 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   }
 }
 
-template <typename T, bool VEC>
+template <typename T>
 kvsel_status launch_slices(const SelectArgs& a, cudaStream_t s) {
   const int64_t grid = (int64_t)a.batch * a.beams * a.segments;
   TraceScope ts("beam_slice", s);
   // 64 groups of four threads hold the n-th maximum near the n-th logit up to n = 32; beyond, every thread is a group
-  if (a.n_out <= 32) return launch_after(beam_slice<T, VEC, 2>, dim3((unsigned)grid), kThreads, 0, s, a);
-  return launch_after(beam_slice<T, VEC, 8>, dim3((unsigned)grid), kThreads, 0, s, a);
+  if (a.n_out <= 32) return launch_after(beam_slice<T, 2>, dim3((unsigned)grid), kThreads, 0, s, a);
+  return launch_after(beam_slice<T, 8>, dim3((unsigned)grid), kThreads, 0, s, a);
 }
 
 }  // namespace
@@ -420,14 +501,11 @@ size_t beam_select_ws(int64_t rows, int32_t segments, int32_t n_out, size_t* bes
 }
 
 kvsel_status launch_beam_select(const SelectArgs& a, int32_t dtype, cudaStream_t s) {
-  const size_t size = dtype == KVSEL_DTYPE_F32 ? 4 : 2;
-  const bool vec = ((uintptr_t)a.logits & 15) == 0 && a.row_stride * size % 16 == 0;
-  kvsel_status st;
-  if (dtype == KVSEL_DTYPE_BF16) st = vec ? launch_slices<__nv_bfloat16, true>(a, s) : launch_slices<__nv_bfloat16, false>(a, s);
-  else if (dtype == KVSEL_DTYPE_F16) st = vec ? launch_slices<__half, true>(a, s) : launch_slices<__half, false>(a, s);
-  else st = vec ? launch_slices<float, true>(a, s) : launch_slices<float, false>(a, s);
+  const kvsel_status st = dtype == KVSEL_DTYPE_BF16  ? launch_slices<__nv_bfloat16>(a, s)
+                          : dtype == KVSEL_DTYPE_F16 ? launch_slices<__half>(a, s)
+                                                     : launch_slices<float>(a, s);
   if (st != KVSEL_OK) return st;
-  const size_t smem = (size_t)kMaxBeamOut * kMaxBeamOut * 16 + sizeof(uint64_t) * (size_t)a.beams * a.segments;
+  const size_t smem = (size_t)kMaxBeamOut * kMaxBeamOut * 16 + sizeof(uint64_t) * (size_t)std::max<int64_t>((int64_t)a.beams * a.segments, 4 * kMaxBeamOut);
   if (set_smem((const void*)beam_merge, smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   TraceScope ts("beam_merge", s);
   return launch_after(beam_merge, dim3((unsigned)a.batch), kMergeThreads, smem, s, a);

@@ -241,10 +241,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
 
 // o of an item's rows from its pieces, sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, and with a prefix from what the decode
 // kernel made of the requests' own rows (normalised: a sum of one at the offset lse).
-// A CTA takes 8 values of each row of an item, a thread per row, so that neighbouring rows' values lie next to one another; of
-// few rows the threads share out the pieces.  Four pieces' loads are in flight at once: latency is what this costs.
-// Chunk: blockIdx.x is a cut between two CTAs' shares, and the first cut of an item speaks for it.  Prefix: a (KV head, item).
-constexpr int kJoinValues = 8, kJoinLoads = 4;
+// A CTA takes 8 (32) values of each row of an item, a thread per row, so that neighbouring rows' values lie next to one another; of
+// few rows the threads share out the pieces.  Four (two) pieces' loads are in flight at once: latency is what this costs.
+// Prefix, many pieces and few items: blockIdx.x is a (KV head, item).  Chunk, two pieces or a few more: blockIdx.x is a cut
+// between two CTAs' shares, and the first cut of an item speaks for it.
+template <int kJoinValues, int kJoinLoads>
 __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ RowsArgs a) {
   wait_for_earlier_kernels();
   let_later_kernels_start();
@@ -339,10 +340,12 @@ __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ R
   float f[kJoinValues];
 #pragma unroll
   for (int e = 0; e < kJoinValues; ++e) f[e] = (num[e] * vsc + (own != 0.f ? own * u[e] : 0.f)) * inv;
-  uint32_t b[kJoinValues / 2];
+  alignas(16) uint32_t b[kJoinValues / 2];
 #pragma unroll
   for (int e = 0; e < kJoinValues / 2; ++e) b[e] = a.out_f16 ? pack16<kF16>(f[2 * e], f[2 * e + 1]) : pack16<kBf16>(f[2 * e], f[2 * e + 1]);
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * a.d + c0) = make_uint4(b[0], b[1], b[2], b[3]);
+  uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * a.d + c0);
+#pragma unroll
+  for (int e = 0; e < kJoinValues / 8; ++e) to[e] = *reinterpret_cast<const uint4*>(b + 4 * e);
   if (a.lse != nullptr && c0 == 0) a.lse[out] = (M + log2f(den) - a.shift) * 0.6931471805599453f;
 }
 
@@ -500,7 +503,7 @@ kvsel_status launch_chunk_attend(const RowsShape& p, const RowsArgs& in, void* w
     if ((st = launch_after(var.kern, dim3(a.grid), kRowsThreads, var.smem, s, a, tk, tv)) != KVSEL_OK) return st;
   }
   TraceScope ts("rows_join", s);
-  return launch_after(rows_join, dim3(std::max(1, a.grid - 1), p.d / kJoinValues), kItemRows, 0, s, a);
+  return launch_after(rows_join<32, 2>, dim3(std::max(1, a.grid - 1), p.d / 32), kItemRows, 0, s, a);
 }
 
 kvsel_status launch_prefix_attend(const RowsShape& p, const PagedShape& own, const RowsArgs& in, void* ws, size_t front, cudaStream_t s) {
@@ -525,7 +528,7 @@ kvsel_status launch_prefix_attend(const RowsShape& p, const PagedShape& own, con
                            const_cast<float*>(a.own_o));
   if (st != KVSEL_OK) return st;
   TraceScope ts("rows_join", s);
-  return launch_after(rows_join, dim3((unsigned)(lay.max_items * a.h_kv), p.d / kJoinValues), kItemRows, 0, s, a);
+  return launch_after(rows_join<8, 4>, dim3((unsigned)(lay.max_items * a.h_kv), p.d / 8), kItemRows, 0, s, a);
 }
 
 }  // namespace kvsel
