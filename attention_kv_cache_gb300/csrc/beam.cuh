@@ -6,7 +6,7 @@
 namespace kvsel {
 
 constexpr int kSliceKeys = 8192;      // tokens of one row that a CTA takes at a time
-constexpr int64_t kSelectCtas = 4096; // segments of all rows, about
+constexpr int64_t kSelectCtas = 2048; // segments of all rows, about
 constexpr int kMaxBeams = 64, kMaxBeamOut = 64;
 constexpr int64_t kMaxLists = 8192;   // slices of a set's rows, and segments at most
 

@@ -61,6 +61,18 @@ struct Tokens {
   uint32_t w[WORDS];
   static __device__ __forceinline__ int place(int tid, int i) { return (i / V * kThreads + tid) * V + i % V; }
 
+  // Two aligned vectors and a shift by the row's offset of WORD words and `bits`.  (The words before the first token, and behind
+  // the last, are of vectors that hold tokens.)
+  template <int WORD>
+  __device__ __forceinline__ void shifted(const uint4* from, uint32_t bits) {
+#pragma unroll
+    for (int v = 0; v < WORDS / 4; ++v) {
+      const uint4 a = __ldg(from + v * kThreads), b = __ldg(from + v * kThreads + 1);
+      const uint32_t y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[4 * v + k] = sizeof(T) == 2 ? __funnelshift_r(y[WORD + k], y[WORD + k + 1], bits) : y[WORD + k];
+    }
+  }
   // x: the slice's first token; tokens from n on are -inf.
   __device__ __forceinline__ void load(const T* x, int n, int tid) {
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15);
@@ -70,24 +82,12 @@ struct Tokens {
         for (int v = 0; v < WORDS / 4; ++v)
           *reinterpret_cast<uint4*>(w + 4 * v) = __ldcs(reinterpret_cast<const uint4*>(x) + v * kThreads + tid);
       } else {
-        // Two aligned vectors and a shift by the row's offset.  (The words before the first token, and behind the last, are of
-        // vectors that hold tokens.)
-        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) - off);
-#pragma unroll
-        for (int v = 0; v < WORDS / 4; ++v) {
-          const uint4 a = __ldg(from + v * kThreads + tid), b = __ldg(from + v * kThreads + tid + 1);
-          uint32_t y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-          if (off & 8) {
-#pragma unroll
-            for (int k = 0; k < 6; ++k) y[k] = y[k + 2];
-          }
-          if (off & 4) {
-#pragma unroll
-            for (int k = 0; k < 5; ++k) y[k] = y[k + 1];
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[4 * v + k] = sizeof(T) == 2 ? __funnelshift_r(y[k], y[k + 1], (off & 2) * 8) : y[k];
-        }
+        const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) - off) + tid;
+        const uint32_t bits = (off & 2) * 8;
+        if (off < 4) shifted<0>(from, bits);
+        else if (off < 8) shifted<1>(from, bits);
+        else if (off < 12) shifted<2>(from, bits);
+        else shifted<3>(from, bits);
       }
     } else {
 #pragma unroll
@@ -125,28 +125,28 @@ struct Tokens {
     }
     return (r == r ? r : -INFINITY) + 0.f;
   }
-  // sum of exp(x - top), a NaN as none
+  // Sum of exp(x - top), a NaN as none.  With c the rounded product top log2 e and r what that leaves, exp(x - top) is
+  // 2^(x log2 e - c) 2^-r: one fused multiply-add per logit, rounded at its distance.
   __device__ __forceinline__ float exp_sum(float top) const {
-    const float2 t2 = make_float2(-top, -top), l2 = make_float2(kLog2e, kLog2e);
+    const float c = top * kLog2e, r = fmaf(top, kLog2e, -c);
+    const float2 c2 = make_float2(-c, -c), l2 = make_float2(kLog2e, kLog2e);
     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < kEach / 2; ++i) {
-      const float2 z = __fmul2_rn(__fadd2_rn(pair(i), t2), l2);
+      const float2 z = __ffma2_rn(pair(i), l2, c2);
       part[i & 1] = __fadd2_rn(part[i & 1], make_float2(ex2f(z.x), ex2f(z.y)));
     }
     const float2 s = __fadd2_rn(part[0], part[1]);
     float sum = s.x + s.y;
     if (sum != sum) {                         // (a NaN among them: once more without it)
       sum = 0.f;
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < kEach / 2; ++i) {
-          const float y = k ? pair(i).y : pair(i).x;
-          sum += y == y ? ex2f((y - top) * kLog2e) : 0.f;
-        }
+      for (int i = 0; i < kEach / 2; ++i) {
+        const float2 y = pair(i), z = __ffma2_rn(y, l2, c2);
+        sum += (y.x == y.x ? ex2f(z.x) : 0.f) + (y.y == y.y ? ex2f(z.y) : 0.f);
+      }
     }
-    return sum;
+    return sum * ex2f(-r);
   }
   // The tokens above `least` (one of the logits, or -inf), or equal to it and not -inf where `equal` ones count: bit i for
   // token i, or in pairs bit i for token 2 i and bit 16 + i for token 2 i + 1.
@@ -176,7 +176,7 @@ struct Tokens {
 };
 
 template <typename T, int KEYS>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_slice(const __grid_constant__ SelectArgs a) {
   __shared__ uint32_t group_key[32 * KEYS];
   __shared__ float warp_max[kThreads / 32];
   __shared__ uint64_t warp_sum[kThreads / 32];
@@ -336,6 +336,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) beam_slice(c
   }
 }
 
+// e^x in 64 bits for x in [-700, 1]: the Taylor series to the 12th power within half a binary order, off by at most 2^-52 of the
+// value there.  (Few fused multiply-adds in line: the merge runs once a step, and its code is fetched as it goes.)
+__device__ __forceinline__ double exp64(double x) {
+  const double k = rint(x * 1.4426950408889634074), g = fma(-k, 0.69314718055994530942, x);
+  double y = 1.0 / 479001600.0;
+  const double c[12] = {1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0,
+                        1.0 / 120.0,      1.0 / 24.0,      1.0 / 6.0,      0.5,           1.0,          1.0};
+#pragma unroll
+  for (int i = 0; i < 12; ++i) y = fma(y, g, c[i]);
+  return y * __longlong_as_double((long long)(1023 + (int)k) << 52);
+}
+// log x for x in [1, 2^40]: the 32-bit one and a step of Newton's, x e^-y - 1 further.
+__device__ __forceinline__ double log64(double x) {
+  const double y = (double)logf((float)x);
+  return y + fma(x, exp64(-y), -1.0);
+}
+
 // A beam's row for the merge: its log-sum, its score, and whether its order is that of the logits.
 struct Beam {
   double lse, score;
@@ -371,7 +388,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   constexpr int kMost = kMaxBeamOut * kMaxBeamOut;
   const int lists = a.beams * a.segments, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint64_t* key = sm;                                          // [kMost] candidates' scores
-  int2* what = reinterpret_cast<int2*>(key + kMost);           // [kMost] (list, entry)
+  int2* what = reinterpret_cast<int2*>(key + kMost);           // [kMost] (list and entry as one number, token)
   uint64_t* head = reinterpret_cast<uint64_t*>(what + kMost);  // [lists]
   const int64_t set = blockIdx.x, row0 = set * a.beams;
   wait_for_earlier_kernels();
@@ -384,12 +401,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
     for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
     for (int i = lane; i < a.segments; i += 32) {
       const double2 p = s[i];
-      if (p.y > 0.0) sum += p.y * exp(p.x - top);
+      if (p.y > 0.0 && p.x - top > -700.0) sum += p.y * exp64(p.x - top);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      const double lse = isinf(top) ? top : top + log(sum);
+      const double lse = isinf(top) ? top : top + log64(sum);
       const double score = a.scores[row0 + k];
       const bool ended = a.ended != nullptr && a.ended[row0 + k] != 0;
       beam[k] = Beam{lse, score, !isfinite(score) ? 2 : ended ? 1 : isinf(lse) ? 2 : 0};
@@ -423,9 +440,24 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   };
   uint64_t found = 0;
   int upto = lists;
-  for (int bit = 63; bit >= 32; --bit) {
-    const uint64_t probe = found | (uint64_t(1) << bit);
-    if (count([&](uint64_t h, int) { return h >= probe; }) >= n) found = probe;
+  if (values <= kMergeThreads) {
+    // few values: the one that n - 1 others precede
+    if (tid == 0) total = 0;
+    __syncthreads();
+    if (tid < values) {
+      const uint64_t h = head[tid];
+      int before = 0;
+#pragma unroll 8
+      for (int v = 0; v < values; ++v) before += (head[v] > h) | ((head[v] == h) & (v < tid));
+      if (before == n - 1) total = tid;
+    }
+    __syncthreads();
+    found = values >= n ? head[total] >> 32 << 32 : 0ull;
+  } else {
+    for (int bit = 63; bit >= 32; --bit) {
+      const uint64_t probe = found | (uint64_t(1) << bit);
+      if (count([&](uint64_t h, int) { return h >= probe; }) >= n) found = probe;
+    }
   }
   if (lists > kMaxBeamOut) {                                   // (depth 1: a value is a list)
     if (count([&](uint64_t h, int) { return h != 0 && h >= found; }) > kMaxBeamOut) {
@@ -451,10 +483,11 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
     const int l = chosen[i], k = l / a.segments;
     for (int e = lane; e < n; e += 32) {
       double z;
-      if (entry(a, beam[k], row0 + k, l - k * a.segments, e, z) < 0 || ordered(z) < found) break;
+      const int token = entry(a, beam[k], row0 + k, l - k * a.segments, e, z);
+      if (token < 0 || ordered(z) < found) break;
       const int c = atomicAdd(&n_cand, 1);
       key[c] = ordered(z);
-      what[c] = make_int2(l, e);
+      what[c] = make_int2(l * kMaxBeamOut + e, token);
     }
   }
   __syncthreads();
@@ -464,21 +497,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
     const uint64_t z = key[c];
     const int2 w = what[c];
     int rank = 0;
-    for (int j = 0; j < c_all; ++j) {
-      const uint64_t y = key[j];
-      rank += y > z;
-      if (y == z) {
-        const int2 u = what[j];
-        rank += u.x < w.x || (u.x == w.x && u.y < w.y);
-      }
-    }
+#pragma unroll 4
+    for (int j = 0; j < c_all; ++j) rank += (key[j] > z) | ((key[j] == z) & (what[j].x < w.x));
     if (rank >= n) continue;
-    const int k = w.x / a.segments;
-    double score;
-    const int token = entry(a, beam[k], row0 + k, w.x - k * a.segments, w.y, score);
-    a.scores_out[set * n + rank] = (float)score;
-    a.parents[set * n + rank] = k;
-    a.tokens[set * n + rank] = token;
+    a.scores_out[set * n + rank] = (float)__longlong_as_double((long long)(z >> 63 ? z & ~(uint64_t(1) << 63) : ~z));
+    a.parents[set * n + rank] = w.x / kMaxBeamOut / a.segments;
+    a.tokens[set * n + rank] = w.y;
   }
 }
 
