@@ -22,9 +22,10 @@ struct SelectArgs {
   int32_t *parents, *tokens;
   float* lse;
   float2* best;         // [row][segment][n_out]: a segment's best tokens, (logit, token as bits) in order; token -1: none
-  double2* sums;        // [row][segment]: largest logit, sum of exp(x - largest)
+  float* tops;          // [row][segment]: largest logit
+  uint64_t* sums;       // [row][segment]: sum of exp(x - largest), in 2^-40
 };
-size_t beam_select_ws(int64_t rows, int32_t segments, int32_t n_out, size_t* best_off, size_t* sums_off);
+size_t beam_select_ws(int64_t rows, int32_t segments, int32_t n_out, size_t* best_off, size_t* sums_off, size_t* tops_off);
 kvsel_status launch_beam_select(const SelectArgs& a, int32_t dtype, cudaStream_t s);
 
 // ---- beam_reorder.cu ---------------------------------------------------------------------

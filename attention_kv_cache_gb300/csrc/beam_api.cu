@@ -20,8 +20,8 @@ kvsel_status check_select(const kvsel_beam_select_desc* p, SelectArgs* out) {
   a.beams = p->beams;
   a.n_out = p->n_out;
   a.vocab = p->vocab;
-  // Segments: slices of their own while there are few rows; of many rows so that the CTAs are some 4096 (each begins a bound and
-  // leaves a list: 64 sets of 16 beams over 128256 tokens take 245 us in slices of their own, SELECT_US in four segments).
+  // Segments: slices of their own while there are few rows; of many rows so that the CTAs are some 2048 (each begins a bound and
+  // leaves a list: 64 sets of 16 beams over 128256 tokens take 245 us in slices of their own, 131 in four segments, 99 in two).
   const int64_t rows = (int64_t)p->batch * p->beams, most = std::max<int64_t>(1, kSelectCtas / rows);
   a.seg_slices = (int32_t)ceil_div(slices, std::min(slices, most));
   a.segments = (int32_t)ceil_div(slices, a.seg_slices);
@@ -52,8 +52,8 @@ kvsel_status kvsel_beam_select_workspace_size(const kvsel_beam_select_desc* desc
   const kvsel_status st = check_select(desc, &a);
   if (st != KVSEL_OK) return st;
   if (bytes == nullptr) return KVSEL_ERR_INVALID_ARG;
-  size_t best, sums;
-  *bytes = beam_select_ws((int64_t)a.batch * a.beams, a.segments, a.n_out, &best, &sums);
+  size_t best, sums, tops;
+  *bytes = beam_select_ws((int64_t)a.batch * a.beams, a.segments, a.n_out, &best, &sums, &tops);
   return KVSEL_OK;
 }
 
@@ -71,8 +71,8 @@ kvsel_status kvsel_beam_select(const kvsel_beam_select_desc* desc, const void* l
     if (!aligned(p, 4)) return KVSEL_ERR_INVALID_ARG;
   if (scores_out == scores) return KVSEL_ERR_INVALID_ARG;
   if (ws == nullptr || !aligned(ws, KVSEL_WS_ALIGN)) return KVSEL_ERR_WORKSPACE;
-  size_t best, sums;
-  if (ws_bytes < beam_select_ws((int64_t)a.batch * a.beams, a.segments, a.n_out, &best, &sums)) return KVSEL_ERR_WORKSPACE;
+  size_t best, sums, tops;
+  if (ws_bytes < beam_select_ws((int64_t)a.batch * a.beams, a.segments, a.n_out, &best, &sums, &tops)) return KVSEL_ERR_WORKSPACE;
   a.logits = logits;
   a.scores = scores;
   a.ended = ended;
@@ -81,7 +81,8 @@ kvsel_status kvsel_beam_select(const kvsel_beam_select_desc* desc, const void* l
   a.tokens = tokens;
   a.lse = lse;
   a.best = reinterpret_cast<float2*>(static_cast<char*>(ws) + best);
-  a.sums = reinterpret_cast<double2*>(static_cast<char*>(ws) + sums);
+  a.sums = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + sums);
+  a.tops = reinterpret_cast<float*>(static_cast<char*>(ws) + tops);
   return launch_beam_select(a, desc->dtype, stream);
 }
 

@@ -7,8 +7,8 @@
 //
 // A segment's n best: of 64 (or 256) groups of threads the n-th largest group maximum over the first 8192 tokens is found bit
 // by bit by one warp, and is a lower bound of their n-th largest logit.  The tokens at or above it (n to 1.4 n of independent
-// logits) are collected and ranked by counting, and the n-th of them is the bound for what follows, renewed when enough have
-// passed it: a token is compared once and hardly ever more.  Where too many reach the bound at once (equal logits, rising
+// logits) are collected and ranked by counting, and the n-th of them is the bound for what follows, renewed when n more have
+// passed it (half as many tokens of the next slice do then): a token is compared once and hardly ever more.  Where too many reach the bound at once (equal logits, rising
 // ones) they are taken 256 at a time.  Tokens at -inf, of which constrained decoding has most of a vocabulary, are left out and
 // fill a short list by their order.
 //
@@ -28,7 +28,7 @@ namespace kvsel {
 namespace {
 
 constexpr int kThreads = 256, kEach = kSliceKeys / kThreads;
-constexpr int kCandidates = 1024, kRenew = 320;    // room for candidates, and how many renew the bound
+constexpr int kCandidates = 1024;              // room for candidates
 constexpr int kMergeThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -58,7 +58,7 @@ __device__ __forceinline__ float ex2f(float x) {
 template <typename T>
 struct Tokens {
   static constexpr int V = 16 / (int)sizeof(T), WORDS = kEach * (int)sizeof(T) / 4;
-  uint32_t w[WORDS];
+  alignas(16) uint32_t w[WORDS];
   static __device__ __forceinline__ int place(int tid, int i) { return (i / V * kThreads + tid) * V + i % V; }
 
   // Two aligned vectors and a shift by the row's offset of WORD words and `bits`.  (The words before the first token, and behind
@@ -91,14 +91,17 @@ struct Tokens {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < WORDS; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          const int p = place(tid, i);
-          w[i] = p < n ? __float_as_uint(x[p]) : 0xff800000u;
-        } else {
-          const int p = place(tid, 2 * i);
-          T u = p < n ? x[p] : T(-INFINITY), v = p + 1 < n ? x[p + 1] : T(-INFINITY);
-          w[i] = (uint32_t)*reinterpret_cast<uint16_t*>(&u) | (uint32_t)*reinterpret_cast<uint16_t*>(&v) << 16;
+      for (int v = 0; v < WORDS / 4; ++v) {
+        const int p = V * (v * kThreads + tid);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[4 * v + k] = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+        if (p < n) {                          // (single elements: the row's last slice alone)
+          alignas(16) T y[V];
+          *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(w + 4 * v);
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (p + e < n) y[e] = x[p + e];
+          *reinterpret_cast<uint4*>(w + 4 * v) = *reinterpret_cast<const uint4*>(y);
         }
       }
     }
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_slice(c
         if (c > kCandidates - kThreads) renew();
       }
       renew();
-    } else if (c_all > kRenew || first == s0 || first + kSliceKeys >= s1) {
+    } else if (c_all >= 2 * n || first == s0 || first + kSliceKeys >= s1) {
       renew();
     }
   }
@@ -313,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_slice(c
     uint64_t all = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) all += warp_sum[w];
-    a.sums[row * a.segments + seg] = make_double2((double)top, (double)all * 0x1p-40);
+    a.tops[row * a.segments + seg] = top;
+    a.sums[row * a.segments + seg] = all;
   }
   const int c_all = n_cand;
   float2* out = a.best + (row * a.segments + seg) * n;
@@ -383,6 +387,7 @@ __device__ __forceinline__ int entry(const SelectArgs& a, const Beam& b, int64_t
 __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constant__ SelectArgs a) {
   extern __shared__ uint64_t sm[];
   __shared__ Beam beam[kMaxBeams];
+  __shared__ float row_top[kMaxBeams];
   __shared__ int n_cand, n_lists, total;
   __shared__ int16_t chosen[kMaxBeamOut];
   constexpr int kMost = kMaxBeamOut * kMaxBeamOut;
@@ -392,26 +397,33 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   uint64_t* head = reinterpret_cast<uint64_t*>(what + kMost);  // [lists]
   const int64_t set = blockIdx.x, row0 = set * a.beams;
   wait_for_earlier_kernels();
-  // the rows' log-sums, a warp each: lanes take segments in turn, whatever the launch
+  // The rows' log-sums.  A 64-bit operation takes a warp 16 cycles of the SM whatever its lanes do (two lanes a clock), so lanes
+  // are filled: a thread for a segment's term, then one for a row's sum, in the order of its segments.
+  double* term = reinterpret_cast<double*>(head);              // [lists], read before the heads are written
   for (int k = warp; k < a.beams; k += kMergeThreads / 32) {
-    const double2* s = a.sums + (row0 + k) * a.segments;
-    double top = -INFINITY, sum = 0.0;
-    for (int i = lane; i < a.segments; i += 32) top = fmax(top, s[i].x);
+    float top = -INFINITY;
+    for (int i = lane; i < a.segments; i += 32) top = fmaxf(top, a.tops[(row0 + k) * a.segments + i]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int i = lane; i < a.segments; i += 32) {
-      const double2 p = s[i];
-      if (p.y > 0.0 && p.x - top > -700.0) sum += p.y * exp64(p.x - top);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      const double lse = isinf(top) ? top : top + log64(sum);
-      const double score = a.scores[row0 + k];
-      const bool ended = a.ended != nullptr && a.ended[row0 + k] != 0;
-      beam[k] = Beam{lse, score, !isfinite(score) ? 2 : ended ? 1 : isinf(lse) ? 2 : 0};
-      if (a.lse != nullptr) a.lse[row0 + k] = (float)lse;
-    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) row_top[k] = top;
+  }
+  __syncthreads();
+  for (int l = tid; l < lists; l += kMergeThreads) {
+    const float top = row_top[l / a.segments], mine = a.tops[row0 * a.segments + l];
+    const uint64_t sum = a.sums[row0 * a.segments + l];
+    const float less = mine - top;                             // (to tell 0 and what is nothing beside the largest; -inf - -inf is NaN)
+    term[l] = sum == 0 ? 0.0 : less == 0.f ? (double)sum : less > -700.f ? (double)sum * exp64((double)mine - (double)top) : 0.0;
+  }
+  __syncthreads();
+  if (tid < a.beams) {
+    const int k = tid;
+    double sum = 0.0;
+    for (int i = 0; i < a.segments; ++i) sum += term[k * a.segments + i];
+    const float top = row_top[k], score = a.scores[row0 + k];
+    const double lse = isinf(top) ? (double)top : (double)top + log64(sum * 0x1p-40);
+    const bool ended = a.ended != nullptr && a.ended[row0 + k] != 0;
+    beam[k] = Beam{lse, (double)score, !isfinite(score) ? 2 : ended ? 1 : isinf(top) ? 2 : 0};
+    if (a.lse != nullptr) a.lse[row0 + k] = (float)lse;
   }
   if (tid == 0) n_cand = n_lists = 0;
   __syncthreads();
@@ -517,10 +529,11 @@ kvsel_status launch_slices(const SelectArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t beam_select_ws(int64_t rows, int32_t segments, int32_t n_out, size_t* best_off, size_t* sums_off) {
+size_t beam_select_ws(int64_t rows, int32_t segments, int32_t n_out, size_t* best_off, size_t* sums_off, size_t* tops_off) {
   auto up = [](size_t x) { return (x + KVSEL_WS_ALIGN - 1) / KVSEL_WS_ALIGN * KVSEL_WS_ALIGN; };
   *sums_off = sizeof(DeviceError);
-  *best_off = up(*sums_off + sizeof(double2) * (size_t)(rows * segments));
+  *tops_off = up(*sums_off + sizeof(uint64_t) * (size_t)(rows * segments));
+  *best_off = up(*tops_off + sizeof(float) * (size_t)(rows * segments));
   return up(*best_off + sizeof(float2) * (size_t)(rows * segments) * n_out);
 }
 
