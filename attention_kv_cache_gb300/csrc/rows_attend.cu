@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ R
   const float vsc = (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / a.unit;
   float own = 0.f;
   if (own_lse != -INFINITY) {
-    const float z = own_lse * kLog2e, top = fmaxf(M, z);
+    const float z = own_lse * kLog2e + a.shift, top = fmaxf(M, z);      // (the pieces' sums are 2^shift times as large)
     const float wo = M == top ? 1.f : exp2f(M - top);
     own = z == top ? 1.f : exp2f(z - top);    // (of a NaN, NaN)
     M = top;
@@ -349,8 +349,11 @@ __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ R
   if (a.lse != nullptr && c0 == 0) a.lse[out] = (M + log2f(den) - a.shift) * 0.6931471805599453f;
 }
 
+// Whether weights are two 16-bit parts (rows_attend.cuh says why).
+bool split_weights(const RowsShape& p) { return p.prefix != 0 && p.cache_dtype != KVSEL_DTYPE_E4M3; }
+
 RowsVariant variant(const RowsShape& p) {
-  const bool split = p.prefix != 0;
+  const bool split = split_weights(p);
   if (p.cache_dtype == KVSEL_DTYPE_E4M3) return rows_variant_e4m3(p.d, split);
   return p.dtype == KVSEL_DTYPE_F16 ? rows_variant_f16(p.d, split) : rows_variant_bf16(p.d, split);
 }
@@ -471,9 +474,10 @@ RowsArgs rows_args(const RowsShape& p, const RowsArgs& in, const Layout& lay, vo
   a.grid = lay.grid;
   a.max_items = (int32_t)lay.max_items;
   a.head_rows = p.batch * (p.h_q / p.h_kv);
-  const bool bf16 = p.cache_dtype == KVSEL_DTYPE_BF16;
-  a.unit = !p.prefix ? 1.f : bf16 ? weight_unit<kBf16>() : weight_unit<kF16>();
-  a.shift = p.prefix ? 0.f : bf16 ? -8.f : 13.f;
+  // factor on O against the sums, and binary orders on both
+  const bool bf16 = p.cache_dtype == KVSEL_DTYPE_BF16, split = split_weights(p);
+  a.unit = !split ? 1.f : bf16 ? weight_unit<kBf16>() : weight_unit<kF16>();
+  a.shift = split ? 0.f : bf16 ? -8.f : 13.f;
   return a;
 }
 

@@ -17,9 +17,10 @@
 // up to 64 (32) rows fill the tile's 128 rows with two (four) copies, which take 64 (32) keys of a step each: the softmax of
 // a step is a thread's loop over its keys, 2000 cycles for 128.  What tiles and copies hold is merged when the piece ends.
 //
-// SPLIT (the shared prefix): weights are a high and a low 16-bit part, as in the decode kernel whose results it must match;
-// the steps wait for HBM there, so the third product is free up to 256 rows.  Without it (chunks, bound by the tensor
-// cores) a weight is rounded once, 2^-9 of it over bf16 and 2^-12 over fp16 products.
+// SPLIT (the shared prefix over 16-bit pools): weights are a high and a low 16-bit part, as in the decode kernel whose results it
+// must match; the steps wait for HBM there, so the third product is free up to 128 rows.  Without it (chunks, bound by the tensor
+// cores, and 8-bit pools) a weight is rounded once, by at most 2^-8 of it over bf16 and 2^-11 over fp16 products: what the
+// outputs' own rounding is, and far below a row's in 8 bits.  (64 requests behind 32768 e4m3 rows: 200 us with the low parts, 174 without.)
 // Factors on the weights as in paged_attend.cuh: 2^-8 over bf16 and 2^13 over fp16 products; without SPLIT it is taken by the
 // exponent, whose rounding at 13 (2^-21 of a weight) is far below the weight's own.
 //
@@ -249,65 +250,73 @@ __device__ __forceinline__ float rows_weights(const float* v, float mul, float n
 // A row's scores as they are compared, from the products: with a cap c z' = c tanh(z / c), a bias slope (t - p), in base 2.
 struct RowsScore {
   float sc, icap, cap2, slope;        // sc: scale with log2 e; icap: scale / cap
-  bool capped, general;               // general: more than a positive factor
+  bool capped, biased;                // biased: with a bias, or a factor that is not positive
 };
-// The products of a thread's keys that are more than a factor away from their scores, or some of which the row does not see:
-// rewritten in TMEM, 32 at a time, the ones not seen as -inf.  d0: distance of the first key to the row's own.
-__device__ __forceinline__ void rows_scores(uint32_t s, int blocks, const RowsScore k, float d0, uint4 see) {
-  uint32_t word[4] = {see.x, see.y, see.z, see.w};
-#pragma unroll 1
-  for (int j = 0; j < blocks; ++j) {
-    float z[32];
-    sm100::tmem_ld32(s + 32 * j, z);
-    if (k.capped) {
-      const float2 ic = make_float2(k.icap, k.icap), cp = make_float2(k.cap2, k.cap2);
-      float big = 0.f;
+// N products as their scores: capped, biased (d0: distance of the first key to the row's own), and those not seen (by 32, where not
+// all are) as -inf.
+template <int N>
+__device__ __forceinline__ void rows_scores(float* z, const RowsScore& k, float d0, bool whole, const uint32_t* see) {
+  if (k.capped) {
+    const float2 ic = make_float2(k.icap, k.icap), cp = make_float2(k.cap2, k.cap2);
+    float big = 0.f;
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const float2 x = __fmul2_rn(make_float2(z[c], z[c + 1]), ic);
-        z[c] = x.x;
-        z[c + 1] = x.y;
-        big = max3(big, fabsf(x.x), fabsf(x.y));
-      }
-      // (scores far below the cap are the rule: the series alone, as tanh_fast has it below 1/4)
-      if (__all_sync(0xffffffffu, big < 0.25f)) {
-        const float2 c3 = make_float2(-17.f / 315.f, -17.f / 315.f), c2 = make_float2(2.f / 15.f, 2.f / 15.f),
-                     c1 = make_float2(-1.f / 3.f, -1.f / 3.f), one = make_float2(1.f, 1.f);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const float2 x = make_float2(z[c], z[c + 1]), x2 = __fmul2_rn(x, x);
-          const float2 y = __fmul2_rn(__fmul2_rn(x, cp), __ffma2_rn(x2, __ffma2_rn(x2, __ffma2_rn(x2, c3, c2), c1), one));
-          z[c] = y.x;
-          z[c + 1] = y.y;
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) z[c] = k.cap2 * tanh_fast(z[c]);
-      }
+    for (int c = 0; c < N; c += 2) {
+      const float2 x = __fmul2_rn(make_float2(z[c], z[c + 1]), ic);
+      z[c] = x.x;
+      z[c + 1] = x.y;
+      big = max3(big, fabsf(x.x), fabsf(x.y));
     }
-    if (k.general) {
-      const float2 s2 = make_float2(k.capped ? 1.f : k.sc, k.capped ? 1.f : k.sc), sl = make_float2(k.slope, k.slope);
-      const float2 dd = make_float2(d0 + 32.f * j, d0 + 32.f * j + 1.f);
+    // (scores far below the cap are the rule: the series alone, as tanh_fast has it below 1/4)
+    if (__all_sync(0xffffffffu, big < 0.25f)) {
+      const float2 c3 = make_float2(-17.f / 315.f, -17.f / 315.f), c2 = make_float2(2.f / 15.f, 2.f / 15.f),
+                   c1 = make_float2(-1.f / 3.f, -1.f / 3.f), one = make_float2(1.f, 1.f);
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        const float2 y = __ffma2_rn(sl, __fadd2_rn(dd, make_float2((float)c, (float)c)), __fmul2_rn(make_float2(z[c], z[c + 1]), s2));
+      for (int c = 0; c < N; c += 2) {
+        const float2 x = make_float2(z[c], z[c + 1]), x2 = __fmul2_rn(x, x);
+        const float2 y = __fmul2_rn(__fmul2_rn(x, cp), __ffma2_rn(x2, __ffma2_rn(x2, __ffma2_rn(x2, c3, c2), c1), one));
         z[c] = y.x;
         z[c + 1] = y.y;
       }
-    }
-    const uint32_t w = j == 0 ? word[0] : j == 1 ? word[1] : j == 2 ? word[2] : word[3];
-    uint32_t r[32];
+    } else {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) r[c] = (w >> c) & 1u ? __float_as_uint(z[c]) : 0xff800000u;
-    sm100::tmem_st32(s + 32 * j, r);
+      for (int c = 0; c < N; ++c) z[c] = k.cap2 * tanh_fast(z[c]);
+    }
+  }
+  if (k.biased) {                                 // (and where the factor is not positive: the bias is 0 then)
+    const float2 s2 = make_float2(k.capped ? 1.f : k.sc, k.capped ? 1.f : k.sc), sl = make_float2(k.slope, k.slope);
+    const float2 dd = make_float2(d0, d0 + 1.f);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float2 y = __ffma2_rn(sl, __fadd2_rn(dd, make_float2((float)c, (float)c)), __fmul2_rn(make_float2(z[c], z[c + 1]), s2));
+      z[c] = y.x;
+      z[c + 1] = y.y;
+    }
+  }
+  if (!whole) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) z[c] = (see[c / 32] >> (c & 31)) & 1u ? z[c] : -INFINITY;
+  }
+}
+// The same for a step's 128 keys, in TMEM.
+__device__ __forceinline__ void rows_scores_tmem(uint32_t s, const RowsScore& k, float d0, bool whole, uint4 see) {
+#pragma unroll 1
+  for (int j = 0; j < 2; ++j) {
+    uint32_t r[64];
+    sm100::tmem_ld64_async(s + 64 * j, r);
+    sm100::tmem_wait_ld64(r);
+    const uint32_t word[2] = {j ? see.z : see.x, j ? see.w : see.y};
+    rows_scores<64>(reinterpret_cast<float*>(r), k, d0 + 64.f * j, whole, word);
+    sm100::tmem_st64(s + 64 * j, r);
   }
   sm100::tmem_wait_st();
 }
 
 // One step of a thread's row: weights of its keys, written over S: all 128 of the step (COPIES 1), or the 32 of copy `copy` with
-// zeros in the other copies' places; updates the offset m, mo, the sum l; returns the factor on what O holds.
+// zeros in the other copies' places; updates the offset m, mo, the sum l; returns the factor on what O holds.  The scores
+// of all 128 are in TMEM as they are compared, but for the factor `mul`; a copy forms its own here.
 template <int KIND, bool SPLIT, int COPIES>
-__device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, float& m, float& mo, float& l) {
+__device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, const RowsScore& k, float d0, bool whole, uint32_t see, float& m, float& mo,
+                                           float& l) {
   using namespace sm100;
   constexpr float kShift = SPLIT ? 0.f : (KIND == kBf16 ? -8.f : 13.f), kLag = weight_lag<KIND>();
   float alpha = 1.f, sum;
@@ -354,6 +363,7 @@ __device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, floa
 #pragma unroll
     for (int c = 0; c < 16; ++c) zero[c] = 0u;
     tmem_ld32(s + 32 * copy, z);
+    rows_scores<32>(z, k, d0, whole, &see);
     offset(rows_max<32>(z) * mul);
     sum = rows_weights<KIND, SPLIT, 32>(z, mul, kShift - mo, hi, lo);
 #pragma unroll
@@ -881,8 +891,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
         score.icap = score.capped ? ksc / a.softcap : 0.f;
         score.cap2 = a.softcap * kLog2e;
         score.slope = a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
-        score.general = score.capped || a.slopes != nullptr || !(head_scale > 0.f);
-        const float mul = score.general ? 1.f : score.sc;
+        score.biased = a.slopes != nullptr || (!score.capped && !(head_scale > 0.f));
+        const bool plain = !score.capped && !score.biased;
+        const float mul = plain ? score.sc : 1.f;
         bool begun = false;
         if (lane == 0 && quarter == 0) o_begun[x] = 0;          // (before the piece's first weights are told of)
         uint32_t step = i0;
@@ -909,21 +920,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
             }
           }
           if (!idle) {
-            if (!whole || score.general) {
+            uint32_t word[4] = {there.x, there.y, there.z, there.w};
+            if (!whole) {
               const int from = low - t0, to = pos + 1 - t0;     // keys of the step that the row sees: [from, to)
-              uint32_t word[4] = {there.x, there.y, there.z, there.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int lo = min(32, max(0, from - 32 * k)), hi = min(32, max(0, to - 32 * k));
                 const uint32_t below_hi = hi >= 32 ? 0xffffffffu : (1u << hi) - 1u, below_lo = lo >= 32 ? 0xffffffffu : (1u << lo) - 1u;
                 word[k] = live ? word[k] & below_hi & ~below_lo : 0u;
               }
-              if (small) word[0] = copy == 0 ? word[0] : copy == 1 ? word[1] : copy == 2 ? word[2] : word[3];
-              rows_scores(tm + kSCol + 32 * copy, small ? 1 : 4, score, (float)(t0 + 32 * copy - pos), make_uint4(word[0], word[1], word[2], word[3]));
             }
             float alpha;
-            if (small) alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, copy, mul, m, mo, l);
-            else alpha = rows_step<KIND, SPLIT, 1>(tm + kSCol, 0, mul, m, mo, l);
+            if (small) {
+              const uint32_t see = copy == 0 ? word[0] : copy == 1 ? word[1] : copy == 2 ? word[2] : word[3];
+              alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, copy, mul, score, (float)(t0 + 32 * copy - pos), whole, see, m, mo, l);
+            } else {
+              if (!whole || !plain) rows_scores_tmem(tm + kSCol, score, (float)(t0 - pos), whole, make_uint4(word[0], word[1], word[2], word[3]));
+              alpha = rows_step<KIND, SPLIT, 1>(tm + kSCol, 0, mul, score, 0.f, true, 0u, m, mo, l);
+            }
             // O of the tile's step before is final (this step's S was issued behind its P V)
             if ((had || begun) && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -1080,7 +1094,8 @@ struct RowsVariant {
 };
 template <int D, int KIND>
 RowsVariant rows_variant(bool split) {
-  return {split ? rows_attend<D, KIND, true> : rows_attend<D, KIND, false>, rows_smem<D, KIND>()};
+  if constexpr (KIND == kE4m3) return {rows_attend<D, KIND, false>, rows_smem<D, KIND>()};
+  else return {split ? rows_attend<D, KIND, true> : rows_attend<D, KIND, false>, rows_smem<D, KIND>()};
 }
 // The kernels of a pool type, each in a file of its own (rows_attend_*.cu).
 RowsVariant rows_variant_bf16(int d, bool split);

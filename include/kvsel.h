@@ -678,7 +678,8 @@ KVSEL_API kvsel_status kvsel_chunk_attend(const kvsel_cache_desc* cache, const k
  * rows count as not shared: the output is right either way.  Other errors are kvsel_paged_attend's; those of
  * a shared page name the group's first request.
  *
- * Arithmetic: kvsel_paged_attend's, the shared rows' and the own rows' parts joined in fp32.
+ * Arithmetic: kvsel_paged_attend's, the shared rows' and the own rows' parts joined in fp32; but with an e4m3 pool a
+ * shared row's weight is rounded once to fp16 (by at most 2^-11 of it) instead of held in two parts.
  */
 KVSEL_API kvsel_status kvsel_prefix_attend_workspace_size(const kvsel_cache_desc* cache,
                                                           const kvsel_paged_attend_desc* desc, int32_t n_groups,
