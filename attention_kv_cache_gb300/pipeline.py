@@ -225,12 +225,22 @@ class PagedDecoder:
     ``rope`` is a kvsel.RopeScaling over ``rot_dim`` elements (None: rows arrive rotated); ``norms`` is
     (q_weight, k_weight) per layer, or None; ``scales`` is (k_scale, v_scale) [n_layers, h_kv] of an
     8-bit pool (``cache_dtype`` torch.float8_e4m3fn).
+
+    Prompts: with ``max_tokens`` rows a step, ``begin_chunk`` and ``chunk_layer`` take any number of new rows per
+    request (a prompt's chunk, or all of it) instead of one.
+
+    Beams: with ``beams`` requests to a set, ``fork`` shares a set's first beam's pages among all of them, every layer's
+    attention reads what they share once, and ``reorder`` puts the beams' pages in order after a selection
+    (``BeamSelector``).  ``share`` names other groups of requests behind common prefixes.
     """
 
     def __init__(self, *, n_layers: int, h_q: int, h_kv: int, head_dim: int, batch: int, max_rows: int,
                  n_pages: int, page_size: int = 16, dtype=torch.bfloat16, cache_dtype=None, rope=None,
                  rot_dim: Optional[int] = None, rope_layout: int = K.ROPE_HALF, norms=None, norm_eps: float = 1e-6,
-                 scales=None, softcap: float = 0.0, window: int = 0, slopes=None, device="cuda"):
+                 scales=None, softcap: float = 0.0, window: int = 0, slopes=None, max_tokens: int = 0, beams: int = 1,
+                 device="cuda"):
+        if beams < 1 or batch % beams:
+            raise ValueError(f"{batch} requests are not sets of {beams} beams")
         cache_dtype = dtype if cache_dtype is None else cache_dtype
         P = page_size
         self.n_layers, self.batch, self.n_pages, self.P = n_layers, batch, n_pages, P
@@ -259,9 +269,24 @@ class PagedDecoder:
         self.q_out = torch.empty((batch, h_q, head_dim), dtype=dtype, device=device)
         self.o = torch.empty_like(self.q_out)
         n = max(K.kvsel_page_assign_workspace_size(batch), K.kvsel_paged_attend_workspace_size(self.cache, self.attend))
-        ws = torch.zeros(n + K.WS_ALIGN, dtype=torch.uint8, device=device)
+        self.max_tokens, self.beams, self.groups = max_tokens, beams, None
+        if max_tokens:
+            heads = lambda h: torch.empty((max_tokens, h, head_dim), dtype=dtype, device=device)   # noqa: E731
+            self.chunk = K.make_chunk_attend_desc(batch=batch, max_blocks=max_blocks, max_tokens=max_tokens,
+                                                  softcap=softcap, window=window)
+            self.chunk_slots, self.chunk_positions = torch.empty(max_tokens, **i64), torch.empty(max_tokens, **i64)
+            self.chunk_q, self.chunk_o = heads(h_q), heads(h_q)
+            n = max(n, K.kvsel_chunk_attend_workspace_size(self.cache, self.chunk))
+        if beams > 1:
+            self.beam = K.make_beam_reorder_desc(batch=batch // beams, beams=beams, max_blocks=max_blocks,
+                                                 n_layers=n_layers, layer_stride=self.k_cache.stride(0))
+            n = max(n, K.kvsel_beam_reorder_workspace_size(self.beam))
+        self.ws = self._workspace(n)
+
+    def _workspace(self, n: int):
+        ws = torch.zeros(n + K.WS_ALIGN, dtype=torch.uint8, device=self.device)
         off = (-ws.data_ptr()) % K.WS_ALIGN
-        self.ws = ws[off:off + n]
+        return ws[off:off + n]
 
     def _assign(self, n_new, slots, positions, stream):
         K.kvsel_page_assign(self.P, self.n_pages, self.lens, n_new, self.free_pages, self.free_head, self.tables,
@@ -324,6 +349,15 @@ class PagedDecoder:
         """Pages, slots and positions of one new row per request."""
         self._assign(self.n_new, self.slots, self.positions, stream)
 
+    def _append(self, layer: int, q, k, v, positions, slots, q_out, stream):
+        ks, vs = self._scale(layer)
+        desc = K.make_rope_desc(rot_dim=self.rot_dim, layout=self.rope_layout, factor=self.factor,
+                                norm_eps=self.norm_eps, q=q, k=k, v=v)
+        qw, kw = (None, None) if self.norms is None else self.norms[layer]
+        K.kvsel_rope_append(self.cache, desc, q, k, v, positions if self.rot_dim else None, slots, qw, kw,
+                            self.inv_freq, q_out, self.k_cache[layer], self.v_cache[layer], ks, vs, self.ws,
+                            stream=stream)
+
     def layer(self, layer: int, q, k, v, stream=None):
         """q [batch, h_q, d], k and v [batch, h_kv, d] (any row strides) of the step's rows; returns o [batch, h_q, d],
         which the next call overwrites."""
@@ -331,12 +365,110 @@ class PagedDecoder:
         self._checked("k", k, self._kv_shape)
         self._checked("v", v, self._kv_shape)
         ks, vs = self._scale(layer)
-        desc = K.make_rope_desc(rot_dim=self.rot_dim, layout=self.rope_layout, factor=self.factor,
-                                norm_eps=self.norm_eps, q=q, k=k, v=v)
-        qw, kw = (None, None) if self.norms is None else self.norms[layer]
-        K.kvsel_rope_append(self.cache, desc, q, k, v, self.positions if self.rot_dim else None, self.slots, qw, kw,
-                            self.inv_freq, self.q_out, self.k_cache[layer], self.v_cache[layer], ks, vs, self.ws,
-                            stream=stream)
+        self._append(layer, q, k, v, self.positions, self.slots, self.q_out, stream)
+        if self.groups is not None:
+            K.kvsel_prefix_attend(self.cache, self.attend, self.q_out, self.k_cache[layer], self.v_cache[layer], self.tables,
+                                  self.lens, *self.groups, self.slopes, ks, vs, self.o, None, self.ws, stream=stream)
+            return self.o
         K.kvsel_paged_attend(self.cache, self.attend, self.q_out, self.k_cache[layer], self.v_cache[layer], self.tables,
                              self.lens, self.slopes, ks, vs, self.o, None, self.ws, stream=stream)
         return self.o
+
+    def begin_chunk(self, n_new, stream=None):
+        """Pages, slots and positions of ``n_new`` [batch] new rows (int64, on the device; at most ``max_tokens`` in all)
+        behind the rows of every request.  Token i of request b is row ``indptr[b] + i`` of ``chunk_layer``'s tensors."""
+        if not self.max_tokens:
+            raise ValueError("chunks need max_tokens")
+        if n_new.shape != (self.batch,) or n_new.dtype != torch.int64 or n_new.device != self.lens.device:
+            raise ValueError(f"n_new is {tuple(n_new.shape)} {n_new.dtype} on {n_new.device}, not ({self.batch},) int64 on "
+                             f"{self.lens.device}")
+        self._assign(n_new, self.chunk_slots, self.chunk_positions, stream)
+
+    def chunk_layer(self, layer: int, q, k, v, stream=None):
+        """q [max_tokens, h_q, d], k and v [max_tokens, h_kv, d] of the chunk's rows, request by request; returns o
+        [max_tokens, h_q, d], which the next call overwrites (rows behind the last token: as they were)."""
+        if not self.max_tokens:
+            raise ValueError("chunks need max_tokens")
+        for what, t, h in (("q", q, self.h_q), ("k", k, self.h_kv), ("v", v, self.h_kv)):
+            self._checked(what, t, (self.max_tokens, h, self.d))
+        ks, vs = self._scale(layer)
+        self._append(layer, q, k, v, self.chunk_positions, self.chunk_slots, self.chunk_q, stream)
+        K.kvsel_chunk_attend(self.cache, self.chunk, self.chunk_q, self.k_cache[layer], self.v_cache[layer], self.tables,
+                             self.lens, self.indptr, self.slopes, ks, vs, self.chunk_o, None, self.ws, stream=stream)
+        return self.chunk_o
+
+    def share(self, group_indptr, shared_lens):
+        """From now on requests ``group_indptr[j] .. group_indptr[j + 1] - 1`` name the same pages for their first
+        ``shared_lens[j]`` rows, which a layer then reads once (int64, on the device; None: no more).  Not in a capture."""
+        if group_indptr is None:
+            self.groups = None
+            return
+        n = shared_lens.numel()
+        for what, t, size in (("group_indptr", group_indptr, n + 1), ("shared_lens", shared_lens, n)):
+            if t.shape != (size,) or t.dtype != torch.int64 or t.device != self.lens.device:
+                raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}, not ({size},) int64 on {self.lens.device}")
+        need = K.kvsel_prefix_attend_workspace_size(self.cache, self.attend, n)
+        if need > self.ws.numel():
+            self.ws = self._workspace(need)
+        self.groups = (group_indptr, shared_lens)
+
+    def reorder(self, parents, stream=None):
+        """Beam j of every set goes on from beam ``parents[set, j]`` (int32, on the device): lengths and pages follow, pages
+        that no beam names any more return to the queue, and a part-full last page is copied for a second child."""
+        if self.beams == 1:
+            raise ValueError("a decoder of single beams")
+        shape = (self.batch // self.beams, self.beams)
+        if parents.shape != shape or parents.dtype != torch.int32 or parents.device != self.lens.device or not parents.is_contiguous():
+            raise ValueError(f"parents is {tuple(parents.shape)} {parents.dtype} on {parents.device}, not {shape} int32 on "
+                             f"{self.lens.device}, contiguous")
+        current, stream = torch.cuda.current_stream(), _torch_stream(stream)
+        if stream != current:
+            stream.wait_stream(current)
+        with torch.cuda.stream(stream):
+            K.kvsel_beam_reorder(self.cache, self.beam, parents, self.lens, self.tables, self.free_pages, self.free_head,
+                                 self.tables, self.lens, self.free_head, self.k_cache, self.v_cache, self.ws, stream=stream)
+            at = self.pos_offset.view(shape)
+            at.copy_(at.gather(1, parents.long().clamp(0, self.beams - 1)))    # (a parent out of range changes nothing else)
+
+    def fork(self, stream=None):
+        """Every set's beams share its first beam's pages (the others hold none, or lose them); the rows in whole pages at this
+        time are what a layer then reads once for a set.  Not in a capture."""
+        self.reorder(torch.zeros((self.batch // self.beams, self.beams), dtype=torch.int32, device=self.device), stream)
+        current, stream = torch.cuda.current_stream(), _torch_stream(stream)
+        with torch.cuda.stream(stream):
+            shared = self.lens[::self.beams] // self.P * self.P
+            groups = torch.arange(0, self.batch + 1, self.beams, dtype=torch.int64, device=self.device)
+        if stream != current:
+            current.wait_stream(stream)
+        self.share(groups, shared)
+
+
+class BeamSelector:
+    """Selections of one shape: the ``n_out`` best continuations of ``sets`` sets of ``beams`` beams over ``vocab`` tokens."""
+
+    def __init__(self, *, sets: int, beams: int, n_out: int, vocab: int, dtype=torch.bfloat16, pad_token: int = 0,
+                 row_stride: int = 0, device="cuda"):
+        kind = {torch.bfloat16: K.DTYPE_BF16, torch.float16: K.DTYPE_F16, torch.float32: K.DTYPE_F32}[dtype]
+        self.rows, self.vocab, self.dtype, self.row_stride = sets * beams, vocab, dtype, row_stride or vocab
+        self.shape, self.device = (sets, beams), torch.device(device)
+        self.desc = K.make_beam_select_desc(batch=sets, beams=beams, n_out=n_out, vocab=vocab, dtype=kind,
+                                            row_stride=row_stride, pad_token=pad_token)
+        n = K.kvsel_beam_select_workspace_size(self.desc)
+        ws = torch.zeros(n + K.WS_ALIGN, dtype=torch.uint8, device=device)
+        off = (-ws.data_ptr()) % K.WS_ALIGN
+        self.ws = ws[off:off + n]
+        self.scores = torch.empty((sets, n_out), device=device)
+        self.parents, self.tokens = (torch.empty((sets, n_out), dtype=torch.int32, device=device) for _ in range(2))
+
+    def select(self, logits, scores, ended=None, stream=None):
+        """logits [sets * beams, vocab] with the rows' stride, scores [sets, beams] fp32, ended [sets, beams] uint8 or None;
+        returns (scores, parents, tokens) [sets, n_out], which the next call overwrites."""
+        if logits.shape != (self.rows, self.vocab) or logits.dtype != self.dtype or logits.stride() != (self.row_stride, 1):
+            raise ValueError(f"logits are {tuple(logits.shape)} {logits.dtype} of strides {logits.stride()}, not "
+                             f"({self.rows}, {self.vocab}) {self.dtype} of ({self.row_stride}, 1)")
+        for what, t, dtype in (("scores", scores, torch.float32), ("ended", ended, torch.uint8)):
+            if t is not None and (t.shape != self.shape or t.dtype != dtype or not t.is_contiguous()):
+                raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype}, not {self.shape} {dtype}, contiguous")
+        K.kvsel_beam_select(self.desc, logits, scores, ended, self.scores, self.parents, self.tokens, None, self.ws,
+                            stream=stream)
+        return self.scores, self.parents, self.tokens

@@ -1,4 +1,5 @@
-"""Float64 definitions of the calls over a paged cache (page assignment, norm + rotation + write, attention).
+"""Float64 definitions of the calls over a paged cache (page assignment, norm + rotation + write, attention of one or many new
+rows, beam selection and the beams' pages).
 
 Plain numpy, request by request and row by row; imports nothing from the library.
 """
@@ -106,3 +107,70 @@ def paged_attend(q, k, v, scale, softcap=0.0, window=0, slopes=None):
     p = np.exp(z - m)
     total = p.sum(-1, keepdims=True)
     return p @ v / total, (m + np.log(total))[:, 0], p @ np.abs(v) / total, zmax
+
+
+def chunk_attend(q, k, v, first, scale, softcap=0.0, window=0, slopes=None):
+    """One request and KV head: q [n, G, d] of its rows first .. first + n - 1, k, v [first + n, d] (all of its rows) ->
+    (o [n, G, d], lse [n, G], mass [n, G, d], zmax), token by token as paged_attend has them."""
+    out = [paged_attend(q[i], k[:first + i + 1], v[:first + i + 1], scale, softcap, window, slopes) for i in range(q.shape[0])]
+    if not out:
+        d, G = k.shape[1], q.shape[1]
+        return np.zeros((0, G, d)), np.zeros((0, G)), np.zeros((0, G, d)), 0.0
+    return (np.stack([x[0] for x in out]), np.stack([x[1] for x in out]), np.stack([x[2] for x in out]),
+            max(x[3] for x in out))
+
+
+def beam_select(logits, scores, n_out, ended=None, pad_token=0):
+    """One set: logits [beams, vocab], scores [beams] -> (scores, parents, tokens, lse [beams]), sorted in Python."""
+    found, lses = [], []
+    for k, x in enumerate(np.asarray(logits, np.float64)):
+        x = np.where(np.isnan(x), -np.inf, x)
+        top = x.max()
+        lse = top if np.isinf(top) else top + math.log(math.fsum(np.exp(x - top)))
+        lses.append(lse)
+        dead = not math.isfinite(scores[k])
+        for v in range(len(x)):
+            if dead:
+                z = -math.inf
+            elif ended is not None and ended[k]:
+                z = float(scores[k]) if v == pad_token else -math.inf
+            else:
+                z = float(scores[k]) + (x[v] - lse) if math.isfinite(lse) else -math.inf
+            found.append((z, k, v))
+    found.sort(key=lambda f: (-f[0], f[1], f[2]))
+    best = found[:n_out]
+    return (np.array([f[0] for f in best]), np.array([f[1] for f in best]), np.array([f[2] for f in best]), np.array(lses))
+
+
+def beam_reorder(P, parents, lens, tables, queue, head):
+    """Set by set, with lists: (tables, lens, queue, head, copies [(row, column, source page, page, rows)]) after a reorder, or
+    None where it cannot be carried out.  parents [sets][beams], the others by request."""
+    beams = len(parents[0])
+    tables, queue = [list(map(int, t)) for t in tables], [int(x) for x in queue]
+    out, len_out, freed, twins = [list(t) for t in tables], [], [], []
+    for s, chosen in enumerate(parents):
+        held = [tables[s * beams + k][:-(-int(lens[s * beams + k]) // P)] for k in range(beams)]
+        named = {x for p in chosen for x in held[p]}
+        for column in range(max((len(r) for r in held), default=0)):
+            for r in held:
+                if column < len(r) and r[column] not in named:
+                    named.add(r[column])
+                    freed.append(r[column])
+        seen = set()
+        for j, p in enumerate(chosen):
+            row, n = s * beams + j, int(lens[s * beams + p])
+            len_out.append(n)
+            out[row][:len(held[p])] = held[p]
+            if p in seen and n % P:
+                twins.append((row, len(held[p]) - 1, held[p][-1], n % P))
+            seen.add(p)
+    if head < len(freed) or head > len(queue) or len(twins) - len(freed) > len(queue) - head:
+        return None
+    queue[head - len(freed):head] = freed
+    head -= len(freed)
+    copies = []
+    for row, column, source, rows in twins:
+        out[row][column] = queue[head]
+        copies.append((row, column, source, queue[head], rows))
+        head += 1
+    return np.array(out), np.array(len_out), np.array(queue), head, copies
