@@ -31,7 +31,7 @@ kvsel_status launch_beam_select(const SelectArgs& a, int32_t dtype, cudaStream_t
 // ---- beam_reorder.cu ---------------------------------------------------------------------
 constexpr int kReorderCols = 128;     // table columns of a CTA
 struct ReorderCopy {
-  int32_t row, column, source, rows;  // the child's table row and column, the parent's page, its filled rows
+  int32_t source, page, rows, pad;    // the parent's page, the child's, and its filled rows
 };
 struct ReorderPlan {
   int64_t head;                       // queue entries taken before the call
@@ -54,9 +54,11 @@ struct ReorderArgs {
   int32_t* parent_of;                 // [batch * beams]: the parents as they were read
   int32_t* blocks;                    // [batch * beams]: pages held before
   int32_t* count;                     // [batch][tiles]: pages freed, then those freed before; negative: refused
+  int32_t* twin;                      // [batch * beams]: the page of its own that a child gets, or -1
+  int32_t* freed;                     // [batch][tiles][beams * kReorderCols]: pages freed
   ReorderCopy* copy;                  // [batch * beams]
 };
-size_t beam_reorder_ws(int32_t batch, int32_t beams, int32_t tiles, size_t off[5]);
+size_t beam_reorder_ws(int32_t batch, int32_t beams, int32_t tiles, size_t off[7]);
 kvsel_status launch_beam_reorder(const ReorderArgs& a, cudaStream_t s);
 
 }  // namespace kvsel

@@ -90,7 +90,7 @@ kvsel_status kvsel_beam_reorder_workspace_size(const kvsel_beam_reorder_desc* de
   const kvsel_status st = check_reorder(desc);
   if (st != KVSEL_OK) return st;
   if (bytes == nullptr) return KVSEL_ERR_INVALID_ARG;
-  size_t off[5];
+  size_t off[7];
   *bytes = beam_reorder_ws(desc->batch, desc->beams, (int32_t)ceil_div(desc->max_blocks, kReorderCols), off);
   return KVSEL_OK;
 }
@@ -121,7 +121,7 @@ kvsel_status kvsel_beam_reorder(const kvsel_cache_desc* cache, const kvsel_beam_
   if (ws == nullptr || !aligned(ws, KVSEL_WS_ALIGN)) return KVSEL_ERR_WORKSPACE;
   ReorderArgs a;
   a.tiles = (int32_t)ceil_div(desc->max_blocks, kReorderCols);
-  size_t off[5];
+  size_t off[7];
   if (ws_bytes < beam_reorder_ws(desc->batch, desc->beams, a.tiles, off)) return KVSEL_ERR_WORKSPACE;
   a.batch = desc->batch;
   a.beams = desc->beams;
@@ -151,8 +151,10 @@ kvsel_status kvsel_beam_reorder(const kvsel_cache_desc* cache, const kvsel_beam_
   a.plan = reinterpret_cast<ReorderPlan*>(base + off[0]);
   a.parent_of = reinterpret_cast<int32_t*>(base + off[1]);
   a.blocks = reinterpret_cast<int32_t*>(base + off[2]);
-  a.copy = reinterpret_cast<ReorderCopy*>(base + off[3]);
-  a.count = reinterpret_cast<int32_t*>(base + off[4]);
+  a.twin = reinterpret_cast<int32_t*>(base + off[3]);
+  a.copy = reinterpret_cast<ReorderCopy*>(base + off[4]);
+  a.count = reinterpret_cast<int32_t*>(base + off[5]);
+  a.freed = reinterpret_cast<int32_t*>(base + off[6]);
   return launch_beam_reorder(a, stream);
 }
 

@@ -6,10 +6,10 @@
 // in the order (set, column, beam), copies then take pages from the new head on in the order (set, child): the freed ones
 // first.  Integer work, the same result every time.
 //
-// Bound: the copies (rows x layers x heads, read and written); small calls by the chain of launches.  Four of them, since
-// a page's place in the queue needs the count of all sets' freed pages before it: count by (set, 128 columns); one CTA's
-// sums, checks, lengths and list of copies; tables and queue; copies.  Each starts while the one before it drains.
-// A refused call stops at the second: nothing of its outputs is written.
+// Bound: the copies (rows x layers x heads, read and written); small calls by the chain of launches.  Three of them, since
+// a page's place in the queue needs the count of all sets' freed pages before it: the freed pages by (set, 128 columns); one
+// CTA's sums, checks, lengths and list of copies with the pages they take; tables, queue and copies.  Each starts while the one
+// before it drains.  A refused call stops at the second: nothing of its outputs is written.
 #include <algorithm>
 
 #include "beam.cuh"
@@ -19,11 +19,12 @@ namespace kvsel {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int64_t kPlanEntries = 8192;       // (set, tile)s whose sums the plan keeps in shared memory
 constexpr int kCopyThreads = 256;
 
 // What a CTA of (set, column tile) knows of its set: parents, which beams go on, pages held; false: refused (bad gives why).
 struct Set {
-  int32_t parent[kMaxBeams], blocks[kMaxBeams];
+  int32_t parent[kMaxBeams], blocks[kMaxBeams], twin[kMaxBeams];   // twin: the page of its own that a child gets, or -1
   uint64_t goes_on;                           // beams that have a child
 };
 
@@ -73,17 +74,24 @@ __global__ void __launch_bounds__(kReorderCols) reorder_count(const __grid_const
   __syncthreads();
   load_tile(a, set, s, first, tile);          // (a thread reads its own column alone)
   bool bad = false;
-  const int n = __popcll(freed_of(a, set, tile, threadIdx.x, first + threadIdx.x, bad));
+  uint64_t freed = freed_of(a, set, tile, threadIdx.x, first + threadIdx.x, bad);
   if (bad) atomicOr(&refused, 2);
+  // the tile's freed pages, by column and beam
   __shared__ int sum[kReorderCols / 32];
-  const int w = __reduce_add_sync(0xffffffffu, n);
-  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = w;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int all = 0;
-    for (int i = 0; i < kReorderCols / 32; ++i) all += sum[i];
-    a.count[(int64_t)s * a.tiles + blockIdx.x] = refused != 0 ? -refused : all;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, own = __popcll(freed);
+  int at = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += u;
   }
+  if (lane == 31) sum[warp] = at;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) at += sum[w];
+  const int64_t entry = (int64_t)s * a.tiles + blockIdx.x;
+  int32_t* list = a.freed + entry * (a.beams * kReorderCols);
+  if (threadIdx.x == kReorderCols - 1) a.count[entry] = refused != 0 ? -refused : at;
+  for (at -= own; freed != 0; freed &= freed - 1) list[at++] = tile[(__ffsll((long long)freed) - 1) * kReorderCols + threadIdx.x];
 }
 
 // Inclusive sum over the CTA's threads; `all`: of all of them.
@@ -107,6 +115,7 @@ __device__ __forceinline__ int scan(int x, int* warp_sum, int& all) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) reorder_plan(const __grid_constant__ ReorderArgs a) {
+  extern __shared__ int32_t before_sm[];      // freed pages before every (set, tile), where they fit
   __shared__ int warp_sum[kPlanThreads / 32];
   __shared__ int bad;                         // the first refused request, the kind of its fault in the low two bits
   const int tid = threadIdx.x, n = a.batch * a.beams;
@@ -127,7 +136,10 @@ __global__ void __launch_bounds__(kPlanThreads) reorder_plan(const __grid_consta
     }
     int all;
     const int upto = scan(c, warp_sum, all);
-    if (i < entries) a.count[i] = freed + upto - c;
+    if (i < entries) {
+      a.count[i] = freed + upto - c;
+      if (entries <= kPlanEntries) before_sm[i] = freed + upto - c;
+    }
     freed += all;
   }
   __syncthreads();
@@ -178,10 +190,23 @@ __global__ void __launch_bounds__(kPlanThreads) reorder_plan(const __grid_consta
     bool twin = false;
     for (int j = set0; j < r && !twin; ++j) twin = a.parents[j] == p;
     const int rest = (int)(len[i] % a.P);
+    int32_t page = -1;
     if (twin && rest != 0) {
-      const int column = blocks_of(len[i], a.P) - 1;
-      a.copy[at++] = ReorderCopy{r, column, a.tables[((int64_t)set0 + p) * a.max_blocks + column], rest};
+      const int column = blocks_of(len[i], a.P) - 1, c = at++;
+      if (c < freed) {
+        // the c-th freed page: of the last (set, tile) with at most c before it
+        int64_t lo = 0, hi = entries;
+        while (hi - lo > 1) {
+          const int64_t mid = (lo + hi) >> 1;
+          if ((entries <= kPlanEntries ? before_sm[mid] : a.count[mid]) <= c) lo = mid; else hi = mid;
+        }
+        page = a.freed[lo * (a.beams * kReorderCols) + (c - (entries <= kPlanEntries ? before_sm[lo] : a.count[lo]))];
+      } else {
+        page = a.free_pages[head - freed + c];
+      }
+      a.copy[c] = ReorderCopy{a.tables[((int64_t)set0 + p) * a.max_blocks + column], page, rest, 0};
     }
+    a.twin[r] = page;
   }
   __syncthreads();                            // every length is read: they may be written over
 #pragma unroll
@@ -193,63 +218,53 @@ __global__ void __launch_bounds__(kPlanThreads) reorder_plan(const __grid_consta
   }
 }
 
-__global__ void __launch_bounds__(kReorderCols) reorder_tables(const __grid_constant__ ReorderArgs a) {
+// The first `table_ctas` CTAs take (set, tile)s: the children's entries, and the tile's freed pages into the queue.  The others take
+// units of the copies, one copy's rows in one layer of K or V: 16 bytes per thread and turn, heads and rows in the pool's
+// own strides.
+__global__ void __launch_bounds__(kCopyThreads) reorder_apply(const __grid_constant__ ReorderArgs a, int table_ctas) {
   extern __shared__ int32_t tile[];
   __shared__ Set set;
-  __shared__ int sum[kReorderCols / 32];
-  const int s = blockIdx.y, first = blockIdx.x * kReorderCols, x = threadIdx.x, column = first + x;
-  wait_for_earlier_kernels();
-  let_later_kernels_start();
-  const ReorderPlan plan = *a.plan;
-  if (plan.bad) return;
-  if (x == 0) set.goes_on = 0;
-  __syncthreads();
-  if (x < a.beams) {
-    const int p = a.parent_of[s * a.beams + x];
-    set.parent[x] = p;
-    set.blocks[x] = a.blocks[s * a.beams + x];
-    atomicOr(reinterpret_cast<unsigned long long*>(&set.goes_on), 1ull << p);
-  }
-  __syncthreads();
-  load_tile(a, set, s, first, tile);
-  bool bad = false;
-  uint64_t freed = freed_of(a, set, tile, x, column, bad);
-  int at = __popcll(freed);
-  const int lane = x & 31, warp = x >> 5;
-  const int own = at;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, at, o);
-    if (lane >= o) at += u;
-  }
-  if (lane == 31) sum[warp] = at;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) at += sum[w];
-  int64_t to = plan.head - plan.freed + a.count[(int64_t)s * a.tiles + blockIdx.x] + at - own;
-  for (; freed != 0; freed &= freed - 1) a.free_pages[to++] = tile[(__ffsll((long long)freed) - 1) * kReorderCols + x];
-  for (int j = 0; j < a.beams; ++j) {
-    const int p = set.parent[j];
-    if (column < set.blocks[p]) a.tables_out[((int64_t)s * a.beams + j) * a.max_blocks + column] = tile[p * kReorderCols + x];
-  }
-}
-
-// A unit is one copy's rows in one layer of K or V: 16 bytes per thread and turn, heads and rows in the pool's own strides.
-__global__ void __launch_bounds__(kCopyThreads) reorder_copy(const __grid_constant__ ReorderArgs a) {
   wait_for_earlier_kernels();
   const ReorderPlan plan = *a.plan;
   if (plan.bad) return;
+  if ((int)blockIdx.x < table_ctas) {
+    const int64_t entries = (int64_t)a.batch * a.tiles;
+    for (int64_t entry = blockIdx.x; entry < entries; entry += table_ctas) {
+      const int s = (int)(entry / a.tiles), first = (int)(entry - (int64_t)s * a.tiles) * kReorderCols;
+      __syncthreads();                        // (the last tile is done with)
+      if (threadIdx.x < a.beams) {
+        set.parent[threadIdx.x] = a.parent_of[s * a.beams + threadIdx.x];
+        set.blocks[threadIdx.x] = a.blocks[s * a.beams + threadIdx.x];
+        set.twin[threadIdx.x] = a.twin[s * a.beams + threadIdx.x];
+      }
+      __syncthreads();
+      // rows by halves of the CTA; all of a tile is read before any of it is written (the tables may be updated in place)
+      const int x = threadIdx.x & (kReorderCols - 1), k0 = threadIdx.x / kReorderCols, column = first + x;
+      for (int k = k0; k < a.beams; k += kCopyThreads / kReorderCols)
+        if (column < set.blocks[k]) tile[k * kReorderCols + x] = a.tables[((int64_t)s * a.beams + k) * a.max_blocks + column];
+      __syncthreads();
+      for (int j = k0; j < a.beams; j += kCopyThreads / kReorderCols) {
+        const int p = set.parent[j], n = set.blocks[p];
+        if (column < n)
+          a.tables_out[((int64_t)s * a.beams + j) * a.max_blocks + column] =
+              column == n - 1 && set.twin[j] >= 0 ? set.twin[j] : tile[p * kReorderCols + x];
+      }
+      const int before = a.count[entry], upto = entry + 1 < entries ? a.count[entry + 1] : plan.freed;
+      const int32_t* list = a.freed + entry * (a.beams * kReorderCols);
+      for (int i = before + threadIdx.x; i < upto; i += kCopyThreads) a.free_pages[plan.head - plan.freed + i] = list[i - before];
+    }
+    return;
+  }
   const int64_t units = (int64_t)plan.copies * a.n_layers * 2;
   const int chunks = a.row_bytes / 16;
   // consecutive chunks are consecutive memory: rows inside heads or heads inside rows
   const bool heads_inside = a.head_stride < a.row_stride;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int64_t u = blockIdx.x - table_ctas; u < units; u += gridDim.x - table_ctas) {
     const int c = (int)(u / (a.n_layers * 2)), part = (int)(u - (int64_t)c * a.n_layers * 2);
     const ReorderCopy y = a.copy[c];
-    const int32_t page = a.free_pages[plan.head - plan.freed + c];
-    if (part == 0 && threadIdx.x == 0) a.tables_out[(int64_t)y.row * a.max_blocks + y.column] = page;
     uint8_t* base = ((part & 1) ? a.v : a.k) + (part >> 1) * a.layer_stride;
     const uint8_t* from = base + y.source * a.page_stride;
-    uint8_t* to = base + page * a.page_stride;
+    uint8_t* to = base + y.page * a.page_stride;
     const int inner = heads_inside ? a.h_kv : y.rows, n = a.h_kv * y.rows * chunks;
     for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kCopyThreads) {
       uint4 v[4];
@@ -271,38 +286,38 @@ __global__ void __launch_bounds__(kCopyThreads) reorder_copy(const __grid_consta
 
 }  // namespace
 
-size_t beam_reorder_ws(int32_t batch, int32_t beams, int32_t tiles, size_t off[5]) {
+size_t beam_reorder_ws(int32_t batch, int32_t beams, int32_t tiles, size_t off[7]) {
   auto up = [](size_t x) { return (x + KVSEL_WS_ALIGN - 1) / KVSEL_WS_ALIGN * KVSEL_WS_ALIGN; };
   const size_t n = (size_t)batch * beams;
   off[0] = sizeof(DeviceError);                                // the plan
   off[1] = off[0] + KVSEL_WS_ALIGN;                            // parents
   off[2] = up(off[1] + sizeof(int32_t) * n);                   // pages held
-  off[3] = up(off[2] + sizeof(int32_t) * n);                   // copies
-  off[4] = up(off[3] + sizeof(ReorderCopy) * n);               // counts
-  return up(off[4] + sizeof(int32_t) * (size_t)batch * tiles);
+  off[3] = up(off[2] + sizeof(int32_t) * n);                   // twins' pages
+  off[4] = up(off[3] + sizeof(int32_t) * n);                   // copies
+  off[5] = up(off[4] + sizeof(ReorderCopy) * n);               // counts
+  off[6] = up(off[5] + sizeof(int32_t) * (size_t)batch * tiles);                        // freed pages by (set, tile)
+  return up(off[6] + sizeof(int32_t) * n * (size_t)tiles * kReorderCols);
 }
 
 kvsel_status launch_beam_reorder(const ReorderArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(int32_t) * (size_t)a.beams * kReorderCols;
-  const dim3 grid((unsigned)a.tiles, (unsigned)a.batch);
+  const int64_t entries = (int64_t)a.batch * a.tiles;
   kvsel_status st;
   {
     TraceScope ts("reorder_count", s);
-    if ((st = launch_after(reorder_count, grid, kReorderCols, smem, s, a)) != KVSEL_OK) return st;
+    if ((st = launch_after(reorder_count, dim3((unsigned)a.tiles, (unsigned)a.batch), kReorderCols, smem, s, a)) != KVSEL_OK) return st;
   }
   {
     TraceScope ts("reorder_plan", s);
-    if ((st = launch_after(reorder_plan, dim3(1), kPlanThreads, 0, s, a)) != KVSEL_OK) return st;
+    const size_t sums = entries <= kPlanEntries ? sizeof(int32_t) * (size_t)entries : 0;
+    if ((st = launch_after(reorder_plan, dim3(1), kPlanThreads, sums, s, a)) != KVSEL_OK) return st;
   }
-  {
-    TraceScope ts("reorder_tables", s);
-    if ((st = launch_after(reorder_tables, grid, kReorderCols, smem, s, a)) != KVSEL_OK) return st;
-  }
-  TraceScope ts("reorder_copy", s);
-  const int64_t resident = resident_ctas((const void*)reorder_copy, kCopyThreads, 0);
+  TraceScope ts("reorder_apply", s);
+  const int64_t resident = resident_ctas((const void*)reorder_apply, kCopyThreads, smem);
   if (resident <= 0) return KVSEL_ERR_CUDA;
-  const int64_t most = (int64_t)a.batch * (a.beams - 1) * a.n_layers * 2;      // every set keeps a beam
-  return launch_after(reorder_copy, dim3((unsigned)std::max<int64_t>(1, std::min(resident, most))), kCopyThreads, 0, s, a);
+  // (every set keeps a beam)
+  const int64_t units = (int64_t)a.batch * (a.beams - 1) * a.n_layers * 2, table_ctas = std::min(entries, resident);
+  return launch_after(reorder_apply, dim3((unsigned)(table_ctas + std::min(resident, units))), kCopyThreads, smem, s, a, (int)table_ctas);
 }
 
 }  // namespace kvsel
