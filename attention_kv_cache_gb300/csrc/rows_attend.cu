@@ -11,7 +11,8 @@
 namespace kvsel {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;            // (256 for few jobs and items: what the plan costs is latency)
+constexpr int kPlanItems = 4096;              // items whose first steps the plan keeps in shared memory
 
 // Inclusive sum over the CTA's threads; `all`: of all of them.
 __device__ int64_t plan_scan(int64_t x, int64_t* warp_sum, int64_t& all) {
@@ -26,7 +27,7 @@ __device__ int64_t plan_scan(int64_t x, int64_t* warp_sum, int64_t& all) {
   __syncthreads();
   int64_t before = 0;
   all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     all += warp_sum[w];
   }
@@ -42,22 +43,28 @@ __device__ __forceinline__ int find_job(const int32_t* first, int n, int x) {
   return lo;
 }
 
-// Steps of the items before each, all steps, and where the CTAs' shares begin.
-__device__ void finish_plan(const RowsArgs& a, int n_items, int64_t* warp_sum) {
+// The items, `make(i)` for each, with the steps of the items before it; then all steps, and where the CTAs' shares begin.
+template <typename Make>
+__device__ __forceinline__ void put_items(const RowsArgs& a, int n_items, int64_t* warp_sum, int32_t* step_sm, Make make) {
   int64_t steps = 0;
-  for (int i0 = 0; i0 < n_items; i0 += kPlanThreads) {
+  for (int i0 = 0; i0 < n_items; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
-    const int64_t s = i < n_items ? a.items[i].steps : 0;
+    RowsItem it = {};
+    if (i < n_items) it = make(i);
     int64_t all;
-    const int64_t upto = plan_scan(s, warp_sum, all);
-    if (i < n_items) a.items[i].step0 = (int32_t)(steps + upto - s);
+    const int64_t upto = plan_scan(it.steps, warp_sum, all);
+    if (i < n_items) {
+      it.step0 = (int32_t)(steps + upto - it.steps);
+      a.items[i] = it;
+      if (i < kPlanItems) step_sm[i] = it.step0;
+    }
     steps += all;
   }
   __syncthreads();
   const int64_t W = steps * a.h_kv;
   const int N = (int)min((int64_t)a.grid, W);
   if (threadIdx.x == 0) *a.plan = RowsPlan{steps, n_items, N};
-  for (int i = threadIdx.x; i < a.grid; i += kPlanThreads) {
+  for (int i = threadIdx.x; i < a.grid; i += blockDim.x) {
     RowsStart st = {};
     if (i < N) {
       const int64_t x = lane_begin64(i, W, N);
@@ -65,7 +72,7 @@ __device__ void finish_plan(const RowsArgs& a, int n_items, int64_t* warp_sum) {
       int lo = 0, hi = n_items;               // the last item that begins at or before y (items without steps come before it)
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.items[mid].step0 <= y) lo = mid; else hi = mid;
+        if ((n_items <= kPlanItems ? step_sm[mid] : a.items[mid].step0) <= y) lo = mid; else hi = mid;
       }
       st.steps = lane_begin64(i + 1, W, N) - x;
       st.g = g;
@@ -80,14 +87,14 @@ __device__ void finish_plan(const RowsArgs& a, int n_items, int64_t* warp_sum) {
 
 // Items of a chunk call: the rows of every request's new tokens, 256 at a time.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant__ RowsArgs a) {
-  extern __shared__ int32_t first[];          // [batch + 1] items before each request, then [batch] its tokens
+  extern __shared__ int32_t first[];          // [batch + 1] items before each request, [batch] its tokens, then the items' steps
   __shared__ int64_t warp_sum[kPlanThreads / 32];
   int32_t* n_tok = first + a.jobs + 1;
   wait_for_earlier_kernels();
   let_later_kernels_start();
   const int64_t cap = (int64_t)a.max_blocks * a.P;
   int64_t items = 0;
-  for (int b0 = 0; b0 < a.jobs; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.jobs; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     int64_t n = 0;
     if (b < a.jobs) {
@@ -108,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant
   const int n_items = (int)min(items, (int64_t)a.max_items);
   if (threadIdx.x == 0) first[a.jobs] = n_items;
   __syncthreads();
-  for (int i = threadIdx.x; i < n_items; i += kPlanThreads) {
+  put_items(a, n_items, warp_sum, n_tok + a.jobs, [&](int i) {
     const int b = find_job(first, a.jobs, i);
     RowsItem it = {};
     const int n = n_tok[b];
@@ -124,10 +131,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant
     it.full_lo = a.window > 0 ? max(0, p1 + 1 - a.window) : 0;
     it.k0 = it.lo / kTileKeys * kTileKeys;
     it.steps = (it.hi - it.k0 + kTileKeys - 1) / kTileKeys;
-    a.items[i] = it;
-  }
-  __syncthreads();
-  finish_plan(a, n_items, warp_sum);
+    return it;
+  });
 }
 
 // Shared whole pages of group j, 0 where they cannot be shared; all threads of the CTA call it.
@@ -155,7 +160,7 @@ __device__ bool groups_ok(const RowsArgs& a) {
 // Of the requests (dealt to the CTAs from the second on): their tables behind the shared pages, and their rows left.
 // The first CTA makes the items: the rows of every group's requests, 256 at a time, over the shared rows.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constant__ RowsArgs a) {
-  extern __shared__ int32_t first[];          // [groups + 1] items before each group, then [groups] its shared rows
+  extern __shared__ int32_t first[];          // [groups + 1] items before each group, [groups] its shared rows, then the items' steps
   __shared__ int64_t warp_sum[kPlanThreads / 32];
   int32_t* rows_of = first + a.jobs + 1;
   wait_for_earlier_kernels();
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
       const int64_t len = a.lens[r], left = len - (int64_t)skip * a.P;
       if (threadIdx.x == 0) a.own_lens[r] = left;
       const int n = left > 0 && len <= (int64_t)a.max_blocks * a.P ? (int)((left + a.P - 1) / a.P) : 0;
-      for (int c = threadIdx.x; c < n; c += kPlanThreads)
+      for (int c = threadIdx.x; c < n; c += blockDim.x)
         a.own_tables[(int64_t)r * a.max_blocks + c] = a.tables[(int64_t)r * a.max_blocks + skip + c];
     }
     return;
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
   const int jobs = ok ? a.jobs : 1;
   // groups, a warp each: their shared rows; then their items
   const int64_t cap = (int64_t)a.max_blocks * a.P;
-  for (int j = threadIdx.x >> 5; j < jobs; j += kPlanThreads / 32) {
+  for (int j = threadIdx.x >> 5; j < jobs; j += blockDim.x / 32) {
     const int64_t r0 = ok ? a.first[j] : 0, r1 = ok ? a.first[j + 1] : a.batch, shared = ok ? a.shared[j] : 0;
     bool low = shared < 0, over = false;
     for (int64_t r = r0 + (threadIdx.x & 31); r < r1; r += 32) {
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
   }
   __syncthreads();
   int64_t items = 0;
-  for (int j0 = 0; j0 < jobs; j0 += kPlanThreads) {
+  for (int j0 = 0; j0 < jobs; j0 += blockDim.x) {
     const int j = j0 + threadIdx.x;
     const int64_t n = j < jobs ? (ok ? a.first[j + 1] - a.first[j] : a.batch) : 0;
     const int64_t t = (n * a.G + kItemRows - 1) / kItemRows;
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
   const int n_items = (int)items;
   if (threadIdx.x == 0) first[jobs] = n_items;
   __syncthreads();
-  for (int i = threadIdx.x; i < n_items; i += kPlanThreads) {
+  put_items(a, n_items, warp_sum, rows_of + a.jobs, [&](int i) {
     const int j = find_job(first, jobs, i);
     const int64_t r0 = ok ? a.first[j] : 0, r1 = ok ? a.first[j + 1] : a.batch;
     RowsItem it = {};
@@ -233,10 +238,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
     }
     it.k0 = it.lo / kTileKeys * kTileKeys;
     it.steps = it.lo < it.hi ? (it.hi - it.k0 + kTileKeys - 1) / kTileKeys : 0;
-    a.items[i] = it;
-  }
-  __syncthreads();
-  finish_plan(a, n_items, warp_sum);
+    return it;
+  });
 }
 
 // o of an item's rows from its pieces, sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, and with a prefix from what the decode
@@ -495,12 +498,13 @@ kvsel_status launch_chunk_attend(const RowsShape& p, const RowsArgs& in, void* w
   RowsArgs a = rows_args(p, in, lay, ws);
   CUtensorMap tk, tv;
   a.box_rows = boxes(p, a.k, a.v, &tk, &tv);
-  const size_t smem = sizeof(int32_t) * (2 * (size_t)a.jobs + 1);
+  const size_t smem = sizeof(int32_t) * (2 * (size_t)a.jobs + 1 + kPlanItems);
+  const unsigned threads = a.jobs <= 256 && a.max_items <= 256 ? 256 : kPlanThreads;
   if (set_smem((const void*)chunk_plan, smem) != cudaSuccess || set_smem((const void*)var.kern, var.smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   kvsel_status st;
   {
     TraceScope ts("chunk_plan", s);
-    if ((st = launch_after(chunk_plan, dim3(1), kPlanThreads, smem, s, a)) != KVSEL_OK) return st;
+    if ((st = launch_after(chunk_plan, dim3(1), threads, smem, s, a)) != KVSEL_OK) return st;
   }
   {
     TraceScope ts("rows_attend", s);
@@ -517,12 +521,13 @@ kvsel_status launch_prefix_attend(const RowsShape& p, const PagedShape& own, con
   RowsArgs a = rows_args(p, in, lay, ws);
   CUtensorMap tk, tv;
   a.box_rows = boxes(p, a.k, a.v, &tk, &tv);
-  const size_t smem = sizeof(int32_t) * (2 * (size_t)a.jobs + 1);
+  const size_t smem = sizeof(int32_t) * (2 * (size_t)a.jobs + 1 + kPlanItems);
+  const unsigned threads = a.jobs <= 256 && a.max_items <= 256 ? 256 : kPlanThreads;
   if (set_smem((const void*)prefix_plan, smem) != cudaSuccess || set_smem((const void*)var.kern, var.smem) != cudaSuccess) return KVSEL_ERR_CUDA;
   kvsel_status st;
   {
     TraceScope ts("prefix_plan", s);
-    if ((st = launch_after(prefix_plan, dim3(1 + std::min(a.batch, 2 * a.grid)), kPlanThreads, smem, s, a)) != KVSEL_OK) return st;
+    if ((st = launch_after(prefix_plan, dim3(1 + std::min(a.batch, 2 * a.grid)), threads, smem, s, a)) != KVSEL_OK) return st;
   }
   {
     TraceScope ts("rows_attend", s);
