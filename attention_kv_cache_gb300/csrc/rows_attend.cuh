@@ -900,14 +900,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
 #pragma unroll 1
         for (int s = cur.s0; s < cur.s1; ++s, ++step) {
           if (!two && (int)(step & 1) != x) continue;
+          const int t0 = k0 + kTileKeys * s;
+          const bool within = t0 >= full_lo && t0 + kTileKeys <= full_hi, partial = rows_partial(k_lo, k_hi, full_lo, full_hi, t0);
           ok = __all_sync(0xffffffffu, rows_wait(s_full(x), n & 1, flag));
           if (!ok) break;
           ++n;
           tc_fence_after();
-          const int t0 = k0 + kTileKeys * s;
           const uint4 there = *reinterpret_cast<const uint4*>(&seen_w[(step & 7) * 4]);
-          const bool whole = t0 >= full_lo && t0 + kTileKeys <= full_hi && (there.x & there.y & there.z & there.w) == 0xffffffffu;
-          if (rows_partial(k_lo, k_hi, full_lo, full_hi, t0)) {
+          const bool whole = within && (there.x & there.y & there.z & there.w) == 0xffffffffu;
+          if (partial) {
             ok = __all_sync(0xffffffffu, rows_wait(full(2 * step + 1), use(2 * step + 1), flag));
             if (!ok) break;
             uint4 bad = *reinterpret_cast<const uint4*>(&bad_w[(step & 7) * 4]);
