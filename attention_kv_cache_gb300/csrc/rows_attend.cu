@@ -355,10 +355,11 @@ __global__ void __launch_bounds__(kItemRows) rows_join(const __grid_constant__ R
 // Whether weights are two 16-bit parts (rows_attend.cuh says why).
 bool split_weights(const RowsShape& p) { return p.prefix != 0 && p.cache_dtype != KVSEL_DTYPE_E4M3; }
 
-RowsVariant variant(const RowsShape& p) {
+// (scored: with a cap or a bias)
+RowsVariant variant(const RowsShape& p, bool scored) {
   const bool split = split_weights(p);
-  if (p.cache_dtype == KVSEL_DTYPE_E4M3) return rows_variant_e4m3(p.d, split);
-  return p.dtype == KVSEL_DTYPE_F16 ? rows_variant_f16(p.d, split) : rows_variant_bf16(p.d, split);
+  if (p.cache_dtype == KVSEL_DTYPE_E4M3) return rows_variant_e4m3(p.d, split, scored);
+  return p.dtype == KVSEL_DTYPE_F16 ? rows_variant_f16(p.d, split, scored) : rows_variant_bf16(p.d, split, scored);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -408,7 +409,7 @@ struct Layout {
   size_t plan, starts, items, own_lens, own_tables, own_o, own_lse, ml, part, total;
 };
 bool layout(const RowsShape& p, size_t front, Layout* out) {
-  const RowsVariant v = variant(p);
+  const RowsVariant v = variant(p, true);      // (all variants: one CTA per SM)
   const int64_t grid = resident_ctas((const void*)v.kern, kRowsThreads, v.smem);     // one per SM
   if (grid <= 0) return false;
   Layout& o = *out;
@@ -494,7 +495,7 @@ size_t rows_ws(const RowsShape& p, size_t front) {
 kvsel_status launch_chunk_attend(const RowsShape& p, const RowsArgs& in, void* ws, cudaStream_t s) {
   Layout lay;
   if (!layout(p, 0, &lay)) return KVSEL_ERR_CUDA;
-  const RowsVariant var = variant(p);
+  const RowsVariant var = variant(p, p.softcap != 0.f || in.slopes != nullptr);
   RowsArgs a = rows_args(p, in, lay, ws);
   CUtensorMap tk, tv;
   a.box_rows = boxes(p, a.k, a.v, &tk, &tv);
@@ -517,7 +518,7 @@ kvsel_status launch_chunk_attend(const RowsShape& p, const RowsArgs& in, void* w
 kvsel_status launch_prefix_attend(const RowsShape& p, const PagedShape& own, const RowsArgs& in, void* ws, size_t front, cudaStream_t s) {
   Layout lay;
   if (!layout(p, front, &lay)) return KVSEL_ERR_CUDA;
-  const RowsVariant var = variant(p);
+  const RowsVariant var = variant(p, p.softcap != 0.f || in.slopes != nullptr);
   RowsArgs a = rows_args(p, in, lay, ws);
   CUtensorMap tk, tv;
   a.box_rows = boxes(p, a.k, a.v, &tk, &tv);

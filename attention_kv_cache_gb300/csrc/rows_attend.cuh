@@ -197,6 +197,23 @@ __device__ __forceinline__ float rows_max(const float* v) {
     for (int i = 0; i < k; ++i) m[i] = fmaxf(m[i], m[i + k]);
   return m[0];
 }
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float rows_min(const float* v) {
+  float m[N / 16];
+#pragma unroll
+  for (int k = 0; k < N / 16; ++k) {
+    const float* c = v + 16 * k;
+    m[k] = min3(min3(min3(c[0], c[1], c[2]), c[3], c[4]), min3(min3(c[5], c[6], c[7]), c[8], c[9]), min3(min3(c[10], c[11], c[12]), c[13], c[14]));
+    m[k] = fminf(m[k], c[15]);
+  }
+  static_assert(N == 64, "four parts");
+  return min3(fminf(m[0], m[1]), m[2], m[3]);
+}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
@@ -252,6 +269,17 @@ struct RowsScore {
   float sc, icap, cap2, slope;        // sc: scale with log2 e; icap: scale / cap
   bool capped, biased;                // biased: with a bias, or a factor that is not positive
 };
+// With the bias, and the factor `by` on what stands there.
+template <int N>
+__device__ __forceinline__ void rows_bias(float* z, float by, float slope, float d0) {
+  const float2 s2 = make_float2(by, by), sl = make_float2(slope, slope), dd = make_float2(d0, d0 + 1.f);
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 y = __ffma2_rn(sl, __fadd2_rn(dd, make_float2((float)c, (float)c)), __fmul2_rn(make_float2(z[c], z[c + 1]), s2));
+    z[c] = y.x;
+    z[c + 1] = y.y;
+  }
+}
 // N products as their scores: capped, biased (d0: distance of the first key to the row's own), and those not seen (by 32, where not
 // all are) as -inf.
 template <int N>
@@ -283,18 +311,37 @@ __device__ __forceinline__ void rows_scores(float* z, const RowsScore& k, float 
     }
   }
   if (k.biased) {                                 // (and where the factor is not positive: the bias is 0 then)
-    const float2 s2 = make_float2(k.capped ? 1.f : k.sc, k.capped ? 1.f : k.sc), sl = make_float2(k.slope, k.slope);
-    const float2 dd = make_float2(d0, d0 + 1.f);
-#pragma unroll
-    for (int c = 0; c < N; c += 2) {
-      const float2 y = __ffma2_rn(sl, __fadd2_rn(dd, make_float2((float)c, (float)c)), __fmul2_rn(make_float2(z[c], z[c + 1]), s2));
-      z[c] = y.x;
-      z[c + 1] = y.y;
-    }
+    rows_bias<N>(z, k.capped ? 1.f : k.sc, k.slope, d0);
   }
   if (!whole) {
 #pragma unroll
     for (int c = 0; c < N; ++c) z[c] = (see[c / 32] >> (c & 31)) & 1u ? z[c] : -INFINITY;
+  }
+}
+// What a cap does to products that stay far below it (|x| < 1/4 of it, the series of tanh_fast), but for the factor scale log2 e:
+// z (1 + w (a1 + w (a2 + w a3))) with w = z^2 and the powers of 1 / cap^2 in the constants.
+struct RowsSeries {
+  float a1, a2, a3;
+  __device__ explicit RowsSeries(float icap) {
+    const float i2 = icap * icap;
+    a1 = -1.f / 3.f * i2;
+    a2 = 2.f / 15.f * i2 * i2;
+    a3 = -17.f / 315.f * i2 * i2 * i2;
+  }
+  __device__ float operator()(float z) const {
+    const float w = z * z;
+    return fmaf(z * w, fmaf(w, fmaf(w, a3, a2), a1), z);
+  }
+};
+template <int N>
+__device__ __forceinline__ void rows_series(float* z, const RowsSeries& k) {
+  const float2 a1 = make_float2(k.a1, k.a1), a2 = make_float2(k.a2, k.a2), a3 = make_float2(k.a3, k.a3);
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 x = make_float2(z[c], z[c + 1]), w = __fmul2_rn(x, x);
+    const float2 y = __ffma2_rn(__fmul2_rn(x, w), __ffma2_rn(w, __ffma2_rn(w, a3, a2), a1), x);
+    z[c] = y.x;
+    z[c + 1] = y.y;
   }
 }
 // The same for a step's 128 keys, in TMEM.
@@ -314,7 +361,7 @@ __device__ __forceinline__ void rows_scores_tmem(uint32_t s, const RowsScore& k,
 // One step of a thread's row: weights of its keys, written over S: all 128 of the step (COPIES 1), or the 32 of copy `copy` with
 // zeros in the other copies' places; updates the offset m, mo, the sum l; returns the factor on what O holds.  The scores
 // of all 128 are in TMEM as they are compared, but for the factor `mul`; a copy forms its own here.
-template <int KIND, bool SPLIT, int COPIES>
+template <int KIND, bool SPLIT, bool SCORED, int COPIES>
 __device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, const RowsScore& k, float d0, bool whole, uint32_t see, float& m, float& mo,
                                            float& l) {
   using namespace sm100;
@@ -352,10 +399,40 @@ __device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, cons
     reg_tie64(rw);
     float* v = reinterpret_cast<float*>(rv);
     float* u = reinterpret_cast<float*>(rw);
-    offset(fmaxf(rows_max<64>(u), rows_max<64>(v)) * mul);
-    sum = rows_weights<KIND, false, 64>(u, mul, kShift - mo, rw, nullptr);
+    float top = fmaxf(rows_max<64>(u), rows_max<64>(v)), by = mul;
+    if constexpr (SCORED) {
+      if (!whole) {                                     // not yet as they are compared (`whole`: they are)
+        bool fit = true;
+        if (k.capped) {
+          // (scores far below the cap are the rule; constants of the series stay finite)
+          const float low = fminf(rows_min<64>(u), rows_min<64>(v));
+          fit = __all_sync(0xffffffffu, fmaxf(top, -low) * k.icap < 0.25f && k.icap < 0x1p20f && k.sc > 0.f);
+          if (fit) {
+            const RowsSeries f(k.icap);
+            rows_series<64>(u, f);
+            rows_series<64>(v, f);
+            top = f(top);                               // (the series rises with its argument)
+            by = k.sc;
+          }
+        }
+        if (!fit) {
+          rows_scores_tmem(s, k, d0, true, make_uint4(0, 0, 0, 0));
+          tmem_ld64_async(s + 64, rv);
+          tmem_ld64_async(s, rw);
+          tmem_wait_ld64(rv);
+          reg_tie64(rw);
+        } else if (k.biased) {
+          rows_bias<64>(u, k.sc, k.slope, d0);
+          rows_bias<64>(v, k.sc, k.slope, d0 + 64.f);
+          by = 1.f;
+        }
+        if (!fit || k.biased) top = fmaxf(rows_max<64>(u), rows_max<64>(v));
+      }
+    }
+    offset(top * by);
+    sum = rows_weights<KIND, false, 64>(u, by, kShift - mo, rw, nullptr);
     tmem_st32(s, rw);
-    sum += rows_weights<KIND, false, 64>(v, mul, kShift - mo, rv, nullptr);
+    sum += rows_weights<KIND, false, 64>(v, by, kShift - mo, rv, nullptr);
     tmem_st32(s + 32, rv);
   } else {
     float z[32];
@@ -375,7 +452,7 @@ __device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, cons
   return alpha;
 }
 
-template <int D, int KIND, bool SPLIT>
+template <int D, int KIND, bool SPLIT, bool SCORED>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensorMap tk,
                                                                const __grid_constant__ CUtensorMap tv) {
   using namespace sm100;
@@ -886,12 +963,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
         const int low = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
         const float head_scale = a.k_scale != nullptr ? a.k_scale[cur.g] : 1.f, ksc = a.scale * head_scale * by;
         RowsScore score;
-        score.capped = a.softcap != 0.f;
+        score.capped = SCORED && a.softcap != 0.f;
         score.sc = ksc * kLog2e;
         score.icap = score.capped ? ksc / a.softcap : 0.f;
         score.cap2 = a.softcap * kLog2e;
-        score.slope = a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
-        score.biased = a.slopes != nullptr || (!score.capped && !(head_scale > 0.f));
+        score.slope = SCORED && a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
+        score.biased = (SCORED && a.slopes != nullptr) || (!score.capped && !(head_scale > 0.f));
         const bool plain = !score.capped && !score.biased;
         const float mul = plain ? score.sc : 1.f;
         bool begun = false;
@@ -934,10 +1011,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
             float alpha;
             if (small) {
               const uint32_t see = copy == 0 ? word[0] : copy == 1 ? word[1] : copy == 2 ? word[2] : word[3];
-              alpha = rows_step<KIND, SPLIT, 4>(tm + kSCol, copy, mul, score, (float)(t0 + 32 * copy - pos), whole, see, m, mo, l);
+              alpha = rows_step<KIND, SPLIT, SCORED, 4>(tm + kSCol, copy, mul, score, (float)(t0 + 32 * copy - pos), whole, see, m, mo, l);
             } else {
-              if (!whole || !plain) rows_scores_tmem(tm + kSCol, score, (float)(t0 - pos), whole, make_uint4(word[0], word[1], word[2], word[3]));
-              alpha = rows_step<KIND, SPLIT, 1>(tm + kSCol, 0, mul, score, 0.f, true, 0u, m, mo, l);
+              // with a mask they are brought to what is compared in TMEM, else in the registers that hold them for the softmax
+              const bool before = !whole || (!plain && (SPLIT || !SCORED));
+              if (before) rows_scores_tmem(tm + kSCol, score, (float)(t0 - pos), whole, make_uint4(word[0], word[1], word[2], word[3]));
+              alpha = rows_step<KIND, SPLIT, SCORED, 1>(tm + kSCol, 0, mul, score, (float)(t0 - pos), before || plain, 0u, m, mo, l);
             }
             // O of the tile's step before is final (this step's S was issued behind its P V)
             if ((had || begun) && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -1093,14 +1172,17 @@ struct RowsVariant {
   RowsKernel kern;
   size_t smem;
 };
+// (SPLIT kernels wait for HBM: one for all scores)
 template <int D, int KIND>
-RowsVariant rows_variant(bool split) {
-  if constexpr (KIND == kE4m3) return {rows_attend<D, KIND, false>, rows_smem<D, KIND>()};
-  else return {split ? rows_attend<D, KIND, true> : rows_attend<D, KIND, false>, rows_smem<D, KIND>()};
+RowsVariant rows_variant(bool split, bool scored) {
+  RowsKernel kern = scored ? rows_attend<D, KIND, false, true> : rows_attend<D, KIND, false, false>;
+  if constexpr (KIND != kE4m3)
+    if (split) kern = rows_attend<D, KIND, true, true>;
+  return {kern, rows_smem<D, KIND>()};
 }
 // The kernels of a pool type, each in a file of its own (rows_attend_*.cu).
-RowsVariant rows_variant_bf16(int d, bool split);
-RowsVariant rows_variant_f16(int d, bool split);
-RowsVariant rows_variant_e4m3(int d, bool split);
+RowsVariant rows_variant_bf16(int d, bool split, bool scored);
+RowsVariant rows_variant_f16(int d, bool split, bool scored);
+RowsVariant rows_variant_e4m3(int d, bool split, bool scored);
 
 }  // namespace kvsel

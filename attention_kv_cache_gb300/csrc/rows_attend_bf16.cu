@@ -3,6 +3,8 @@
 
 namespace kvsel {
 
-RowsVariant rows_variant_bf16(int d, bool split) { return d == 64 ? rows_variant<64, kBf16>(split) : rows_variant<128, kBf16>(split); }
+RowsVariant rows_variant_bf16(int d, bool split, bool scored) {
+  return d == 64 ? rows_variant<64, kBf16>(split, scored) : rows_variant<128, kBf16>(split, scored);
+}
 
 }  // namespace kvsel

@@ -3,6 +3,8 @@
 
 namespace kvsel {
 
-RowsVariant rows_variant_e4m3(int d, bool split) { return d == 64 ? rows_variant<64, kE4m3>(split) : rows_variant<128, kE4m3>(split); }
+RowsVariant rows_variant_e4m3(int d, bool split, bool scored) {
+  return d == 64 ? rows_variant<64, kE4m3>(split, scored) : rows_variant<128, kE4m3>(split, scored);
+}
 
 }  // namespace kvsel
