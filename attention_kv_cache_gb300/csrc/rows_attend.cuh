@@ -393,12 +393,33 @@ __device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, cons
     tmem_st32(s, hi);
   } else if constexpr (COPIES == 1) {
     uint32_t rv[64], rw[64];
+    float* v = reinterpret_cast<float*>(rv);
+    float* u = reinterpret_cast<float*>(rw);
+    if constexpr (KIND == kBf16 && !SCORED) {
+      // No weight is above their sum: the largest score is looked for only where a row has no offset yet or the sum passes what
+      // the lag allows (both rare), and the weights are formed again.
+      bool look = __any_sync(0xffffffffu, m == -INFINITY);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        tmem_ld64_async(s + 64, rv);
+        tmem_ld64_async(s, rw);
+        tmem_wait_ld64(rv);
+        reg_tie64(rw);
+        if (look) offset(fmaxf(rows_max<64>(u), rows_max<64>(v)) * mul);
+        sum = rows_weights<KIND, false, 64>(u, mul, kShift - mo, rw, nullptr);
+        sum += rows_weights<KIND, false, 64>(v, mul, kShift - mo, rv, nullptr);
+        if (look || !__any_sync(0xffffffffu, sum > 1.f)) break;
+        look = true;
+      }
+      tmem_st32(s, rw);
+      tmem_st32(s + 32, rv);
+      l = l * alpha + sum;
+      return alpha;
+    }
     tmem_ld64_async(s + 64, rv);
     tmem_ld64_async(s, rw);
     tmem_wait_ld64(rv);                                 // one wait covers both loads
     reg_tie64(rw);
-    float* v = reinterpret_cast<float*>(rv);
-    float* u = reinterpret_cast<float*>(rw);
     float top = fmaxf(rows_max<64>(u), rows_max<64>(v)), by = mul;
     if constexpr (SCORED) {
       if (!whole) {                                     // not yet as they are compared (`whole`: they are)
