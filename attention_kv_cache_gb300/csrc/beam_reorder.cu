@@ -9,7 +9,8 @@
 // Bound: the copies (rows x layers x heads, read and written); small calls by the chain of launches.  Three of them, since
 // a page's place in the queue needs the count of all sets' freed pages before it: the freed pages by (set, 128 columns); one
 // CTA's sums, checks, lengths and list of copies with the pages they take; tables, queue and copies.  Each starts while the one
-// before it drains.  A refused call stops at the second: nothing of its outputs is written.
+// before it drains.  A refused call stops at the second: nothing of its outputs is written.  (One set of 4: 12 us, 24 of 5: 14;
+// 64 of 8 with 378 MB to read and write: 77 us, 4.9 TB/s.)
 #include <algorithm>
 
 #include "beam.cuh"

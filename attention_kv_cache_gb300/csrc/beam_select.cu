@@ -12,6 +12,10 @@
 // ones) they are taken 256 at a time.  Tokens at -inf, of which constrained decoding has most of a vocabulary, are left out and
 // fill a short list by their order.
 //
+// 64 sets of 16 beams over 128256 bf16 logits: 98 us, 2.7 TB/s; the same read alone runs at 6 TB/s.  A slice costs a warp 420
+// instructions, 13 cycles each with eight warps to a scheduler: a third of them the exponentials (without them 12 us less),
+// as much the candidates (14).  A slice ahead by cp.async, one barrier a slice or ranks by four lanes left the time as it is.
+//
 // Ties are the rule with 16-bit logits, and scores of different beams may lie within a rounding of each other, so scores are
 // formed and compared in 64 bits.  Exponentials are ex2.approx (2^-22 of each, of either sign) summed in fp32 by thread and
 // then as 64-bit whole multiples of 2^-40: the sum is off by the mean of its terms' errors and the same for equal rows,

@@ -9,23 +9,35 @@
 // Roles of the 16 warps: 0-3 and 4-7 softmax of tile A and B, a thread per row of the tile; 8-11 load K and V; 12 issues
 // the products S, 13 P V.  S = Q K^T goes to TMEM; the softmax reads it, keeps an exponent offset that moves only when a row's largest
 // score passes it by 2^lag (so O is rescaled rarely) and writes the weights over S as 16-bit values, which O += P V takes from
-// TMEM with V as it lies.
+// TMEM with V as it lies.  (bf16: the weights' sum bounds the largest of them, which is looked for only where the sum does not do.)
 //
 // An item of more than 128 rows has them in both tiles, which share every step; P V of one and S of the other are issued in
 // alternation, as the prefill kernel does.  A smaller item has its rows in both: the tiles take steps in turn, so
-// that two chains S -> softmax -> P V -> S run at once (one alone takes 5000 cycles a step, which HBM brings in 2800).  Items of
-// up to 64 (32) rows fill the tile's 128 rows with two (four) copies, which take 64 (32) keys of a step each: the softmax of
-// a step is a thread's loop over its keys, 2000 cycles for 128.  What tiles and copies hold is merged when the piece ends.
+// that two chains S -> softmax -> P V -> S run at once (one alone takes 4000 cycles a step, which HBM brings in 2800).  Items of
+// up to 32 rows fill the tile's 128 rows with four copies, which take 32 keys of a step each: the softmax of a step is a
+// thread's loop over its keys, 2000 cycles for 128.  What tiles and copies hold is merged when the piece ends.
+//
+// Bound: with full items the chain of a tile's step, 2000 cycles of softmax and as many of S and P V with the waits between them;
+// TMEM holds S and O of two tiles and no third S that could be formed meanwhile.  4096 tokens behind 12288, 32 / 8 heads
+// of 128, bf16: 798 us, 1.2 PFLOP/s, a step of both tiles in 4000 cycles where its products take 2048.  (Halves of a step told
+// of apart, to start P V early: 912; steps of 64 keys: 1127.)  With few rows HBM and the start: 16 requests of 5 tokens behind up
+// to 8191: 102 us, 2.8 TB/s.
+//
+// SCORED: kernels for capped or biased scores, which are formed in the registers that hold them for the softmax; a step with
+// a mask has them formed in TMEM first.  (8 chunks behind up to 7000 rows, 8-bit, capped, a window: 415 us when all were
+// formed in TMEM, 397 now.)
 //
 // SPLIT (the shared prefix over 16-bit pools): weights are a high and a low 16-bit part, as in the decode kernel whose results it
 // must match; the steps wait for HBM there, so the third product is free up to 128 rows.  Without it (chunks, bound by the tensor
 // cores, and 8-bit pools) a weight is rounded once, by at most 2^-8 of it over bf16 and 2^-11 over fp16 products: what the
-// outputs' own rounding is, and far below a row's in 8 bits.  (64 requests behind 32768 e4m3 rows: 200 us with the low parts, 174 without.)
+// outputs' own rounding is, and far below a row's in 8 bits.  (64 requests behind 32768 e4m3 rows take 167 us; the low parts
+// would add 26.)
 // Factors on the weights as in paged_attend.cuh: 2^-8 over bf16 and 2^13 over fp16 products; without SPLIT it is taken by the
 // exponent, whose rounding at 13 (2^-21 of a weight) is far below the weight's own.
 //
-// K and V come by cp.async, a warp per 32 rows, whole rows at a time, into the 128-byte swizzled layout of the products: any
-// page size, order and stride.  An e4m3 pool's rows pass through registers, where they become fp16.
+// K and V come into the 128-byte swizzled layout of the products, a warp per 32 rows of a step: by TMA boxes of 8 to 32 rows
+// where pages are made of such, else by cp.async, whole rows at a time: any page size, order and stride.  An e4m3 pool's rows
+// (boxes of bytes in a ring of their own, or rows by plain loads) pass through registers, where they become fp16.
 //
 // Rows that some token of the item does not see may hold anything: their scores are replaced, and where a V row in such a
 // step is not finite its bad values are zeros in shared memory (0 times infinity is no number) and are added to the rows that

@@ -280,8 +280,11 @@ class PagedDecoder:
         if beams > 1:
             self.beam = K.make_beam_reorder_desc(batch=batch // beams, beams=beams, max_blocks=max_blocks,
                                                  n_layers=n_layers, layer_stride=self.k_cache.stride(0))
-            n = max(n, K.kvsel_beam_reorder_workspace_size(self.beam))
-        self.ws = self._workspace(n)
+            # (what ``fork`` shares stands in one place, so that a captured step reads the next prompt's)
+            self.fork_indptr, self.fork_rows = torch.arange(0, batch + 1, beams, **i64), torch.zeros(batch // beams, **i64)
+            n = max(n, K.kvsel_beam_reorder_workspace_size(self.beam),
+                    K.kvsel_prefix_attend_workspace_size(self.cache, self.attend, batch // beams))
+        self.ws, self._outgrown = self._workspace(n), []
 
     def _workspace(self, n: int):
         ws = torch.zeros(n + K.WS_ALIGN, dtype=torch.uint8, device=self.device)
@@ -399,7 +402,8 @@ class PagedDecoder:
 
     def share(self, group_indptr, shared_lens):
         """From now on requests ``group_indptr[j] .. group_indptr[j + 1] - 1`` name the same pages for their first
-        ``shared_lens[j]`` rows, which a layer then reads once (int64, on the device; None: no more).  Not in a capture."""
+        ``shared_lens[j]`` rows, which a layer then reads once (int64, on the device; None: no more).  Not in a capture; a captured
+        step goes on reading the tensors that it was captured with."""
         if group_indptr is None:
             self.groups = None
             return
@@ -409,6 +413,7 @@ class PagedDecoder:
                 raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}, not ({size},) int64 on {self.lens.device}")
         need = K.kvsel_prefix_attend_workspace_size(self.cache, self.attend, n)
         if need > self.ws.numel():
+            self._outgrown.append(self.ws)         # (captured steps, and calls still running, use it)
             self.ws = self._workspace(need)
         self.groups = (group_indptr, shared_lens)
 
@@ -433,14 +438,13 @@ class PagedDecoder:
     def fork(self, stream=None):
         """Every set's beams share its first beam's pages (the others hold none, or lose them); the rows in whole pages at this
         time are what a layer then reads once for a set.  Not in a capture."""
-        self.reorder(torch.zeros((self.batch // self.beams, self.beams), dtype=torch.int32, device=self.device), stream)
         current, stream = torch.cuda.current_stream(), _torch_stream(stream)
-        with torch.cuda.stream(stream):
-            shared = self.lens[::self.beams] // self.P * self.P
-            groups = torch.arange(0, self.batch + 1, self.beams, dtype=torch.int64, device=self.device)
         if stream != current:
-            current.wait_stream(stream)
-        self.share(groups, shared)
+            stream.wait_stream(current)
+        with torch.cuda.stream(stream):            # the temporaries are that stream's too
+            self.reorder(torch.zeros((self.batch // self.beams, self.beams), dtype=torch.int32, device=self.device), stream)
+            self.fork_rows.copy_(self.lens[::self.beams] // self.P * self.P)
+        self.share(self.fork_indptr, self.fork_rows)
 
 
 class BeamSelector:
@@ -462,7 +466,7 @@ class BeamSelector:
 
     def select(self, logits, scores, ended=None, stream=None):
         """logits [sets * beams, vocab] with the rows' stride, scores [sets, beams] fp32, ended [sets, beams] uint8 or None;
-        returns (scores, parents, tokens) [sets, n_out], which the next call overwrites."""
+        returns (scores, parents, tokens) [sets, n_out], which the next call overwrites (its ``scores`` are a copy of them)."""
         if logits.shape != (self.rows, self.vocab) or logits.dtype != self.dtype or logits.stride() != (self.row_stride, 1):
             raise ValueError(f"logits are {tuple(logits.shape)} {logits.dtype} of strides {logits.stride()}, not "
                              f"({self.rows}, {self.vocab}) {self.dtype} of ({self.row_stride}, 1)")

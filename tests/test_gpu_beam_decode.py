@@ -208,3 +208,67 @@ def test_refusals(cuda):
             print(i)
     with pytest.raises(K.KvselError):
         BeamSelector(sets=2, beams=2, n_out=65, vocab=50, device=cuda)
+
+
+def graph_of(run):
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            run()
+    torch.cuda.current_stream().wait_stream(side)
+    return g
+
+
+def test_captured_step_reads_the_next_fork(cuda):
+    """A step captured behind one prompt's fork runs behind another's: shorter, so that the first one's shared rows are too many."""
+    from attention_kv_cache_gb300 import kvsel as K
+    model, beams = Model(cuda), 3
+    make = lambda: decoder(cuda, K, beams, 128, 40, max_tokens=100, beams=beams)     # noqa: E731
+    dec, tokens = make(), torch.tensor([5, 6, 7], device=cuda)
+    out = torch.empty((beams, LAYERS, HQ, D), dtype=torch.bfloat16, device=cuda)
+    text = torch.randint(0, VOCAB, (100,), generator=torch.Generator().manual_seed(2)).to(cuda)
+
+    def begin(d, n):
+        d.lens.zero_()
+        d.free_pages.copy_(torch.arange(40, dtype=torch.int32, device=cuda))
+        d.free_head.zero_()
+        chunk(d, model, text, torch.tensor([n, 0, 0], device=cuda))
+        d.fork()
+
+    begin(dec, 100)
+    before = dec.ws.data_ptr()
+    g = graph_of(lambda: out.copy_(step(dec, model, tokens)))
+    begin(dec, 41)
+    assert dec.ws.data_ptr() == before
+    g.replay()
+    torch.cuda.synchronize()
+    assert K.kvsel_read_device_error(dec.ws) == K.OK and dec.lens.tolist() == [42] * beams
+    other = make()
+    begin(other, 41)
+    assert torch.equal(out, step(other, model, tokens))
+
+
+def test_an_outgrown_workspace_stays(cuda):
+    """Sharing may need more room: the room that captured steps use is not given to anyone else."""
+    from attention_kv_cache_gb300 import kvsel as K
+    model, batch = Model(cuda), 4
+    dec, tokens = decoder(cuda, K, batch, 64, 16), torch.tensor([1, 2, 3, 4], device=cuda)
+    for _ in range(20):
+        o = step(dec, model, tokens)
+    lens = dec.lens.clone()
+    start, n = dec.ws.data_ptr(), dec.ws.numel()
+    out = torch.empty_like(o)
+    g = graph_of(lambda: out.copy_(step(dec, model, tokens)))
+    dec.share(torch.arange(batch + 1, device=cuda), torch.full((batch,), 16, device=cuda))
+    assert dec.ws.numel() > n
+    others = [torch.full((n + K.WS_ALIGN,), 255, dtype=torch.uint8, device=cuda) for _ in range(8)]
+    assert all(x.data_ptr() + x.numel() <= start or x.data_ptr() >= start + n for x in others)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dec.lens, lens + 1) and all((x == 255).all() for x in others)
+    fresh = decoder(cuda, K, batch, 64, 16)
+    for _ in range(21):
+        want = step(fresh, model, tokens)
+    assert torch.equal(out, want)
