@@ -193,6 +193,32 @@ def test_long_tail_behind_one_score_is_kept(cuda, K):
         assert (c.o[:6, :, 1] > 0.003).all()
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(dtype="f16"), dict(cache="e4m3"), dict(d=64), dict(slopes=True), dict(softcap=90.0),
+                                dict(softcap=500.0, cache="e4m3", dtype="f16")],
+                         ids=["bf16", "f16", "e4m3", "heads of 64", "bias", "cap", "far cap"])
+@pytest.mark.parametrize("shape", ["rise", "fall", "peaks"])
+@pytest.mark.parametrize("new", [[70, 40], [3, 20]], ids=["many", "few"])
+def test_scores_that_move_by_a_hundred_binary_orders(cuda, K, kw, shape, new):
+    """The largest score so far is passed in every step, in none but the first, or by some keys far above the others."""
+    c = Case(K, cuda, [900, 300], new, **kw)
+    c.qs[..., 0] = 8.0 * (c.d / 128) ** 0.5
+    for b, n in enumerate(c.lens):
+        t = torch.arange(n)[:, None]
+        ramp = {"rise": t / n, "fall": 1 - t / n, "peaks": (t % 200 == 150).float()}[shape]
+        c.rows[0][b][:, :, 0] = (100.0 * ramp).to(c.rows[0][b].dtype)
+        C.put_rows(c.pools[0], c.order, c.tables, c.P, b, 0, c.rows[0][b])
+    c.run().check()
+
+
+@pytest.mark.parametrize("softcap", [0.0, 0.7, 30.0])
+@pytest.mark.parametrize("new", [[70, 40], [3, 20]], ids=["many", "few"])
+def test_scales_that_are_not_positive(cuda, K, softcap, new):
+    c = Case(K, cuda, [900, 300], new, cache="e4m3", softcap=softcap, slopes=softcap == 30.0)
+    c.scales[0][0] *= -1
+    c.scales[0][1] = 0.0
+    c.run().check()
+
+
 def test_no_lse_and_repeated_calls_agree(cuda, K):
     c = Case(K, cuda, [0, 100, 3000], [200, 1, 40], cache="e4m3").run()
     torch.cuda.synchronize()
