@@ -210,6 +210,18 @@ def test_scores_that_move_by_a_hundred_binary_orders(cuda, K, kw, shape, new):
     c.run().check()
 
 
+@pytest.mark.parametrize("cache", ["bf16", "f16", "e4m3"])
+def test_rows_begin_where_those_beside_them_rise(cuda, K, cache):
+    """Windows that end at a step's edge for some tokens and before it for their neighbours: the step is the first for some rows of a
+    warp, and 13 binary orders above the last one for the others.  Requests enough that a CTA has steps in a row."""
+    c = Case(K, cuda, [900] * 12, [70] * 12, h_kv=8, dtype="bf16" if cache == "e4m3" else cache, cache=cache, window=163)
+    c.qs[..., 0] = 8.0
+    for b, n in enumerate(c.lens):
+        c.rows[0][b][:, :, 0] = (100.0 * torch.arange(n)[:, None] / n).to(c.rows[0][b].dtype)
+        C.put_rows(c.pools[0], c.order, c.tables, c.P, b, 738, c.rows[0][b][738:])
+    c.run().check()
+
+
 @pytest.mark.parametrize("softcap", [0.0, 0.7, 30.0])
 @pytest.mark.parametrize("new", [[70, 40], [3, 20]], ids=["many", "few"])
 def test_scales_that_are_not_positive(cuda, K, softcap, new):
