@@ -382,9 +382,10 @@ class PagedDecoder:
         behind the rows of every request.  Token i of request b is row ``indptr[b] + i`` of ``chunk_layer``'s tensors."""
         if not self.max_tokens:
             raise ValueError("chunks need max_tokens")
-        if n_new.shape != (self.batch,) or n_new.dtype != torch.int64 or n_new.device != self.lens.device:
+        if (n_new.shape != (self.batch,) or n_new.dtype != torch.int64 or n_new.device != self.lens.device
+                or not n_new.is_contiguous()):
             raise ValueError(f"n_new is {tuple(n_new.shape)} {n_new.dtype} on {n_new.device}, not ({self.batch},) int64 on "
-                             f"{self.lens.device}")
+                             f"{self.lens.device}, contiguous")
         self._assign(n_new, self.chunk_slots, self.chunk_positions, stream)
 
     def chunk_layer(self, layer: int, q, k, v, stream=None):
@@ -409,8 +410,9 @@ class PagedDecoder:
             return
         n = shared_lens.numel()
         for what, t, size in (("group_indptr", group_indptr, n + 1), ("shared_lens", shared_lens, n)):
-            if t.shape != (size,) or t.dtype != torch.int64 or t.device != self.lens.device:
-                raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}, not ({size},) int64 on {self.lens.device}")
+            if t.shape != (size,) or t.dtype != torch.int64 or t.device != self.lens.device or not t.is_contiguous():
+                raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}, not ({size},) int64 on {self.lens.device}, "
+                                 "contiguous")
         need = K.kvsel_prefix_attend_workspace_size(self.cache, self.attend, n)
         if need > self.ws.numel():
             self._outgrown.append(self.ws)         # (captured steps, and calls still running, use it)
@@ -467,12 +469,14 @@ class BeamSelector:
     def select(self, logits, scores, ended=None, stream=None):
         """logits [sets * beams, vocab] with the rows' stride, scores [sets, beams] fp32, ended [sets, beams] uint8 or None;
         returns (scores, parents, tokens) [sets, n_out], which the next call overwrites (its ``scores`` are a copy of them)."""
-        if logits.shape != (self.rows, self.vocab) or logits.dtype != self.dtype or logits.stride() != (self.row_stride, 1):
-            raise ValueError(f"logits are {tuple(logits.shape)} {logits.dtype} of strides {logits.stride()}, not "
-                             f"({self.rows}, {self.vocab}) {self.dtype} of ({self.row_stride}, 1)")
+        device = self.scores.device
+        if (logits.shape != (self.rows, self.vocab) or logits.dtype != self.dtype or logits.stride() != (self.row_stride, 1)
+                or logits.device != device):
+            raise ValueError(f"logits are {tuple(logits.shape)} {logits.dtype} of strides {logits.stride()} on {logits.device}, not "
+                             f"({self.rows}, {self.vocab}) {self.dtype} of ({self.row_stride}, 1) on {device}")
         for what, t, dtype in (("scores", scores, torch.float32), ("ended", ended, torch.uint8)):
-            if t is not None and (t.shape != self.shape or t.dtype != dtype or not t.is_contiguous()):
-                raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype}, not {self.shape} {dtype}, contiguous")
+            if t is not None and (t.shape != self.shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+                raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}, not {self.shape} {dtype} on {device}, contiguous")
         K.kvsel_beam_select(self.desc, logits, scores, ended, self.scores, self.parents, self.tokens, None, self.ws,
                             stream=stream)
         return self.scores, self.parents, self.tokens

@@ -210,6 +210,24 @@ def test_refusals(cuda):
         BeamSelector(sets=2, beams=2, n_out=65, vocab=50, device=cuda)
 
 
+def test_refusals_of_other_layouts_and_devices(cuda):
+    """Views that are not dense, whose neighbours the kernels would read, and tensors on the host."""
+    from attention_kv_cache_gb300 import kvsel as K
+    from attention_kv_cache_gb300.pipeline import BeamSelector
+    dec = decoder(cuda, K, 4, 100, 40, max_tokens=40, beams=2)
+    long = torch.zeros(8, dtype=torch.int64, device=cuda)
+    pick = BeamSelector(sets=2, beams=2, n_out=4, vocab=50, device=cuda)
+    logits, scores = torch.zeros(4, 50, dtype=torch.bfloat16, device=cuda), torch.zeros(2, 2, device=cuda)
+    ended = torch.zeros(2, 2, dtype=torch.uint8, device=cuda)
+    for f in (lambda: dec.begin_chunk(long[::2]), lambda: dec.share(long[:6:2], long[:2]), lambda: dec.share(long[:3], long[:4:2]),
+              lambda: pick.select(logits.cpu(), scores), lambda: pick.select(logits, scores.cpu()),
+              lambda: pick.select(logits, scores, ended.cpu()), lambda: pick.select(logits, scores.t(), ended[:, :1].expand(2, 2))):
+        with pytest.raises(ValueError):
+            f()
+    pick.select(logits, scores, ended)
+    torch.cuda.synchronize()
+
+
 def graph_of(run):
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
