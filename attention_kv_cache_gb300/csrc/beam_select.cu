@@ -133,27 +133,31 @@ struct Tokens {
     return (r == r ? r : -INFINITY) + 0.f;
   }
   // Sum of exp(x - top), a NaN as none.  With c the rounded product top log2 e and r what that leaves, exp(x - top) is
-  // 2^(x log2 e - c) 2^-r: one fused multiply-add per logit, rounded at its distance.
+  // 2^(x log2 e - c) 2^-r: one fused multiply-add per logit, rounded at its distance.  r is up to half a unit of c's last place, so
+  // that holds while the largest is moderate; beyond 2^20 (masks of large finite values are) the difference is taken first.
   __device__ __forceinline__ float exp_sum(float top) const {
     const float c = top * kLog2e, r = fmaf(top, kLog2e, -c);
     const float2 c2 = make_float2(-c, -c), l2 = make_float2(kLog2e, kLog2e);
-    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float sum = NAN;
+    if (fabsf(top) < 0x1p20f) {
+      float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < kEach / 2; ++i) {
-      const float2 z = __ffma2_rn(pair(i), l2, c2);
-      part[i & 1] = __fadd2_rn(part[i & 1], make_float2(ex2f(z.x), ex2f(z.y)));
+      for (int i = 0; i < kEach / 2; ++i) {
+        const float2 z = __ffma2_rn(pair(i), l2, c2);
+        part[i & 1] = __fadd2_rn(part[i & 1], make_float2(ex2f(z.x), ex2f(z.y)));
+      }
+      const float2 s = __fadd2_rn(part[0], part[1]);
+      sum = (s.x + s.y) * ex2f(-r);
     }
-    const float2 s = __fadd2_rn(part[0], part[1]);
-    float sum = s.x + s.y;
-    if (sum != sum) {                         // (a NaN among them: once more without it)
+    if (sum != sum) {                         // (or a NaN among them: once more without it)
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < kEach / 2; ++i) {
-        const float2 y = pair(i), z = __ffma2_rn(y, l2, c2);
-        sum += (y.x == y.x ? ex2f(z.x) : 0.f) + (y.y == y.y ? ex2f(z.y) : 0.f);
+        const float2 y = pair(i);
+        sum += (y.x == y.x ? ex2f((y.x - top) * kLog2e) : 0.f) + (y.y == y.y ? ex2f((y.y - top) * kLog2e) : 0.f);
       }
     }
-    return sum * ex2f(-r);
+    return sum;
   }
   // The tokens above `least` (one of the logits, or -inf), or equal to it and not -inf where `equal` ones count: bit i for
   // token i, or in pairs bit i for token 2 i and bit 16 + i for token 2 i + 1.
