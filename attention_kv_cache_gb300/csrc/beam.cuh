@@ -9,6 +9,7 @@ constexpr int kSliceKeys = 8192;      // tokens of one row that a CTA takes at a
 constexpr int64_t kSelectCtas = 2048; // segments of all rows, about
 constexpr int kMaxBeams = 64, kMaxBeamOut = 64;
 constexpr int64_t kMaxLists = 8192;   // slices of a set's rows, and segments at most
+constexpr int64_t kMaxSegSlices = 1024;   // of a segment: 2^23 terms of 2^40 at most, whose sum has 64 bits
 
 // ---- beam_select.cu ----------------------------------------------------------------------
 struct SelectArgs {
