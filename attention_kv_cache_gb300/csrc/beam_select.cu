@@ -365,31 +365,45 @@ __device__ __forceinline__ double log64(double x) {
   return y + fma(x, exp64(-y), -1.0);
 }
 
+// Whether candidate a comes before b: as numbers of 128 bits, a > b.
+__device__ __forceinline__ int precedes(ulonglong2 a, ulonglong2 b) {
+  uint32_t r;
+  asm("{\n\t.reg .b64 t;\n\tsub.cc.u64 t, %1, %2;\n\tsubc.cc.u64 t, %3, %4;\n\tsubc.u32 %0, 0, 0;\n\t}" : "=r"(r) : "l"(b.x), "l"(a.x), "l"(b.y), "l"(a.y));
+  return -(int)r;
+}
+
 // A beam's row for the merge: its log-sum, its score, and whether its order is that of the logits.
 struct Beam {
   double lse, score;
   int kind;             // 0: by logit; 1: ended, the pad token and then every other one at -inf; 2: every token at -inf
 };
 
-// Entry i of list (beam k, segment): its token, or -1, and its score.
-__device__ __forceinline__ int entry(const SelectArgs& a, const Beam& b, int64_t row, int segment, int i, double& score) {
+// Entry i of list (beam k, segment): its token, or -1, its score, and its place among equal scores (the larger comes first): the
+// smaller beam, the larger logit (where the score is not -inf), the smaller token.
+constexpr int kTokenBits = 26;
+static_assert(kMaxLists * kSliceKeys <= int64_t(1) << kTokenBits && kMaxBeams <= 1 << (32 - kTokenBits), "beam, logit and token fill 64 bits");
+__device__ __forceinline__ int entry(const SelectArgs& a, const Beam& b, int64_t row, int k, int segment, int i, double& score, uint64_t& place) {
   score = -INFINITY;
+  uint32_t logit = 0;
+  int token = -1;
   if (b.kind == 0) {
     const float2 e = a.best[(row * a.segments + segment) * a.n_out + i];
-    const int token = __float_as_int(e.y);
+    token = __float_as_int(e.y);
     if (token >= 0) {
       const double z = b.score + ((double)e.x - b.lse);
       score = z == z ? z : -INFINITY;
+      if (score != -INFINITY) logit = ordered(e.x);
     }
-    return token;
+  } else if (segment == 0) {
+    token = i;
+    if (b.kind == 1) {
+      if (i == 0) score = b.score;
+      token = i == 0 ? a.pad_token : i - 1 < a.pad_token ? i - 1 : i;
+    }
+    if (token >= a.vocab) token = -1;
   }
-  if (segment != 0) return -1;
-  int token = i;
-  if (b.kind == 1) {
-    if (i == 0) score = b.score;
-    token = i == 0 ? a.pad_token : i - 1 < a.pad_token ? i - 1 : i;
-  }
-  return token < a.vocab ? token : -1;
+  place = (uint64_t)(kMaxBeams - 1 - k) << (32 + kTokenBits) | (uint64_t)logit << kTokenBits | (uint32_t)((1 << kTokenBits) - 1 - token);
+  return token;
 }
 
 __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constant__ SelectArgs a) {
@@ -400,9 +414,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   __shared__ int16_t chosen[kMaxBeamOut];
   constexpr int kMost = kMaxBeamOut * kMaxBeamOut;
   const int lists = a.beams * a.segments, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint64_t* key = sm;                                          // [kMost] candidates' scores
-  int2* what = reinterpret_cast<int2*>(key + kMost);           // [kMost] (list and entry as one number, token)
-  uint64_t* head = reinterpret_cast<uint64_t*>(what + kMost);  // [lists]
+  ulonglong2* cand = reinterpret_cast<ulonglong2*>(sm);        // [kMost] candidates: place among equal scores, score
+  uint64_t* head = sm + 2 * kMost;                             // [lists]
   const int64_t set = blockIdx.x, row0 = set * a.beams;
   wait_for_earlier_kernels();
   // The rows' log-sums.  A 64-bit operation takes a warp 16 cycles of the SM whatever its lanes do (two lanes a clock), so lanes
@@ -436,13 +449,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
   if (tid == 0) n_cand = n_lists = 0;
   __syncthreads();
   // The n-th largest of the lists' first entries (of as many as make 2 n, where there are few lists), by its upper half, which is
-  // enough unless more lists than there is room for reach it; then by all of it, and of the lists equal to it those
-  // before the place `upto`.
+  // enough unless more lists than there is room for reach it; then by all of it, and of the lists equal to it those whose first
+  // entries' places are `from` or larger.
   const int n = a.n_out, depth = lists > n ? 1 : min(n, (2 * n + lists - 1) / lists), values = lists * depth;
   for (int v = tid; v < values; v += kMergeThreads) {
     const int l = v / depth, k = l / a.segments;
     double z;
-    head[v] = entry(a, beam[k], row0 + k, l - k * a.segments, v - l * depth, z) >= 0 ? ordered(z) : 0ull;   // (a real key is not 0)
+    uint64_t w;
+    head[v] = entry(a, beam[k], row0 + k, k, l - k * a.segments, v - l * depth, z, w) >= 0 ? ordered(z) : 0ull;   // (a real key is not 0)
   }
   __syncthreads();
   auto count = [&](auto test) {
@@ -458,8 +472,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
     __syncthreads();
     return c;
   };
-  uint64_t found = 0;
-  int upto = lists;
+  auto place_of = [&](int l) {                                 // of a list's first entry
+    const int k = l / a.segments;
+    double z;
+    uint64_t w;
+    (void)entry(a, beam[k], row0 + k, k, l - k * a.segments, 0, z, w);
+    return w;
+  };
+  uint64_t found = 0, from = 0;
   if (values <= kMergeThreads) {
     // few values: the one that n - 1 others precede
     if (tid == 0) total = 0;
@@ -486,16 +506,16 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
         if (count([&](uint64_t h, int) { return h >= probe; }) >= n) found = probe;
       }
       if (count([&](uint64_t h, int) { return h != 0 && h >= found; }) > n) {
-        int lo = 0;                                            // fewer than n before lo
-        for (int bit = 1 << 12; bit > 0; bit >>= 1)
-          if (count([&](uint64_t h, int l) { return h > found || (h == found && h != 0 && l < lo + bit); }) < n) lo += bit;
-        upto = lo + 1;
+        for (int bit = 63; bit >= 0; --bit) {
+          const uint64_t probe = from | (uint64_t(1) << bit);
+          if (count([&](uint64_t h, int l) { return h > found || (h == found && h != 0 && place_of(l) >= probe); }) >= n) from = probe;
+        }
       }
     }
   }
   for (int l = tid; l < lists; l += kMergeThreads) {
     const uint64_t h = head[l * depth];
-    if (h > found || (h == found && h != 0 && l < upto)) chosen[atomicAdd(&n_lists, 1)] = (int16_t)l;
+    if (h > found || (h == found && h != 0 && (from == 0 || place_of(l) >= from))) chosen[atomicAdd(&n_lists, 1)] = (int16_t)l;
   }
   __syncthreads();
   // what those lists hold at or above it, a warp each
@@ -503,26 +523,24 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge(const __grid_constan
     const int l = chosen[i], k = l / a.segments;
     for (int e = lane; e < n; e += 32) {
       double z;
-      const int token = entry(a, beam[k], row0 + k, l - k * a.segments, e, z);
-      if (token < 0 || ordered(z) < found) break;
+      uint64_t w;
+      if (entry(a, beam[k], row0 + k, k, l - k * a.segments, e, z, w) < 0 || ordered(z) < found) break;
       const int c = atomicAdd(&n_cand, 1);
-      key[c] = ordered(z);
-      what[c] = make_int2(l * kMaxBeamOut + e, token);
+      cand[c] = make_ulonglong2(w, ordered(z));
     }
   }
   __syncthreads();
   const int c_all = n_cand;
-  // equal scores: the earlier list (beam, then segment), then the earlier entry
   for (int c = tid; c < c_all; c += kMergeThreads) {
-    const uint64_t z = key[c];
-    const int2 w = what[c];
+    const ulonglong2 mine = cand[c];
     int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < c_all; ++j) rank += (key[j] > z) | ((key[j] == z) & (what[j].x < w.x));
+    for (int j = 0; j < c_all; ++j) rank += precedes(cand[j], mine);
     if (rank >= n) continue;
+    const uint64_t z = mine.y, w = mine.x;
     a.scores_out[set * n + rank] = (float)__longlong_as_double((long long)(z >> 63 ? z & ~(uint64_t(1) << 63) : ~z));
-    a.parents[set * n + rank] = w.x / kMaxBeamOut / a.segments;
-    a.tokens[set * n + rank] = w.y;
+    a.parents[set * n + rank] = kMaxBeams - 1 - (int)(w >> (32 + kTokenBits));
+    a.tokens[set * n + rank] = (1 << kTokenBits) - 1 - (int)(w & ((1u << kTokenBits) - 1));
   }
 }
 

@@ -136,10 +136,10 @@ def beam_select(logits, scores, n_out, ended=None, pad_token=0):
                 z = float(scores[k]) if v == pad_token else -math.inf
             else:
                 z = float(scores[k]) + (x[v] - lse) if math.isfinite(lse) else -math.inf
-            found.append((z, k, v))
-    found.sort(key=lambda f: (-f[0], f[1], f[2]))
+            found.append((z, k, -x[v] if z > -math.inf else 0.0, v))
+    found.sort(key=lambda f: (-f[0], *f[1:]))                # equal scores: the smaller beam, the larger logit, the smaller token
     best = found[:n_out]
-    return (np.array([f[0] for f in best]), np.array([f[1] for f in best]), np.array([f[2] for f in best]), np.array(lses))
+    return (np.array([f[0] for f in best]), np.array([f[1] for f in best]), np.array([f[3] for f in best]), np.array(lses))
 
 
 def beam_reorder(P, parents, lens, tables, queue, head):
