@@ -1009,6 +1009,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
         RowsScore score;
         score.capped = SCORED && a.softcap != 0.f;
         score.sc = ksc * kLog2e;
+        // (a factor that ended at 0 would make no number of the rows not seen, at -inf; 2^-126 leaves nothing of the others either)
+        if (KIND == kE4m3 && head_scale > 0.f) score.sc = fmaxf(score.sc, 0x1p-126f);
         score.icap = score.capped ? ksc / a.softcap : 0.f;
         score.cap2 = a.softcap * kLog2e;
         score.slope = SCORED && a.slopes != nullptr && live ? a.slopes[h] * kLog2e : 0.f;
