@@ -43,6 +43,9 @@ __device__ __forceinline__ int find_job(const int32_t* first, int n, int x) {
   return lo;
 }
 
+// (hi - k0 + 127 may pass 2^31)
+__device__ __forceinline__ int steps_of(const RowsItem& it) { return (int)(((uint32_t)(it.hi - it.k0) + kTileKeys - 1) / kTileKeys); }
+
 // The items, `make(i)` for each, with the steps of the items before it; then all steps, and where the CTAs' shares begin.
 template <typename Make>
 __device__ __forceinline__ void put_items(const RowsArgs& a, int n_items, int64_t* warp_sum, int32_t* step_sm, Make make) {
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan(const __grid_constant
     it.full_hi = p0 + 1;
     it.full_lo = a.window > 0 ? max(0, p1 + 1 - a.window) : 0;
     it.k0 = it.lo / kTileKeys * kTileKeys;
-    it.steps = (it.hi - it.k0 + kTileKeys - 1) / kTileKeys;
+    it.steps = steps_of(it);
     return it;
   });
 }
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan(const __grid_constan
       it.full_lo = (int)max((int64_t)0, most - a.window);
     }
     it.k0 = it.lo / kTileKeys * kTileKeys;
-    it.steps = it.lo < it.hi ? (it.hi - it.k0 + kTileKeys - 1) / kTileKeys : 0;
+    it.steps = it.lo < it.hi ? steps_of(it) : 0;
     return it;
   });
 }

@@ -147,9 +147,9 @@ struct RowsWalk {
   }
 };
 
-// Whether a step's keys that are loaded include one that some row of the item does not see.
+// Whether a step's keys that are loaded include one that some row of the item does not see.  (t0 + kTileKeys may be 2^31.)
 __device__ __forceinline__ bool rows_partial(int lo, int hi, int full_lo, int full_hi, int t0) {
-  return max(t0, lo) < full_lo || min(t0 + kTileKeys, hi) > full_hi;
+  return max(t0, lo) < full_lo || min(kTileKeys, hi - t0) > full_hi - t0;
 }
 // Adds to this thread's O (TMEM at `o`) the values of V rows that are not finite and that the thread's row sees.
 template <int D, int KIND>
@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
       if (!have) return r;
       const RowsItem& it = *p.item;
       const int t0 = it.k0 + kTileKeys * s, t = t0 + 32 * w + lane, tb = R != 0 ? t & ~(R - 1) : t;
-      r.flags = kMore | (t >= it.lo && t < it.hi ? kNeed : 0u) | (tb < it.hi && tb + max(R, 1) > it.lo ? kBox : 0u) |
-                (t0 < it.lo || t0 + kTileKeys > it.hi || rows_partial(it.lo, it.hi, it.full_lo, it.full_hi, t0) ? kPartial : 0u);
+      r.flags = kMore | (t >= it.lo && t < it.hi ? kNeed : 0u) | (tb < it.hi && tb > it.lo - max(R, 1) ? kBox : 0u) |
+                (t0 < it.lo || it.hi - t0 < kTileKeys || rows_partial(it.lo, it.hi, it.full_lo, it.full_hi, t0) ? kPartial : 0u);
       r.g = p.g;
       r.table = it.table;
       if (r.flags & kBox) {
@@ -1024,7 +1024,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_attend(const __grid_cons
         for (int s = cur.s0; s < cur.s1; ++s, ++step) {
           if (!two && (int)(step & 1) != x) continue;
           const int t0 = k0 + kTileKeys * s;
-          const bool within = t0 >= full_lo && t0 + kTileKeys <= full_hi, partial = rows_partial(k_lo, k_hi, full_lo, full_hi, t0);
+          const bool within = t0 >= full_lo && full_hi - t0 >= kTileKeys, partial = rows_partial(k_lo, k_hi, full_lo, full_hi, t0);
           ok = __all_sync(0xffffffffu, rows_wait(s_full(x), n & 1, flag));
           if (!ok) break;
           ++n;
