@@ -282,6 +282,7 @@ class PagedDecoder:
                                                  n_layers=n_layers, layer_stride=self.k_cache.stride(0))
             # (what ``fork`` shares stands in one place, so that a captured step reads the next prompt's)
             self.fork_indptr, self.fork_rows = torch.arange(0, batch + 1, beams, **i64), torch.zeros(batch // beams, **i64)
+            self._head, self._stays = torch.empty(1, **i64), torch.arange(beams, **i64).expand(batch // beams, beams)
             n = max(n, K.kvsel_beam_reorder_workspace_size(self.beam),
                     K.kvsel_prefix_attend_workspace_size(self.cache, self.attend, batch // beams))
         self.ws, self._outgrown = self._workspace(n), []
@@ -421,7 +422,8 @@ class PagedDecoder:
 
     def reorder(self, parents, stream=None):
         """Beam j of every set goes on from beam ``parents[set, j]`` (int32, on the device): lengths and pages follow, pages
-        that no beam names any more return to the queue, and a part-full last page is copied for a second child."""
+        that no beam names any more return to the queue, and a part-full last page is copied for a second child.  A reordering that
+        cannot be carried out (a parent or a length out of range, too few pages) is recorded and changes nothing."""
         if self.beams == 1:
             raise ValueError("a decoder of single beams")
         shape = (self.batch // self.beams, self.beams)
@@ -432,10 +434,13 @@ class PagedDecoder:
         if stream != current:
             stream.wait_stream(current)
         with torch.cuda.stream(stream):
+            self._head.fill_(-1)                   # (a refused call writes nothing)
             K.kvsel_beam_reorder(self.cache, self.beam, parents, self.lens, self.tables, self.free_pages, self.free_head,
-                                 self.tables, self.lens, self.free_head, self.k_cache, self.v_cache, self.ws, stream=stream)
+                                 self.tables, self.lens, self._head, self.k_cache, self.v_cache, self.ws, stream=stream)
+            done = self._head >= 0
+            torch.where(done, self._head, self.free_head, out=self.free_head)
             at = self.pos_offset.view(shape)
-            at.copy_(at.gather(1, parents.long().clamp(0, self.beams - 1)))    # (a parent out of range changes nothing else)
+            at.copy_(at.gather(1, torch.where(done, parents, self._stays)))
 
     def fork(self, stream=None):
         """Every set's beams share its first beam's pages (the others hold none, or lose them); the rows in whole pages at this
@@ -445,7 +450,7 @@ class PagedDecoder:
             stream.wait_stream(current)
         with torch.cuda.stream(stream):            # the temporaries are that stream's too
             self.reorder(torch.zeros((self.batch // self.beams, self.beams), dtype=torch.int32, device=self.device), stream)
-            self.fork_rows.copy_(self.lens[::self.beams] // self.P * self.P)
+            torch.where(self._head >= 0, self.lens[::self.beams] // self.P * self.P, self.fork_rows, out=self.fork_rows)
         self.share(self.fork_indptr, self.fork_rows)
 
 
