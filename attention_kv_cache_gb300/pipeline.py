@@ -292,6 +292,12 @@ class PagedDecoder:
         off = (-ws.data_ptr()) % K.WS_ALIGN
         return ws[off:off + n]
 
+    def device_error(self, stream=None) -> int:
+        """The first error that the device recorded in this decoder's calls since the last query, those of steps captured over a
+        workspace that it has outgrown among them, or OK; waits for ``stream``, not in a capture."""
+        found = [K.kvsel_read_device_error(ws, stream) for ws in (*self._outgrown, self.ws)]
+        return next((x for x in found if x != K.OK), K.OK)
+
     def _assign(self, n_new, slots, positions, stream):
         K.kvsel_page_assign(self.P, self.n_pages, self.lens, n_new, self.free_pages, self.free_head, self.tables,
                             self.lens, self.free_head, self.indptr, slots, positions, None, self.ws,
@@ -402,10 +408,11 @@ class PagedDecoder:
                              self.lens, self.indptr, self.slopes, ks, vs, self.chunk_o, None, self.ws, stream=stream)
         return self.chunk_o
 
-    def share(self, group_indptr, shared_lens):
+    def share(self, group_indptr, shared_lens, stream=None):
         """From now on requests ``group_indptr[j] .. group_indptr[j + 1] - 1`` name the same pages for their first
         ``shared_lens[j]`` rows, which a layer then reads once (int64, on the device; None: no more).  Not in a capture; a captured
-        step goes on reading the tensors that it was captured with."""
+        step goes on reading the tensors that it was captured with.  A larger workspace that this needs begins on ``stream``;
+        ``device_error`` reads those before it too."""
         if group_indptr is None:
             self.groups = None
             return
@@ -417,7 +424,8 @@ class PagedDecoder:
         need = K.kvsel_prefix_attend_workspace_size(self.cache, self.attend, n)
         if need > self.ws.numel():
             self._outgrown.append(self.ws)         # (captured steps, and calls still running, use it)
-            self.ws = self._workspace(need)
+            with torch.cuda.stream(_torch_stream(stream)):
+                self.ws = self._workspace(need)
         self.groups = (group_indptr, shared_lens)
 
     def reorder(self, parents, stream=None):
@@ -451,7 +459,7 @@ class PagedDecoder:
         with torch.cuda.stream(stream):            # the temporaries are that stream's too
             self.reorder(torch.zeros((self.batch // self.beams, self.beams), dtype=torch.int32, device=self.device), stream)
             torch.where(self._head >= 0, self.lens[::self.beams] // self.P * self.P, self.fork_rows, out=self.fork_rows)
-        self.share(self.fork_indptr, self.fork_rows)
+        self.share(self.fork_indptr, self.fork_rows, stream)
 
 
 class BeamSelector:

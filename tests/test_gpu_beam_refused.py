@@ -66,3 +66,21 @@ def test_a_refused_fork_is_not_shared(cuda):
     tokens = torch.tensor([7, 8, 9, 10], device=cuda)
     assert torch.equal(step(dec, model, tokens), step(same, model, tokens))
     assert K.kvsel_read_device_error(dec.ws) == K.OK and LAYERS == 2
+
+
+def test_errors_of_a_step_captured_before_sharing(cuda):
+    """Sharing needs more room than the captured step's workspace, in which its errors still arrive."""
+    from attention_kv_cache_gb300 import kvsel as K
+    model, tokens = Model(cuda), torch.tensor([1, 2, 3, 4], device=cuda)
+    dec = decoder(cuda, K, 4, 64, 16)
+    for _ in range(16):
+        step(dec, model, tokens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(dec, model, tokens)
+    small = dec.ws
+    dec.share(torch.arange(5, device=cuda), torch.full((4,), 16, device=cuda))
+    assert dec.ws is not small
+    dec.free_head.fill_(16)                                    # no page is left for the next step's rows
+    graph.replay()
+    assert dec.device_error() == K.ERR_INVALID_ARG and dec.device_error() == K.OK

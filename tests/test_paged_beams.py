@@ -97,3 +97,33 @@ def test_a_reordering_is_one_streams_work(monkeypatch):
     dec.reorder(torch.zeros(2, 2, dtype=torch.int32), stream=side)
     dec.fork(stream=side)
     assert r.log[0] == ("wait", "side", "main") and all(e[1] == "side" for e in r.log), r.log
+
+
+def test_errors_of_outgrown_workspaces_are_found(monkeypatch):
+    """A captured step goes on writing its errors where it did."""
+    Beams(monkeypatch)
+    errors = {}
+    monkeypatch.setattr(K, "kvsel_read_device_error", lambda ws, stream=None: errors.pop(ws.data_ptr(), K.OK))
+    dec = decoder(batch=4)
+    small = dec.ws
+    long = lambda *x: torch.tensor(x)              # noqa: E731
+    dec.share(long(0, 2, 3, 4), long(16, 0, 0))
+    if dec.ws is small:                            # (the workspace is larger than this one's need)
+        monkeypatch.setattr(K, "kvsel_prefix_attend_workspace_size", lambda cache, desc, groups: small.numel() + 256)
+        dec.share(long(0, 2, 4), long(16, 0))
+    assert dec.ws is not small and dec.device_error() == K.OK
+    errors[small.data_ptr()] = K.ERR_DEVICE
+    assert dec.device_error() == K.ERR_DEVICE and dec.device_error() == K.OK
+    errors.update({small.data_ptr(): K.ERR_INVALID_ARG, dec.ws.data_ptr(): K.ERR_DEVICE})
+    assert dec.device_error() == K.ERR_INVALID_ARG and dec.device_error() == K.OK
+
+
+def test_a_larger_workspace_begins_on_the_stream(monkeypatch):
+    r = Beams(monkeypatch)
+    monkeypatch.setattr(torch, "zeros", r.made("zeros", torch.zeros))
+    dec = decoder(batch=4)
+    monkeypatch.setattr(K, "kvsel_prefix_attend_workspace_size", lambda cache, desc, groups: dec.ws.numel() + 256)
+    side = Stream("side", r.log)
+    r.log.clear()
+    dec.share(torch.tensor([0, 4]), torch.tensor([16]), stream=side)
+    assert r.log == [("zeros", "side")]
