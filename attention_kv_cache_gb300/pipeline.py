@@ -298,6 +298,11 @@ class PagedDecoder:
         found = [K.kvsel_read_device_error(ws, stream) for ws in (*self._outgrown, self.ws)]
         return next((x for x in found if x != K.OK), K.OK)
 
+    def _unshare(self):
+        """A set's beams share no rows that one of them does not hold any more: its prompt is replaced by what comes in now."""
+        if self.beams > 1:
+            torch.minimum(self.fork_rows, self.lens.view(-1, self.beams).amin(1), out=self.fork_rows)
+
     def _assign(self, n_new, slots, positions, stream):
         K.kvsel_page_assign(self.P, self.n_pages, self.lens, n_new, self.free_pages, self.free_head, self.tables,
                             self.lens, self.free_head, self.indptr, slots, positions, None, self.ws,
@@ -342,6 +347,7 @@ class PagedDecoder:
                 raise ValueError(f"text_lens of {tuple(text.shape)}, not one per request of {self.batch}")
             if self.attend.window or self.slopes is not None:
                 self._whole(text, rows)
+            self._unshare()
             slots = torch.empty(n, dtype=torch.int64, device=self.device)
             self._assign(torch.full_like(self.lens, rows), slots, None, stream)
             self.pos_offset.copy_(text)                # (slots alone were assigned: positions begin with the next row)
@@ -393,6 +399,8 @@ class PagedDecoder:
                 or not n_new.is_contiguous()):
             raise ValueError(f"n_new is {tuple(n_new.shape)} {n_new.dtype} on {n_new.device}, not ({self.batch},) int64 on "
                              f"{self.lens.device}, contiguous")
+        with torch.cuda.stream(_torch_stream(stream)):
+            self._unshare()
         self._assign(n_new, self.chunk_slots, self.chunk_positions, stream)
 
     def chunk_layer(self, layer: int, q, k, v, stream=None):
@@ -409,10 +417,10 @@ class PagedDecoder:
         return self.chunk_o
 
     def share(self, group_indptr, shared_lens, stream=None):
-        """From now on requests ``group_indptr[j] .. group_indptr[j + 1] - 1`` name the same pages for their first
-        ``shared_lens[j]`` rows, which a layer then reads once (int64, on the device; None: no more).  Not in a capture; a captured
-        step goes on reading the tensors that it was captured with.  A larger workspace that this needs begins on ``stream``;
-        ``device_error`` reads those before it too."""
+        """Until the next call of ``share`` or ``fork`` (so before one of them is replaced) requests
+        ``group_indptr[j] .. group_indptr[j + 1] - 1`` name the same pages for their first ``shared_lens[j]`` rows, which a layer then
+        reads once (int64, on the device; None: no more).  Not in a capture; a captured step goes on reading the tensors that it
+        was captured with.  A larger workspace that this needs begins on ``stream``; ``device_error`` reads those before it too."""
         if group_indptr is None:
             self.groups = None
             return
@@ -452,7 +460,8 @@ class PagedDecoder:
 
     def fork(self, stream=None):
         """Every set's beams share its first beam's pages (the others hold none, or lose them); the rows in whole pages at this
-        time are what a layer then reads once for a set.  Not in a capture."""
+        time are what a layer then reads once for a set, until ``admit`` or ``begin_chunk`` finds that one of its beams holds
+        fewer rows (a prompt that replaces it).  Not in a capture."""
         current, stream = torch.cuda.current_stream(), _torch_stream(stream)
         if stream != current:
             stream.wait_stream(current)

@@ -14,6 +14,7 @@ class Beams(Recorder):
     def __init__(self, monkeypatch):
         super().__init__(monkeypatch)
         monkeypatch.setattr(K, "kvsel_prefix_attend_workspace_size", lambda cache, desc, groups: 256 * groups)
+        monkeypatch.setattr(K, "kvsel_chunk_attend_workspace_size", lambda cache, desc: 256)
         monkeypatch.setattr(K, "kvsel_beam_reorder", self.reorder)
         self.refused = 0
 
@@ -127,3 +128,30 @@ def test_a_larger_workspace_begins_on_the_stream(monkeypatch):
     r.log.clear()
     dec.share(torch.tensor([0, 4]), torch.tensor([16]), stream=side)
     assert r.log == [("zeros", "side")]
+
+
+@pytest.mark.parametrize("way", ["chunk", "admit"])
+def test_replaced_prompts_share_no_rows(monkeypatch, way):
+    """Rows that a set's beams hold no more are not shared when new ones come in; what other sets share stays."""
+    r = Beams(monkeypatch)
+    dec = beams(max_tokens=100)
+    dec.lens.copy_(torch.tensor([40, 0, 33, 0]))
+    dec.free_head.fill_(9)
+    dec.tables[:, :3] = torch.arange(12, dtype=torch.int32).view(4, 3)
+    dec.fork()
+    assert dec.fork_rows.tolist() == [32, 32]
+    side = Stream("side", r.log)
+
+    def come():
+        r.log.clear()
+        if way == "chunk":
+            dec.begin_chunk(torch.tensor([5, 6, 7, 8]), stream=side)
+        else:
+            dec.admit(*(torch.zeros(4, 2, 2, 3, 64, dtype=torch.bfloat16) for _ in range(2)), [50, 50, 50, 50], stream=side)
+        assert [e[2] for e in r.log if e[0] == "kvsel_page_assign"] == ["side"]
+
+    come()
+    assert dec.fork_rows.tolist() == [32, 32]
+    dec.lens[:2] = torch.tensor([50, 0])                       # one of the set's beams begins anew
+    come()
+    assert dec.fork_rows.tolist() == [0, 32]
