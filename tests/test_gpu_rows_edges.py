@@ -130,3 +130,11 @@ def test_all_rows_of_the_longest_request(cuda, K, call, new, P):
         want, ls, mass = every_row(pools, q[i], n, P, period, blocks, d ** -0.5, pos)
         assert (np.abs(C.f64(lse)[i] - ls) <= 2.0 ** -23 * steps + 2.0 ** -16).all()
         assert (np.abs(C.f64(o)[i] - want) <= 2.0 ** -8 * np.abs(want) + (9 * 2.0 ** -23 * steps + 2.0 ** -8 + 2.0 ** -16) * mass).all()
+
+
+def test_offsets_that_fall(cuda, K):
+    """The request whose offsets fall is reported and left out; the one behind it has the tokens that its own offsets say."""
+    c = Chunk(K, cuda, [40, 60, 80], [0, 7, 9])
+    c.indptr.copy_(torch.tensor([7, 7, 0, 9]))
+    c.new = [0, 0, 9]
+    c.run().check(error=K.ERR_INVALID_ARG)
