@@ -21,7 +21,7 @@ kvsel_status check_select(const kvsel_beam_select_desc* p, SelectArgs* out) {
   a.n_out = p->n_out;
   a.vocab = p->vocab;
   // Segments: slices of their own while there are few rows; of many rows so that the CTAs are some 2048 (each begins a bound and
-  // leaves a list: 64 sets of 16 beams over 128256 tokens take 245 us in slices of their own, 131 in four segments, 99 in two).
+  // leaves a list: 64 sets of 16 beams over 128256 tokens took 245 us in slices of their own, 131 in four segments, 99 in two).
   const int64_t rows = (int64_t)p->batch * p->beams, most = std::max<int64_t>(1, kSelectCtas / rows);
   a.seg_slices = (int32_t)std::min(kMaxSegSlices, ceil_div(slices, std::min(slices, most)));
   a.segments = (int32_t)ceil_div(slices, a.seg_slices);

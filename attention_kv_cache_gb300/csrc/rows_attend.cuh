@@ -14,25 +14,28 @@
 //
 // An item of more than 128 rows has them in both tiles, which share every step; P V of one and S of the other are issued in
 // alternation, as the prefill kernel does.  A smaller item has its rows in both: the tiles take steps in turn, so
-// that two chains S -> softmax -> P V -> S run at once (one alone takes 4000 cycles a step, which HBM brings in 2800).  Items of
-// up to 32 rows fill the tile's 128 rows with four copies, which take 32 keys of a step each: the softmax of a step is a
-// thread's loop over its keys, 2000 cycles for 128.  What tiles and copies hold is merged when the piece ends.
+// that two chains S -> softmax -> P V -> S run at once (one alone takes 4000 cycles a step and more; HBM brings one in 2800,
+// which is what the two in turn take).  Items of up to 32 rows fill the tile's 128 rows with four copies, which take 32 keys
+// of a step each: the softmax of a step is a thread's loop over its keys, 2000 cycles for 128.  What tiles and copies hold is
+// merged when the piece ends.
 //
 // Bound: with full items the chain of a tile's step, 2000 cycles of softmax and as many of S and P V with the waits between them;
-// TMEM holds S and O of two tiles and no third S that could be formed meanwhile.  4096 tokens behind 12288, 32 / 8 heads
-// of 128, bf16: 798 us, 1.2 PFLOP/s, a step of both tiles in 4000 cycles where its products take 2048.  (Halves of a step told
-// of apart, to start P V early: 912; steps of 64 keys: 1127.)  With few rows HBM and the start: 16 requests of 5 tokens behind up
-// to 8191: 102 us, 2.8 TB/s.
+// TMEM holds S and O of two tiles, at d = 128 with no room for a third S that could be formed meanwhile (at 64 a tile leaves 64 of
+// its 256 columns unused).  4096 tokens behind 12288, 32 / 8 heads
+// of 128, bf16: 791 us, 1.2 PFLOP/s, a step of both tiles in 4000 cycles where its products take 2048.  (Halves of a step told
+// of apart, to start P V early: 912; steps of 64 keys: 1127.)  With few rows HBM, and what a piece costs beside its
+// steps (queries, a first step alone, the merge of tiles and copies: 11 us): 16 requests of 5 tokens behind up to 8191: 101 us,
+// 2.8 TB/s; of CTAs with 29 steps each, those with one piece take 50 us, with two 63, the slowest, with four, 83.
 //
 // SCORED: kernels for capped or biased scores, which are formed in the registers that hold them for the softmax; a step with
 // a mask has them formed in TMEM first.  (8 chunks behind up to 7000 rows, 8-bit, capped, a window: 415 us when all were
-// formed in TMEM, 397 now.)
+// formed in TMEM, 396 now.)
 //
 // SPLIT (the shared prefix over 16-bit pools): weights are a high and a low 16-bit part, as in the decode kernel whose results it
 // must match; the steps wait for HBM there, so the third product is free up to 128 rows.  Without it (chunks, bound by the tensor
-// cores, and 8-bit pools) a weight is rounded once, by at most 2^-8 of it over bf16 and 2^-11 over fp16 products: what the
-// outputs' own rounding is, and far below a row's in 8 bits.  (64 requests behind 32768 e4m3 rows take 167 us; the low parts
-// would add 26.)
+// cores, and 8-bit pools) a weight is rounded once, by at most 2^-8 of it over bf16 and 2^-11 over fp16 products (or 2^-33 of the
+// row's largest: those below 2^-22 of it are subnormal): what the outputs' own rounding is, and far below a row's in 8 bits.
+// (64 requests behind 32768 e4m3 rows take 166 us; the low parts would add 26.)
 // Factors on the weights as in paged_attend.cuh: 2^-8 over bf16 and 2^13 over fp16 products; without SPLIT it is taken by the
 // exponent, whose rounding at 13 (2^-21 of a weight) is far below the weight's own.
 //
@@ -412,8 +415,8 @@ __device__ __forceinline__ float rows_step(uint32_t s, int copy, float mul, cons
       // No weight is above their sum: the largest score is looked for only where a row has no offset yet or the sum passes what
       // the products' type holds (both rare), and the weights are formed again.  Over fp16 products the offset is then put 5
       // binary orders above the largest, where 128 weights of that size stay within 2^15: what is lost of a weight is
-      // below 2^-32 of the row's largest.  (4096 tokens behind 12288, 32 / 8 heads of 128: bf16 867 -> 796 us, fp16 931 -> 807; over an
-      // e4m3 pool, whose softmax has fewer registers, 1072 -> 1112: not there.)
+      // below 2^-32 of the row's largest.  (4096 tokens behind 12288, 32 / 8 heads of 128: bf16 867 -> 791 us, fp16 931 -> 796; over an
+      // e4m3 pool, whose softmax has fewer registers, 1072 -> 1112 when it was tried: not there.)
       constexpr float kMost = KIND == kBf16 ? 1.f : 0x1p15f, kAbove = KIND == kBf16 ? 0.f : 5.f;
       bool look = __any_sync(0xffffffffu, m == -INFINITY);
 #pragma unroll 1

@@ -637,12 +637,14 @@ KVSEL_API kvsel_status kvsel_paged_attend(const kvsel_cache_desc* cache, const k
  *                 current device: query it where the call runs
  *
  * A length outside [0, max_blocks * P], offsets that fall or leave [0, max_tokens], or more new tokens than rows record
- * KVSEL_ERR_INVALID_ARG (detail: the request), whose tokens are then left as they were; a page id outside
+ * KVSEL_ERR_INVALID_ARG (detail: the request), whose tokens are then left as they were (where offsets fall, a later request
+ * may claim tokens of an earlier one: which of the two writes them is open); a page id outside
  * [0, n_pages) records KVSEL_ERR_DEVICE (detail: the request) and its rows are left out.
  *
  * Arithmetic: products of 16-bit values (e4m3 values as fp16, exactly) accumulated in fp32 on the tensor cores, softmax
- * statistics in fp32, each weight rounded once to the products' 16-bit type.  With an e4m3 pool the query row is held
- * in fp16 scaled by a power of two of its own (2^-24 of the row's largest value).
+ * statistics in fp32, each weight rounded once to the products' 16-bit type: by at most 2^-8 of it over bf16, 2^-11 of it or
+ * 2^-33 of the row's largest weight over fp16 products (a 16-bit value, where kvsel_paged_attend holds two).  With an e4m3
+ * pool the query row is held in fp16 scaled by a power of two of its own (2^-24 of the row's largest value).
  */
 typedef struct {
   int32_t batch;          /* requests: 1 .. KVSEL_PAGED_MAX_BATCH */
@@ -669,6 +671,7 @@ KVSEL_API kvsel_status kvsel_chunk_attend(const kvsel_cache_desc* cache, const k
  * of those rows the whole pages are read once for all of them, through the first one's table, and every
  * request's other rows through its own.  A group of one request, or of no shared rows, is an ordinary request.
  *
+ *   n_groups      1 .. batch
  *   group_indptr  [device] int64 [n_groups + 1], rising, from 0 to batch
  *   shared_lens   [device] int64 [n_groups]: at most the shortest length of the group
  *   others        as kvsel_paged_attend's; ws of kvsel_prefix_attend_workspace_size() bytes
@@ -679,7 +682,8 @@ KVSEL_API kvsel_status kvsel_chunk_attend(const kvsel_cache_desc* cache, const k
  * a shared page name the group's first request.
  *
  * Arithmetic: kvsel_paged_attend's, the shared rows' and the own rows' parts joined in fp32; but with an e4m3 pool a
- * shared row's weight is rounded once to fp16 (by at most 2^-11 of it) instead of held in two parts.
+ * shared row's weight is rounded once to fp16 (by at most 2^-11 of it, or 2^-38 of the row's largest) instead of held in two
+ * parts.
  */
 KVSEL_API kvsel_status kvsel_prefix_attend_workspace_size(const kvsel_cache_desc* cache,
                                                           const kvsel_paged_attend_desc* desc, int32_t n_groups,
@@ -710,8 +714,9 @@ KVSEL_API kvsel_status kvsel_prefix_attend(const kvsel_cache_desc* cache, const 
  *   lse         [device] fp32 [batch][beams] out: log sum exp of the row, or NULL
  *   ws          [device] workspace of kvsel_beam_select_workspace_size() bytes
  *
- * Scores are formed and compared in fp64, from log-sums whose exponentials are within 2^-22 each (of either sign, so that
- * the sum of many is nearer) and are added exactly; they are rounded once.
+ * Scores are formed and compared in fp64 and rounded once.  Of a log-sum, exponentials are within 2^-22 of their own (of
+ * either sign, so that the sum of many is nearer); each of 256 threads adds its own in fp32, 32 of every 8192 tokens, and
+ * the threads' sums are added exactly: it is within 2^-18 + 2^-21 ceil(vocab / 8192), and the same for equal rows of a call.
  */
 typedef struct {
   int32_t batch;          /* sets >= 1; batch * beams at most KVSEL_PAGED_MAX_BATCH */
